@@ -35,6 +35,15 @@ MEP_RANK_MAJOR = 0
 MEP_EXPERT_MAJOR = 1
 MEP_RANK_SUM = 2
 
+MEP_FP32 = 0
+MEP_BF16 = 1
+MEP_SCORE_SOFTMAX = 0
+MEP_SCORE_SIGMOID = 1
+MEP_ACT_NONE = 0
+MEP_ACT_GELU = 1
+MEP_ACT_SILU = 2
+MEP_ACT_SILU_GLU = 3
+
 
 class MepConfig(C.Structure):
     _fields_ = [
@@ -45,6 +54,28 @@ class MepConfig(C.Structure):
         ("max_num_inp_token_per_rank", C.c_int32),
         ("world_size", C.c_int32),
         ("rank", C.c_int32),
+        ("quant", C.c_int32),
+    ]
+
+
+class MepGateConfig(C.Structure):
+    _fields_ = [
+        ("num_experts", C.c_int32),
+        ("top_k", C.c_int32),
+        ("score", C.c_int32),
+        ("dtype", C.c_int32),
+        ("normalize", C.c_int32),
+        ("scale", C.c_float),
+        ("balance_coef", C.c_float),
+    ]
+
+
+class MepLinearConfig(C.Structure):
+    _fields_ = [
+        ("num_experts", C.c_int32),
+        ("in_dim", C.c_int32),
+        ("out_dim", C.c_int32),
+        ("act", C.c_int32),
         ("quant", C.c_int32),
     ]
 
@@ -67,6 +98,7 @@ def lib() -> C.CDLL:
         L = C.CDLL(LIB_PATH)
         p, i32, i64, sz = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
         cfgp = C.POINTER(MepConfig)
+        gatep, linp = C.POINTER(MepGateConfig), C.POINTER(MepLinearConfig)
         sig = {
             "mep_error_string": ([C.c_int], C.c_char_p),
             "mep_workspace_bytes": ([cfgp], sz),
@@ -87,6 +119,14 @@ def lib() -> C.CDLL:
             "mep_reset": ([p, p], C.c_int),
             "mep_get_status": ([p, p, C.POINTER(i32)], C.c_int),
             "mep_get_route": ([p, p, p, p], C.c_int),
+            "mep_gate": ([gatep, p, p, i32, p, p, p], C.c_int),
+            "mep_balance_workspace_bytes": ([gatep, i32], sz),
+            "mep_balance_loss": ([gatep, p, p, p, i32, p, p, p, p, sz, p], C.c_int),
+            "mep_gate_backward": ([gatep, p, p, p, i32, p, p, p, p, p], C.c_int),
+            "mep_expert_linear": ([linp, p, p, p, p, i64, i64, p, p, p, p, p, p, p], C.c_int),
+            "mep_linear_workspace_bytes": ([linp, i64], sz),
+            "mep_expert_linear_backward": ([linp, p, p, p, p, p, p, i64, i64, p, p, p, p, sz, p],
+                                           C.c_int),
             "mep_probe_e4m3": ([p, p, i64, p], C.c_int),
             "mep_probe_bf16": ([p, p, i64, p], C.c_int),
             "mep_probe_mxfp4": ([p, p, p, i64, p], C.c_int),
@@ -446,6 +486,148 @@ def mep_get_route(h, recv_row, em_row=None, stream=None) -> None:
             _need("mep_get_route", "em_row", em_row, n)
     s = _stream(stream, recv_row)
     _check("mep_get_route", lib().mep_get_route(h, _ptr(recv_row), _ptr(em_row), s))
+
+
+# ---------------------------------------------------------------------------
+# router and experts: no handle, the config says every size
+# ---------------------------------------------------------------------------
+
+def _check_tensors(fn, **tensors) -> None:
+    """Type and size of each (tensor, bytes the call touches, dtype), and one
+    device for all; tensors given as addresses are taken as they are."""
+    import torch
+    dev = None
+    for name, (t, nbytes, dtype) in tensors.items():
+        if t is None or isinstance(t, int):
+            continue
+        want = {"f32": (torch.float32,), "i32": (torch.int32,), "u8": (torch.uint8, torch.bool),
+                "bf16": (torch.bfloat16, torch.int16),
+                "e4m3": (torch.float8_e4m3fn, torch.uint8), "any": None}[dtype]
+        if want is not None and t.dtype not in want:
+            raise ValueError(f"{fn}: {name} must be {want[0]}, not {t.dtype}")
+        if t.nbytes < nbytes:
+            raise ValueError(f"{fn}: {name} holds {t.nbytes} bytes, the call touches {nbytes}")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{fn}: {name} is on {t.device}, not on {dev}")
+
+
+class _on_device:
+    """Makes the device of the first GPU tensor current for a call (a launch
+    goes to the current device)."""
+
+    def __init__(self, *tensors):
+        self.dev = next((d for d in (t.get_device() for t in tensors if hasattr(t, "get_device"))
+                         if d >= 0), None)
+
+    def __enter__(self):
+        self.guard = None
+        if self.dev is not None:
+            import torch
+            if torch.cuda.current_device() != self.dev:
+                self.guard = torch.cuda.device(self.dev)
+                self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _logits_kind(c):
+    return ("f32", 4) if c.dtype == MEP_FP32 else ("bf16", 2)
+
+
+def mep_gate(cfg, logits, bias, T, indices, weights, stream=None) -> None:
+    kind, size = _logits_kind(cfg)
+    E, k = cfg.num_experts, cfg.top_k
+    _check_tensors("mep_gate", logits=(logits, T * E * size, kind), bias=(bias, 4 * E, "f32"),
+                   indices=(indices, 4 * T * k, "i32"), weights=(weights, 4 * T * k, "f32"))
+    with _on_device(indices):
+        _check("mep_gate", lib().mep_gate(C.byref(cfg), _ptr(logits), _ptr(bias), T, _ptr(indices),
+                                          _ptr(weights), _stream(stream, indices)))
+
+
+def mep_balance_workspace_bytes(cfg, T) -> int:
+    return lib().mep_balance_workspace_bytes(C.byref(cfg), T)
+
+
+def mep_balance_loss(cfg, logits, indices, token_mask, T, counts, prob_mean, loss, workspace,
+                     stream=None) -> None:
+    """The workspace is a tensor of mep_balance_workspace_bytes(cfg, T) zeroed
+    bytes (its size is passed on)."""
+    kind, size = _logits_kind(cfg)
+    E, k = cfg.num_experts, cfg.top_k
+    _check_tensors("mep_balance_loss", logits=(logits, T * E * size, kind),
+                   indices=(indices, 4 * T * k, "i32"), token_mask=(token_mask, T, "u8"),
+                   counts=(counts, 4 * (E + 1), "i32"), prob_mean=(prob_mean, 4 * E, "f32"),
+                   loss=(loss, 4, "f32"), workspace=(workspace, 0, "any"))
+    with _on_device(counts):
+        _check("mep_balance_loss", lib().mep_balance_loss(
+            C.byref(cfg), _ptr(logits), _ptr(indices), _ptr(token_mask), T, _ptr(counts),
+            _ptr(prob_mean), _ptr(loss), _ptr(workspace),
+            workspace.nbytes if workspace is not None else 0, _stream(stream, counts)))
+
+
+def mep_gate_backward(cfg, logits, indices, token_mask, T, grad_weights, counts, grad_loss,
+                      grad_logits, stream=None) -> None:
+    kind, size = _logits_kind(cfg)
+    E, k = cfg.num_experts, cfg.top_k
+    _check_tensors("mep_gate_backward", logits=(logits, T * E * size, kind),
+                   indices=(indices, 4 * T * k, "i32"), token_mask=(token_mask, T, "u8"),
+                   grad_weights=(grad_weights, 4 * T * k, "f32"),
+                   counts=(counts, 4 * (E + 1), "i32"), grad_loss=(grad_loss, 4, "f32"),
+                   grad_logits=(grad_logits, T * E * size, kind))
+    with _on_device(grad_logits):
+        _check("mep_gate_backward", lib().mep_gate_backward(
+            C.byref(cfg), _ptr(logits), _ptr(indices), _ptr(token_mask), T, _ptr(grad_weights),
+            _ptr(counts), _ptr(grad_loss), _ptr(grad_logits), _stream(stream, grad_logits)))
+
+
+def _weight_rows(c) -> int:
+    return 2 * c.out_dim if c.act == MEP_ACT_SILU_GLU else c.out_dim
+
+
+def mep_expert_linear(cfg, em_x, em_scales, em_counts, em_offsets, cap_em, num_rows, w, w_scales,
+                      bias, residual, y, z, stream=None) -> None:
+    E, K, N, Nz = cfg.num_experts, cfg.in_dim, cfg.out_dim, _weight_rows(cfg)
+    fp8 = cfg.quant != MEP_QUANT_NONE
+    kind, size = ("e4m3", 1) if fp8 else ("bf16", 2)
+    _check_tensors("mep_expert_linear", em_x=(em_x, cap_em * K * size, kind),
+                   em_scales=(em_scales, 4 * cap_em * (K // 128) if fp8 else 0, "f32"),
+                   em_counts=(em_counts, 4 * E, "i32"), em_offsets=(em_offsets, 4 * E + 4, "i32"),
+                   w=(w, E * Nz * K * size, kind),
+                   w_scales=(w_scales, 4 * E * (Nz // 128) * (K // 128) if fp8 else 0, "f32"),
+                   bias=(bias, 4 * E * Nz, "f32"), residual=(residual, 2 * cap_em * N, "bf16"),
+                   y=(y, 2 * cap_em * N, "bf16"), z=(z, 2 * cap_em * Nz, "bf16"))
+    with _on_device(y):
+        _check("mep_expert_linear", lib().mep_expert_linear(
+            C.byref(cfg), _ptr(em_x), _ptr(em_scales), _ptr(em_counts), _ptr(em_offsets), cap_em,
+            num_rows, _ptr(w), _ptr(w_scales), _ptr(bias), _ptr(residual), _ptr(y), _ptr(z),
+            _stream(stream, y)))
+
+
+def mep_linear_workspace_bytes(cfg, cap_em) -> int:
+    return lib().mep_linear_workspace_bytes(C.byref(cfg), cap_em)
+
+
+def mep_expert_linear_backward(cfg, grad_y, z, em_x, w, em_counts, em_offsets, cap_em, num_rows,
+                               grad_x, grad_w, grad_bias, workspace, stream=None) -> None:
+    """The workspace is a tensor of mep_linear_workspace_bytes(cfg, cap_em)
+    bytes (its size is passed on)."""
+    E, K, N, Nz = cfg.num_experts, cfg.in_dim, cfg.out_dim, _weight_rows(cfg)
+    _check_tensors("mep_expert_linear_backward", grad_y=(grad_y, 2 * cap_em * N, "bf16"),
+                   z=(z, 2 * cap_em * Nz if cfg.act != MEP_ACT_NONE else 0, "bf16"),
+                   em_x=(em_x, 2 * cap_em * K, "bf16"), w=(w, 2 * E * Nz * K, "bf16"),
+                   em_counts=(em_counts, 4 * E, "i32"), em_offsets=(em_offsets, 4 * E + 4, "i32"),
+                   grad_x=(grad_x, 2 * cap_em * K, "bf16"), grad_w=(grad_w, 2 * E * Nz * K, "bf16"),
+                   grad_bias=(grad_bias, 4 * E * Nz, "f32"), workspace=(workspace, 0, "any"))
+    with _on_device(workspace):
+        _check("mep_expert_linear_backward", lib().mep_expert_linear_backward(
+            C.byref(cfg), _ptr(grad_y), _ptr(z), _ptr(em_x), _ptr(w), _ptr(em_counts),
+            _ptr(em_offsets), cap_em, num_rows, _ptr(grad_x), _ptr(grad_w), _ptr(grad_bias),
+            _ptr(workspace), workspace.nbytes if workspace is not None else 0,
+            _stream(stream, workspace)))
 
 
 def mep_probe_e4m3(inp, out, n, stream=None) -> None:

@@ -1,0 +1,682 @@
+// Router: top-k selection with its weights, the load-balance loss, and their
+// gradient with respect to the logits.
+//
+// A token's E logits sit in the registers of a group of LPT lanes (8 lanes up
+// to 64 experts, 16 up to 512, the whole wave beyond), EPL values a lane, so a
+// wave works on 64 / LPT tokens at once and reduces over 8 or 16 lanes with
+// DPP moves that cost one instruction a step.  Lane l of a group holds, for
+// c = 0.., the V consecutive experts (c*LPT + l)*V.. (V: one 16-byte load when
+// every row starts on a 16-byte boundary, else single loads of the same
+// experts).  Values past E stay out of every maximum and sum.
+#include <algorithm>
+#include <type_traits>
+
+#include "dev.h"
+#include "mep_internal.h"
+
+namespace mep {
+
+namespace {
+
+// ---- reductions over a group of LPT consecutive lanes, result in every lane --
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xf, 0xf, false);
+}
+
+// DPP controls: exchanges within 2 and 4 lanes (quad permutations), with the
+// mirrored lane of 8 (row_half_mirror) and of 16 (row_mirror).  After the quad
+// steps all 4 lanes agree, so a mirror is as good as an exchange.
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
+
+template <int LPT, class F>
+__device__ __forceinline__ uint32_t group_reduce(uint32_t v, F f) {
+  v = f(v, dpp<kXor1>(v));
+  v = f(v, dpp<kXor2>(v));
+  v = f(v, dpp<kHalfMirror>(v));
+  if (LPT >= 16) v = f(v, dpp<kMirror>(v));
+  if (LPT == 64) {
+    v = f(v, (uint32_t)__shfl_xor((int)v, 16));
+    v = f(v, (uint32_t)__shfl_xor((int)v, 32));
+  }
+  return v;
+}
+
+template <int LPT>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  return group_reduce<LPT>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+
+template <int LPT>
+__device__ __forceinline__ uint32_t group_min(uint32_t v) {
+  return group_reduce<LPT>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+}
+
+// Every lane adds the same pairs (a + b and b + a round alike), so all agree.
+template <int LPT>
+__device__ __forceinline__ float group_sum(float v) {
+  return __uint_as_float(group_reduce<LPT>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+
+template <int LPT>
+__device__ __forceinline__ float group_fmax(float v) {
+  return __uint_as_float(group_reduce<LPT>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+}
+
+// ---- values ---------------------------------------------------------------
+
+// Unsigned keys in the order of the values: -inf < ... < -0 = +0 < ... < +inf
+// are keys above 1, NaN is 1 (ranks last), 0 is below every value (absent).
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);  // -0 + 0 is +0
+  const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+  return v != v ? 1u : k;
+}
+
+__device__ __forceinline__ uint64_t order_key(double v) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v + 0.0);
+  const uint64_t k = u ^ ((uint64_t)((int64_t)u >> 63) | 0x8000000000000000ull);
+  return v != v ? 1ull : k;
+}
+
+__device__ __forceinline__ float key_value(uint32_t k) {
+  if (k == 1u) return __uint_as_float(0x7fc00000u);
+  return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+
+// The sigmoid and its slope s (1 - s), neither with a cancellation.
+__device__ __forceinline__ float sigmoid(float x, float& slope) {
+  const float e = expf(-fabsf(x)), r = 1.0f / (1.0f + e);
+  slope = e * r * r;
+  return x < 0.0f ? e * r : r;
+}
+
+__device__ __forceinline__ float load_logit(const float* p) { return *p; }
+__device__ __forceinline__ float load_logit(const uint16_t* p) {
+  return __uint_as_float((uint32_t)*p << 16);
+}
+
+template <class TL>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int V = 4;
+  static __device__ __forceinline__ void load(const float* p, float* v) {
+    const float4 q = *reinterpret_cast<const float4*>(p);
+    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+  }
+  static __device__ __forceinline__ void store(float* p, const float* v) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+  static __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+};
+template <>
+struct Vec<uint16_t> {
+  static constexpr int V = 8;
+  static __device__ __forceinline__ void load(const uint16_t* p, float* v) {
+    const u32x4 q = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo(q[i]);
+      v[2 * i + 1] = bf16_hi(q[i]);
+    }
+  }
+  static __device__ __forceinline__ void store(uint16_t* p, const float* v) {
+    u32x4 q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = pack_bf16_rne(v[2 * i], v[2 * i + 1]);
+    *reinterpret_cast<u32x4*>(p) = q;
+  }
+  static __device__ __forceinline__ void store1(uint16_t* p, float v) {
+    *p = (uint16_t)pack_bf16_rne(v, 0.0f);
+  }
+};
+
+// The expert of lane l's register i.
+template <class TL, int LPT>
+__device__ __forceinline__ int expert_of(int i, int l) {
+  constexpr int V = Vec<TL>::V;
+  return ((i / V) * LPT + l) * V + i % V;
+}
+
+// A token's logits (row p of E); registers past E get -inf.  `wide`: E is a
+// multiple of V, so rows are 16-byte aligned and a load never straddles E.
+template <class TL, int LPT, int EPL>
+__device__ __forceinline__ void load_row(const TL* p, int E, int l, bool wide, float (&x)[EPL]) {
+  constexpr int V = Vec<TL>::V;
+  if (wide) {
+#pragma unroll
+    for (int c = 0; c < EPL / V; ++c) {
+      const int e = (c * LPT + l) * V;
+      if (e < E) {
+        Vec<TL>::load(p + e, &x[c * V]);
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[c * V + v] = -__builtin_inff();
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = expert_of<TL, LPT>(i, l);
+      x[i] = e < E ? load_logit(p + e) : -__builtin_inff();
+    }
+  }
+}
+
+// ---- the router -----------------------------------------------------------
+
+constexpr int kGateThreads = 256;
+
+// How far apart two fp32 scores sigmoid(x) + b must be for their order to be
+// the order of the exact scores: the sigmoid is within 3 units of 2^-24 (its
+// value is at most 1) and the sum rounds once more, so each score is within
+// 2^-22 (1 + |score|) and two of them within twice that.
+__device__ __forceinline__ bool scores_apart(float hi, float lo) {
+  return hi - lo > 4.76837158203125e-07f * (1.0f + fabsf(hi));
+}
+
+// k rounds of "largest key, lowest expert among equals, take it out".  What
+// bounds the kernel for many experts is these rounds (about 5 EPL + 8
+// instructions each, for 64 / LPT tokens), not the one pass over the logits.
+//
+// The selection with a bias is on sigmoid(x) + b in fp32.  Where neighbours of
+// the first k + 1 are too close for fp32 to order them (about 1 token in 2000
+// at 256 experts) the token's selection is done again in fp64; equal logits
+// with equal biases are equal scores and need no second look.
+template <class TL, int LPT, int EPL, bool BIAS>
+__global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
+  constexpr int SLOTS = (kMaxTopk + LPT - 1) / LPT;  // results a lane may hold
+  const int l = threadIdx.x % LPT;
+  const int64_t t = ((int64_t)blockIdx.x * kGateThreads + threadIdx.x) / LPT;
+  const bool live = t < a.T;
+  const int E = a.E, k = a.k;
+  const TL* row = reinterpret_cast<const TL*>(a.logits) + (live ? t : a.T - 1) * (int64_t)E;
+
+  float x[EPL];
+  load_row<TL, LPT, EPL>(row, E, l, a.wide, x);
+  uint32_t key[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = expert_of<TL, LPT>(i, l);
+    float s = x[i];
+    if (BIAS) s = e < E ? sigmoid(s) + a.bias[e] : 0.0f;
+    key[i] = e < E ? order_key(s) : 0u;
+  }
+
+  uint32_t got_key[SLOTS];
+  int got[SLOTS];
+#pragma unroll
+  for (int s = 0; s < SLOTS; ++s) { got_key[s] = 1u; got[s] = 0; }
+  uint32_t first = 0;
+  uint32_t last = 0;
+  int last_e = 0;
+  bool unsure = false;
+#pragma unroll
+  for (int s = 0; s < SLOTS; ++s) {
+    for (int jj = 0; jj < LPT; ++jj) {
+      const int j = s * LPT + jj;
+      if (j >= k) break;
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) m = key[i] > m ? key[i] : m;
+      m = group_max<LPT>(m);
+      uint32_t e = 0xffffffffu;
+#pragma unroll
+      for (int i = EPL - 1; i >= 0; --i) {
+        if (key[i] == m) e = (uint32_t)expert_of<TL, LPT>(i, l);
+      }
+      e = group_min<LPT>(e);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if ((uint32_t)expert_of<TL, LPT>(i, l) == e) key[i] = 0u;
+      if (j == 0) first = m;
+      if (BIAS) {
+        if (j > 0 && !scores_apart(key_value(last), key_value(m))) {
+          // row and bias loads hit the cache; equal inputs need no second look
+          const bool same = load_logit(row + last_e) == load_logit(row + e) &&
+                            a.bias[last_e] == a.bias[e];
+          unsure |= !same;
+        }
+        last = m;
+        last_e = (int)e;
+      }
+      if (l == jj) {
+        got_key[s] = m;
+        got[s] = (int)e;
+      }
+    }
+  }
+
+  if (BIAS) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) m = key[i] > m ? key[i] : m;
+    m = group_max<LPT>(m);  // the best score left out; 0 when k == E
+    if (m != 0u && !scores_apart(key_value(last), key_value(m))) unsure = true;
+    if (unsure) {  // the same for all lanes of the group
+      uint64_t out = 0;  // this lane's registers already taken
+#pragma unroll
+      for (int s = 0; s < SLOTS; ++s) {
+        for (int jj = 0; jj < LPT; ++jj) {
+          const int j = s * LPT + jj;
+          if (j >= k) break;
+          uint64_t best = 0;
+          int be = 0;
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) {
+            const int e = expert_of<TL, LPT>(i, l);
+            if (e < E && !((out >> i) & 1)) {
+              const uint64_t q =
+                  order_key(1.0 / (1.0 + exp(-(double)x[i])) + (double)a.bias[e]);
+              if (q > best) {  // registers hold ascending experts: the lowest wins
+                best = q;
+                be = e;
+              }
+            }
+          }
+          for (int d = 1; d < LPT; d <<= 1) {
+            const uint64_t oq = __shfl_xor((unsigned long long)best, d);
+            const int oe = __shfl_xor(be, d);
+            if (oq > best || (oq == best && oe < be)) {
+              best = oq;
+              be = oe;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < EPL; ++i)
+            if (expert_of<TL, LPT>(i, l) == be) out |= 1ull << i;
+          if (l == jj) got[s] = be;
+        }
+      }
+    }
+  }
+
+  // weights: lane l holds positions l, l + LPT, ...
+  float w[SLOTS];
+  const float m = key_value(first);  // the largest logit (softmax only)
+  float sum = 0.0f;
+#pragma unroll
+  for (int s = 0; s < SLOTS; ++s) {
+    const int j = s * LPT + l;
+    w[s] = 0.0f;
+    if (j < k) {
+      const float v = BIAS ? load_logit(row + got[s]) : key_value(got_key[s]);
+      w[s] = a.score == MEP_SCORE_SIGMOID ? sigmoid(v)
+             : m == -__builtin_inff()     ? 0.0f
+                                          : expf(v - m);
+    }
+    sum += w[s];
+  }
+  float scale = a.scale;
+  if (a.normalize || a.score == MEP_SCORE_SOFTMAX) {
+    if (!a.normalize) {  // softmax over all experts
+      sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (expert_of<TL, LPT>(i, l) < E) sum += expf(x[i] - m);
+    }
+    sum = group_sum<LPT>(sum);
+    // nothing selectable (every logit -inf): all weights are 0
+    if (a.score == MEP_SCORE_SOFTMAX && m == -__builtin_inff()) sum = 1.0f;
+    if (sum == 0.0f) sum = 1.0f;
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) w[s] = w[s] / sum;
+  }
+  if (!live) return;
+#pragma unroll
+  for (int s = 0; s < SLOTS; ++s) {
+    const int j = s * LPT + l;
+    if (j < k) {
+      a.indices[t * k + j] = got[s];
+      a.weights[t * k + j] = w[s] * scale;
+    }
+  }
+}
+
+// ---- scores as probabilities ----------------------------------------------
+
+// A token's probabilities over the experts in registers: softmax(x), or the
+// sigmoids over their sum: p[i] * inv.  A row of -inf has probability 0
+// everywhere.  SLOPE: sigmoid scores leave their slopes in x.
+template <int LPT, int EPL, bool SLOPE>
+__device__ __forceinline__ void probabilities(float (&x)[EPL], int score, float (&p)[EPL], float& m,
+                                              float& inv) {
+  float sum = 0.0f;
+  m = 0.0f;
+  if (score == MEP_SCORE_SOFTMAX) {
+    m = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) m = fmaxf(m, x[i]);
+    m = group_fmax<LPT>(m);
+    const float shift = m == -__builtin_inff() ? 0.0f : m;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {  // registers past E hold -inf: exp gives 0
+      p[i] = expf(x[i] - shift);
+      sum += p[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      p[i] = SLOPE ? sigmoid(x[i], x[i]) : sigmoid(x[i]);
+      sum += p[i];
+    }
+  }
+  sum = group_sum<LPT>(sum);
+  inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+}
+
+// ---- balance loss ---------------------------------------------------------
+
+// Blocks of up to 16 tokens a round sum their tokens' probabilities in
+// registers (a group's lanes keep their experts), join the groups through LDS
+// in a fixed order, count the named experts with LDS integer atomics, and
+// write one row of partial sums and counts.  The block that finishes last adds
+// the rows up in order, so the result does not depend on the blocks' timing.
+constexpr int kBalanceThreads = 256;
+
+template <class TL, int LPT, int EPL>
+__global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a) {
+  constexpr int GROUPS = kBalanceThreads / LPT;
+  extern __shared__ float lds[];  // [E] sums, then [E] counts and the valid tokens
+  const int E = a.E, l = threadIdx.x % LPT, g = threadIdx.x / LPT;
+  float* sums = lds;
+  int* cnt = reinterpret_cast<int*>(lds + E);
+  for (int e = threadIdx.x; e <= E; e += kBalanceThreads) cnt[e] = 0;
+  __syncthreads();
+
+  float acc[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) acc[i] = 0.0f;
+  for (int64_t t = (int64_t)blockIdx.x * GROUPS + g; t < a.T; t += (int64_t)gridDim.x * GROUPS) {
+    if (a.mask && a.mask[t] == 0) continue;  // the same for all lanes of the group
+    float x[EPL], p[EPL], m, inv;
+    load_row<TL, LPT, EPL>(reinterpret_cast<const TL*>(a.logits) + t * E, E, l, a.wide, x);
+    probabilities<LPT, EPL, false>(x, a.score, p, m, inv);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) acc[i] += p[i] * inv;
+    for (int j = l; j < a.k; j += LPT) {
+      const int e = a.indices[t * a.k + j];
+      if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
+    }
+    if (l == 0) atomicAdd(&cnt[E], 1);
+  }
+  for (int q = 0; q < GROUPS; ++q) {
+    if (q == g) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = expert_of<TL, LPT>(i, l);
+        if (e < E) sums[e] = q == 0 ? acc[i] : sums[e] + acc[i];
+      }
+    }
+    __syncthreads();
+  }
+  float* part = a.part_sum + (size_t)blockIdx.x * E;
+  int32_t* pcnt = a.part_cnt + (size_t)blockIdx.x * (E + 1);
+  for (int e = threadIdx.x; e <= E; e += kBalanceThreads) {
+    if (e < E) part[e] = sums[e];
+    pcnt[e] = cnt[e];
+  }
+
+  // the last block to arrive joins the partial rows
+  __shared__ int is_last;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) is_last = atomicAdd(a.done, 1u) == gridDim.x - 1;
+  __syncthreads();
+  if (!is_last) return;
+  __threadfence();
+  double* dot = reinterpret_cast<double*>(lds);  // the sums are done with
+  int64_t n = 0;
+  for (unsigned b = 0; b < gridDim.x; ++b) n += a.part_cnt[(size_t)b * (E + 1) + E];
+  double mine = 0.0;
+  for (int e = threadIdx.x; e < E; e += kBalanceThreads) {
+    double s = 0.0;
+    int32_t c = 0;
+    for (unsigned b = 0; b < gridDim.x; ++b) {
+      s += (double)a.part_sum[(size_t)b * E + e];
+      c += a.part_cnt[(size_t)b * (E + 1) + e];
+    }
+    const double mean = n > 0 ? s / (double)n : 0.0;
+    a.counts[e] = c;
+    a.prob_mean[e] = (float)mean;
+    mine += (double)c * mean;
+  }
+  __syncthreads();
+  dot[threadIdx.x] = mine;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double s = 0.0;
+    for (int i = 0; i < kBalanceThreads; ++i) s += dot[i];
+    a.counts[E] = (int32_t)n;
+    a.loss[0] = n > 0 ? (float)(s * (double)a.coef * (double)E / ((double)a.k * (double)n)) : 0.0f;
+    *a.done = 0u;  // ready for the next call on this workspace
+  }
+}
+
+// ---- gradient -------------------------------------------------------------
+
+// One pass over the logits gives both gradients.  The loss: with
+// u_e = dL/dp_e = grad_loss coef E c_e / (k n^2),
+//   softmax:  dx = p (u - sum u p),   sigmoid:  dx = s (1 - s) / S (u - sum u p).
+// The weights: only selected experts receive a gradient of their own; lane j
+// works out position j's and adds it through the group's row in LDS, a
+// repeated expert's positions added up in order first.
+constexpr int kGradThreads = 256;
+
+template <class TL, int LPT, int EPL>
+__global__ __launch_bounds__(kGradThreads) void gate_backward_kernel(GateBackwardArgs a) {
+  constexpr int SLOTS = (kMaxTopk + LPT - 1) / LPT;
+  extern __shared__ float lds[];  // [groups][E]: what the weights' gradient adds
+  const int l = threadIdx.x % LPT, g = threadIdx.x / LPT;
+  const int E = a.E, k = a.k;
+  const int64_t t = (int64_t)blockIdx.x * (kGradThreads / LPT) + g;
+  const bool live = t < a.T;
+  const int64_t tt = live ? t : a.T - 1;
+  const bool valid = !a.mask || a.mask[tt] != 0;
+  const TL* row = reinterpret_cast<const TL*>(a.logits) + tt * E;
+  float* extra = lds + (size_t)g * E;
+
+  float x[EPL], p[EPL], m, inv;
+  load_row<TL, LPT, EPL>(row, E, l, a.wide, x);
+  probabilities<LPT, EPL, true>(x, a.score, p, m, inv);
+  const bool softmax = a.score == MEP_SCORE_SOFTMAX;
+
+  // the loss' gradient for each expert's probability
+  float u[EPL], dot = 0.0f;
+  float coef = 0.0f;
+  if (a.counts) {
+    const double n = (double)a.counts[E];
+    coef = n > 0 ? (float)((double)a.grad_loss[0] * (double)a.coef * E / (k * n * n)) : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = expert_of<TL, LPT>(i, l);
+    u[i] = a.counts && e < E ? coef * (float)a.counts[e] : 0.0f;
+    dot += u[i] * (p[i] * inv);
+  }
+  dot = group_sum<LPT>(dot);
+
+  // the weights' gradient for each position
+  float shift = 0.0f;  // unnormalised softmax: sum over positions of g p, taken off every expert
+  if (a.grad_weights) {
+    for (int e = l; e < E; e += LPT) extra[e] = 0.0f;
+    int id[SLOTS];
+    float v[SLOTS], d[SLOTS], gw[SLOTS];
+    float total = 0.0f, gsum = 0.0f;
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      const int j = s * LPT + l;
+      id[s] = -1;
+      v[s] = d[s] = gw[s] = 0.0f;
+      if (j < k) {
+        const int e = a.indices[tt * k + j];
+        if (e >= 0 && e < E) {
+          id[s] = e;
+          gw[s] = a.scale * a.grad_weights[tt * k + j];
+          const float xe = load_logit(row + e);
+          if (softmax) {
+            v[s] = m == -__builtin_inff() ? 0.0f : expf(xe - m);
+          } else {
+            v[s] = sigmoid(xe, d[s]);
+          }
+        }
+      }
+      total += v[s];
+      gsum += gw[s] * v[s];
+    }
+    total = group_sum<LPT>(total);
+    gsum = group_sum<LPT>(gsum);
+    const float tinv = total == 0.0f ? 0.0f : 1.0f / total;
+    float add[SLOTS];
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      if (softmax)
+        add[s] = a.normalize ? v[s] * tinv * (gw[s] - gsum * tinv) : v[s] * inv * gw[s];
+      else
+        add[s] = a.normalize ? d[s] * tinv * (gw[s] - gsum * tinv) : d[s] * gw[s];
+    }
+    if (softmax && !a.normalize) shift = gsum * inv;
+    __syncthreads();
+    // a repeated expert: its first position adds up all of them
+    float sum[SLOTS];
+    bool mine[SLOTS];
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) { sum[s] = 0.0f; mine[s] = id[s] >= 0; }
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      for (int jj = 0; jj < LPT; ++jj) {
+        const int j = s * LPT + jj;
+        if (j >= k) break;
+        const int oe = __shfl(id[s], jj, LPT);
+        const float oa = __shfl(add[s], jj, LPT);
+#pragma unroll
+        for (int q = 0; q < SLOTS; ++q) {
+          if (oe == id[q]) {
+            sum[q] += oa;
+            if (j < q * LPT + l) mine[q] = false;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s)
+      if (mine[s]) extra[id[s]] = sum[s];
+    __syncthreads();
+  }
+
+  if (!live) return;
+  TL* out = reinterpret_cast<TL*>(a.grad_logits) + t * E;
+  float r[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = expert_of<TL, LPT>(i, l);
+    float v;
+    if (softmax)
+      v = p[i] * inv * (u[i] - dot - shift);
+    else
+      v = x[i] * inv * (u[i] - dot);
+    if (a.grad_weights && e < E) v += extra[e];
+    r[i] = valid ? v : 0.0f;
+  }
+  constexpr int V = Vec<TL>::V;
+  if (a.wide) {
+#pragma unroll
+    for (int c = 0; c < EPL / V; ++c) {
+      const int e = (c * LPT + l) * V;
+      if (e < E) Vec<TL>::store(out + e, &r[c * V]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = expert_of<TL, LPT>(i, l);
+      if (e < E) Vec<TL>::store1(out + e, r[i]);
+    }
+  }
+}
+
+// ---- launches -------------------------------------------------------------
+
+// Calls f with the (lanes, values a lane) that hold E experts.
+template <class F>
+void by_experts(int E, F f) {
+  using std::integral_constant;
+  if (E <= 64) f(integral_constant<int, 8>{}, integral_constant<int, 8>{});
+  else if (E <= 128) f(integral_constant<int, 16>{}, integral_constant<int, 8>{});
+  else if (E <= 256) f(integral_constant<int, 16>{}, integral_constant<int, 16>{});
+  else if (E <= 512) f(integral_constant<int, 16>{}, integral_constant<int, 32>{});
+  else if (E <= 1024) f(integral_constant<int, 64>{}, integral_constant<int, 16>{});
+  else f(integral_constant<int, 64>{}, integral_constant<int, 64>{});
+}
+
+int lanes_of(int E) { return E <= 64 ? 8 : E <= 512 ? 16 : 64; }
+
+template <class TL>
+void gate_typed(const GateArgs& a, hipStream_t s) {
+  const int64_t threads = (int64_t)a.T * lanes_of(a.E);
+  const unsigned blocks = (unsigned)((threads + kGateThreads - 1) / kGateThreads);
+  by_experts(a.E, [&](auto lpt, auto epl) {
+    if (a.bias)
+      gate_kernel<TL, lpt(), epl(), true><<<blocks, kGateThreads, 0, s>>>(a);
+    else
+      gate_kernel<TL, lpt(), epl(), false><<<blocks, kGateThreads, 0, s>>>(a);
+  });
+}
+
+}  // namespace
+
+static bool is_wide(int E, int dtype) { return E % (dtype == MEP_BF16 ? 8 : 4) == 0; }
+
+hipError_t launch_gate(const GateArgs& a0, hipStream_t s) {
+  if (a0.T == 0) return hipSuccess;
+  GateArgs a = a0;
+  a.wide = is_wide(a.E, a.dtype);
+  if (a.dtype == MEP_BF16) gate_typed<uint16_t>(a, s);
+  else gate_typed<float>(a, s);
+  return hipGetLastError();
+}
+
+int balance_blocks(int E, int64_t T) {
+  const int64_t groups = kBalanceThreads / lanes_of(E);
+  const int64_t want = (T + 4 * groups - 1) / (4 * groups);
+  return (int)(want < 1 ? 1 : want > 64 ? 64 : want);
+}
+
+hipError_t launch_balance(const BalanceArgs& a0, hipStream_t s) {
+  BalanceArgs a = a0;
+  a.wide = is_wide(a.E, a.dtype);
+  const unsigned blocks = (unsigned)balance_blocks(a.E, a.T);
+  by_experts(a.E, [&](auto lpt, auto epl) {
+    const size_t lds = std::max((size_t)(2 * a.E + 1) * 4, (size_t)kBalanceThreads * 8);
+    if (a.dtype == MEP_BF16)
+      balance_kernel<uint16_t, lpt(), epl()><<<blocks, kBalanceThreads, lds, s>>>(a);
+    else
+      balance_kernel<float, lpt(), epl()><<<blocks, kBalanceThreads, lds, s>>>(a);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_gate_backward(const GateBackwardArgs& a0, hipStream_t s) {
+  if (a0.T == 0) return hipSuccess;
+  GateBackwardArgs a = a0;
+  a.wide = is_wide(a.E, a.dtype);
+  by_experts(a.E, [&](auto lpt, auto epl) {
+    const int groups = kGradThreads / lpt();
+    const unsigned blocks = (unsigned)((a.T + groups - 1) / groups);
+    const size_t lds = a.grad_weights ? (size_t)groups * a.E * 4 : 0;
+    if (a.dtype == MEP_BF16)
+      gate_backward_kernel<uint16_t, lpt(), epl()><<<blocks, kGradThreads, lds, s>>>(a);
+    else
+      gate_backward_kernel<float, lpt(), epl()><<<blocks, kGradThreads, lds, s>>>(a);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace mep

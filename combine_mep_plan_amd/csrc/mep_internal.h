@@ -209,6 +209,78 @@ struct WsPtrs {
   uint32_t* ufirst;
 };
 
+struct GateArgs {              // router: top-k experts and weights
+  const void* logits;           // [T,E] fp32 or bf16
+  const float* bias;            // [E] selection bias (sigmoid), or null
+  int32_t* indices;             // [T,k]
+  float* weights;               // [T,k]
+  int32_t T, E, k, score, dtype, normalize;
+  float scale;
+  bool wide;                    // rows are whole 16-byte units, set at launch
+};
+
+struct BalanceArgs {
+  const void* logits;
+  const int32_t* indices;       // [T,k]
+  const uint8_t* mask;          // [T], or null: every token counts
+  int32_t* counts;              // [E+1]
+  float* prob_mean;             // [E]
+  float* loss;                  // [1]
+  uint32_t* done;               // blocks that have written their row; 0 between calls
+  float* part_sum;              // [blocks][E]
+  int32_t* part_cnt;            // [blocks][E+1]
+  int32_t T, E, k, score, dtype;
+  float coef;
+  bool wide;
+};
+
+struct GateBackwardArgs {
+  const void* logits;
+  const int32_t* indices;       // [T,k]
+  const uint8_t* mask;          // [T], or null
+  const float* grad_weights;    // [T,k], or null
+  const int32_t* counts;        // [E+1], or null: no loss gradient
+  const float* grad_loss;       // [1]
+  void* grad_logits;            // [T,E] in the logits' type
+  int32_t T, E, k, score, dtype, normalize;
+  float scale, coef;
+  bool wide;
+};
+
+struct LinearArgs {            // experts' product over expert-major rows
+  const void* x;                // [cap_em,K]
+  const float* x_scales;        // [cap_em,K/128], E4M3 only
+  const void* w;                // [E,Nz,K]
+  const float* w_scales;        // [E,Nz/128,K/128], E4M3 only
+  const float* bias;            // [E,Nz], or null
+  const void* residual;         // [cap_em,N] bf16, or null
+  void* y;                      // [cap_em,N] bf16
+  void* z;                      // [cap_em,Nz] bf16, or null
+  const int32_t* counts;        // [E]
+  const int32_t* offsets;       // [E+1]
+  int64_t cap, num_rows;
+  int32_t E, K, N, Nz, act, quant;
+};
+
+struct LinearBackwardArgs {
+  const void* grad_y;           // [cap_em,N] bf16
+  const void* z;                // [cap_em,Nz] bf16; unused without an activation
+  const void* x;                // [cap_em,K] bf16
+  const void* w;                // [E,Nz,K] bf16
+  const int32_t* counts;
+  const int32_t* offsets;
+  void* grad_x;                 // [cap_em,K] bf16, or null
+  void* grad_w;                 // [E,Nz,K] bf16, or null
+  float* grad_bias;             // [E,Nz], or null
+  void* grad_z;                 // workspace [cap_em,Nz] bf16; grad_y without an activation
+  float* part;                  // workspace [row blocks][Nz]: bias gradient of each block
+  int64_t cap, num_rows;
+  int32_t E, K, N, Nz, act;
+};
+
+constexpr int kSegRows = 128;   // expert segments start at multiples of this many rows
+constexpr int kMaxExperts = kMaxRanks * kMaxEpr;
+
 // Host-side checks and argument packing shared by the entry points
 // (mep_abi.cpp); each check returns MEP_OK or a MEP_ERR_* code.
 int check_config(const mep_config* c);
@@ -238,6 +310,12 @@ hipError_t launch_combine_fp8(const CombineArgs& a, hipStream_t s);  // y holds 
 hipError_t launch_cast_fp8(const CastArgs& a, hipStream_t s);
 hipError_t launch_to_expert_major(const EmArgs& a, hipStream_t s);
 hipError_t launch_convert_combine_input(const ConvertArgs& a, hipStream_t s);
+hipError_t launch_gate(const GateArgs& a, hipStream_t s);
+int balance_blocks(int E, int64_t T);  // rows of partial sums a balance call writes
+hipError_t launch_balance(const BalanceArgs& a, hipStream_t s);
+hipError_t launch_gate_backward(const GateBackwardArgs& a, hipStream_t s);
+hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
+hipError_t launch_linear_backward(const LinearBackwardArgs& a, hipStream_t s);
 hipError_t launch_copy_i32(const int32_t* src, int32_t* dst, int64_t n, hipStream_t s);
 hipError_t launch_probe_e4m3(const float* in, uint8_t* out, int64_t n, hipStream_t s);
 hipError_t launch_probe_bf16(const float* in, uint16_t* out, int64_t n, hipStream_t s);

@@ -10,11 +10,11 @@
  *
  * Conventions (every entry point):
  *   - Pointers named x, scales, recv_*, y, y8, out, em_*, indices, weights,
- *     recv_counts, src_token_pos and workspace are DEVICE pointers, caller-owned, borrowed
- *     only for the duration of the asynchronous call on `stream`
- *     (a hipStream_t passed as void*; NULL = the null stream).  The library
- *     never allocates or frees device memory and never synchronises, except
- *     in mep_get_status.
+ *     recv_counts, src_token_pos and workspace, and all tensors of the router
+ *     and expert calls, are DEVICE pointers, caller-owned, borrowed only for
+ *     the duration of the asynchronous call on `stream` (a hipStream_t passed
+ *     as void*; NULL = the null stream).  The library never allocates or frees
+ *     device memory and never synchronises, except in mep_get_status.
  *   - All device pointers must be 16-byte aligned (MEP_ERR_ALIGN otherwise).
  *   - Errors a host can see (null pointers, bad shapes, alignment, call order)
  *     return a negative MEP_ERR_* code synchronously and launch nothing.
@@ -358,6 +358,140 @@ int mep_get_status(mep_handle *h, void *stream, int32_t *device_status);
  * mep_dispatch_standard_moe).  Either pointer may be NULL, not both.
  */
 int mep_get_route(mep_handle *h, int32_t *recv_row, int32_t *em_row, void *stream);
+
+/* ---- router ------------------------------------------------------------ */
+#define MEP_FP32 0               /* logits and their gradient: fp32               */
+#define MEP_BF16 1               /* logits and their gradient: bf16               */
+#define MEP_SCORE_SOFTMAX 0      /* p = softmax of the logits                      */
+#define MEP_SCORE_SIGMOID 1      /* s = 1 / (1 + exp(-x)), p = s / sum of s        */
+
+typedef struct mep_gate_config {
+  int32_t num_experts; /* E: 1..4096                                             */
+  int32_t top_k;       /* k: 1..32, k <= E                                       */
+  int32_t score;       /* MEP_SCORE_*                                            */
+  int32_t dtype;       /* MEP_FP32 or MEP_BF16                                   */
+  int32_t normalize;   /* not 0: a token's k weights are divided by their sum    */
+  float scale;         /* factor of every weight                                 */
+  float balance_coef;  /* coef of the balance loss                               */
+} mep_gate_config;
+
+/*
+ * Router: the k experts of each token and their weights, in the form the plan,
+ * dispatch and combine take them.  logits is [T,E]; per token,
+ *   softmax: the k largest logits; v_j = exp(x_j - max) / sum over all experts
+ *            of the same (p_j);
+ *   sigmoid: the k largest s_e + bias[e] (bias fp32 [E], NULL for none); v_j =
+ *            s_j, without the bias;
+ *   weights[t, j] = scale * v_j, or scale * v_j / sum_j v_j when normalizing.
+ * indices (int32) and weights (fp32) are [T,k], largest first; equal values go
+ * to the lower expert, and sigmoid scores that fp32 cannot order are compared
+ * in 64 bits.  All k experts of a token are different, whatever its logits: NaN
+ * ranks last, and a selected NaN gives NaN weights, as does a logit of +inf
+ * under softmax; where every v_j is 0 (logits of -inf) the weights are 0.
+ * 0 <= T <= 2^26.  MEP_ERR_CONFIG for a bias with softmax scores.
+ */
+int mep_gate(const mep_gate_config *cfg, const void *logits, const float *bias, int32_t T,
+             int32_t *indices, float *weights, void *stream);
+
+/*
+ * Load-balance loss of a batch and what it is made of.  With n the tokens that
+ * count (token_mask[t] != 0, uint8 [T]; NULL: all T), over those tokens
+ *   counts[e]    = number of (t, j) with indices[t, j] == e (int32; ids outside
+ *                  [0, E) are left out); counts[E] = n;
+ *   prob_mean[e] = (1/n) sum_t p[t, e] (fp32 [E]);
+ *   loss[0]      = balance_coef * E / (k n) * sum_e counts[e] prob_mean[e].
+ * All are 0 when n is 0.  Rows that do not count may hold anything, NaN
+ * included.  Results do not depend on timing (no floating-point atomics).
+ * workspace: at least mep_balance_workspace_bytes(cfg, T) bytes (0 if cfg or T is
+ * invalid), zero-filled before its first use; it serves one call at a time and
+ * is ready for the next when the call has run.  0 <= T <= 2^26,
+ * T*k <= INT32_MAX.
+ */
+size_t mep_balance_workspace_bytes(const mep_gate_config *cfg, int32_t T);
+int mep_balance_loss(const mep_gate_config *cfg, const void *logits, const int32_t *indices,
+                     const uint8_t *token_mask, int32_t T, int32_t *counts, float *prob_mean,
+                     float *loss, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradient of the router's weights (for fixed indices) and of the balance loss
+ * with respect to the logits, in one pass:
+ *   grad_logits = d( sum_tj grad_weights[t, j] weights[t, j]
+ *                    + grad_loss[0] * loss ) / d logits, in the logits' type.
+ * grad_weights (fp32 [T,k]) may be NULL: no gradient from the weights; counts
+ * (as mep_balance_loss wrote it) and grad_loss (fp32, one value on the device)
+ * may be NULL together: none from the loss.  Not both groups.  Counts are
+ * constants of the differentiation.  Ids outside [0, E) have no weight and no
+ * gradient; an expert a token names twice collects both.  A token that does not
+ * count (token_mask) gets a row of zeros.  0 <= T <= 2^26.
+ */
+int mep_gate_backward(const mep_gate_config *cfg, const void *logits, const int32_t *indices,
+                      const uint8_t *token_mask, int32_t T, const float *grad_weights,
+                      const int32_t *counts, const float *grad_loss, void *grad_logits,
+                      void *stream);
+
+/* ---- experts' products ---------------------------------------------------- */
+#define MEP_ACT_NONE 0
+#define MEP_ACT_GELU 1           /* z/2 (1 + erf(z / sqrt 2))                      */
+#define MEP_ACT_SILU 2           /* z / (1 + exp(-z))                              */
+#define MEP_ACT_SILU_GLU 3       /* silu(z[:, :N]) * z[:, N:]                      */
+
+typedef struct mep_linear_config {
+  int32_t num_experts; /* E: 1..4096 segments                                    */
+  int32_t in_dim;      /* K: multiple of 8, of 128 for E4M3; at most 2^20        */
+  int32_t out_dim;     /* N, columns of y: likewise                              */
+  int32_t act;         /* MEP_ACT_*; Nz, rows of a weight, is 2N for
+                          MEP_ACT_SILU_GLU (gate rows, then the others) and N
+                          otherwise                                              */
+  int32_t quant;       /* MEP_QUANT_NONE: bf16 rows and weights;
+                          MEP_QUANT_FP8_E4M3_BLOCK128: E4M3 rows with one scale per
+                          128 columns, as the dispatch writes them, and E4M3
+                          weights with one scale per 128 x 128                   */
+} mep_linear_config;
+
+/*
+ * The experts' product over an expert-major buffer (mep_to_expert_major,
+ * mep_dispatch_standard_moe): for every expert e and row r of its em_counts[e]
+ * rows from em_offsets[e] on,
+ *   z[r, :] = em_x[r, :] . w[e]^T + bias[e, :]      (fp32 accumulation)
+ *   y[r, :] = bf16_rne(act(z[r, :]) + residual[r, :])
+ * em_x is [cap_em,K], w [E,Nz,K], bias fp32 [E,Nz] or NULL, residual bf16
+ * [cap_em,N] or NULL, y bf16 [cap_em,N]; z, bf16 [cap_em,Nz], receives the
+ * product before the activation for mep_expert_linear_backward, or is NULL.
+ * E4M3: em_scales fp32 [cap_em,K/128], w_scales fp32 [E,Nz/128,K/128]; a value is
+ * code * scale; both NULL for bf16.  Rows outside the segments' counts (padding,
+ * rows behind the last segment) are neither used nor written, and rows past
+ * cap_em are left out.  em_offsets[e] must be multiples of 128, em_counts[e] >=
+ * 0 and segments must not overlap, as the calls above write them.  One segment
+ * over a whole batch (E = 1) is an ordinary dense layer.  num_rows is the number
+ * of rows to expect in all segments together (T*k): it selects among kernels and
+ * sizes the launch; results are complete for any value.  0 <= cap_em <=
+ * INT32_MAX.  y and z overlap no input, but y may be residual itself.
+ */
+int mep_expert_linear(const mep_linear_config *cfg, const void *em_x, const float *em_scales,
+                      const int32_t *em_counts, const int32_t *em_offsets, int64_t cap_em,
+                      int64_t num_rows, const void *w, const float *w_scales, const float *bias,
+                      const void *residual, void *y, void *z, void *stream);
+
+/*
+ * Gradients of mep_expert_linear (bf16 only).  With grad_z = grad_y * act'(z)
+ * (grad_y itself without an activation), per expert over its rows
+ *   grad_x[r, :]    = grad_z[r, :] . w[e]           (bf16 [cap_em,K])
+ *   grad_w[e]       = grad_z^T . em_x               (bf16 [E,Nz,K])
+ *   grad_bias[e, :] = sum over rows of grad_z       (fp32 [E,Nz])
+ * each NULL when not wanted, not all three.  z is the forward call's (NULL
+ * allowed without an activation).  The residual's gradient is grad_y.  Rows of
+ * grad_x outside the segments are not written; an expert without rows has zeros
+ * in grad_w and grad_bias.  grad_z is rounded to bf16 for the two products, not
+ * for grad_bias.  workspace: mep_linear_workspace_bytes(cfg, cap_em) bytes (0 if cfg
+ * or cap_em is invalid), of any content; it serves one call at a time.
+ * num_rows as above.  No output may overlap an input.
+ */
+size_t mep_linear_workspace_bytes(const mep_linear_config *cfg, int64_t cap_em);
+int mep_expert_linear_backward(const mep_linear_config *cfg, const void *grad_y, const void *z,
+                               const void *em_x, const void *w, const int32_t *em_counts,
+                               const int32_t *em_offsets, int64_t cap_em, int64_t num_rows,
+                               void *grad_x, void *grad_w, float *grad_bias, void *workspace,
+                               size_t workspace_bytes, void *stream);
 
 /*
  * Codec probes: run, over n values, exactly the device conversions the

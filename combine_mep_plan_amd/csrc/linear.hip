@@ -7,11 +7,18 @@
 //   grad_x    dx[r, k] = sum_n w[e, n, k] dz[r, n]
 //   grad_w    dw[e, n, k] = sum_r x[r, k] dz[r, n]
 // An operand whose summed index is contiguous in memory is "direct", the others
-// (w in grad_x, both in grad_w) are turned around on their way into LDS.
+// (w in grad_x, both in grad_w) are "turned": the hardware's transposing LDS
+// reads give MFMA the values that lie along the summed index.
 //
-// LDS holds tiles of 128 rows by 64 values of the summed index, 128 bytes a
-// row, its eight 16-byte units exchanged by the low bits of the row so that the
-// MFMA operand reads (16 rows, one unit each) touch every bank once.
+// A tile of 256 x 256 outputs takes 64 bf16 (128 E4M3) values of the summed index
+// a step: 32 KiB of each operand, moved from memory straight into LDS (no
+// registers), in two buffers of each, so that the next step's loads run while
+// this step's 64 MFMAs a wave do.  A step reads (256 + 256) x 128 bytes from
+// memory and 192 KiB from LDS for 8.4 MFLOP: LDS at 128 bytes a clock needs 75%
+// of the time the matrix cores need, which is why the tile is this large.
+// 16-byte units of an LDS row are exchanged by the row's low bits (by the
+// source address, as the loads fill LDS lane after lane) so that operand reads
+// touch every bank once.
 #include <algorithm>
 #include <type_traits>
 
@@ -27,9 +34,6 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 
 enum Mode { kForward, kGradX, kGradW };
-
-constexpr int kTile = 128;      // rows and columns of an output tile
-constexpr int kThreads = 256;
 
 struct TileArgs {
   const unsigned char* a;       // first operand: w (forward, grad_x), x (grad_w)
@@ -59,43 +63,93 @@ __device__ __forceinline__ int segment_rows(const TileArgs& a, int e) {
 
 __device__ __forceinline__ u32x4 zero4() { return u32x4{0, 0, 0, 0}; }
 
-__device__ __forceinline__ int swizzle(int row, int unit) { return unit ^ (row & 7); }
-
 __device__ __forceinline__ float silu(float z) { return z / (1.0f + expf(-z)); }
 __device__ __forceinline__ float gelu(float z) {
   return 0.5f * z * (1.0f + erff(z * 0.70710678118654752f));
 }
 
-// Columns of the weight that LDS row r of the tile at column tile n holds: with a
-// gated activation every 32 rows are 16 gate rows and the 16 rows they gate.
-template <bool GLU>
+// Row of the weight that row r of column tile n holds: with a gated activation
+// every 32 rows are 16 gate rows and the 16 rows they gate, so that both halves
+// of an output land in the same lane.
+template <bool GLU, int BN>
 __device__ __forceinline__ int weight_row(int n, int r, int cols) {
-  if (!GLU) return min(n * kTile + r, cols - 1);
-  const int c = min(n * (kTile / 2) + (r >> 5) * 16 + (r & 15), cols - 1);
+  if (!GLU) return min(n * BN + r, cols - 1);
+  const int c = min(n * (BN / 2) + (r >> 5) * 16 + (r & 15), cols - 1);
   return (r & 16) ? cols + c : c;
 }
 
-template <Mode MODE, bool FP8, int ACT>
-__global__ __launch_bounds__(kThreads) void tile_kernel(TileArgs a) {
-  constexpr bool GLU = MODE == kForward && ACT == MEP_ACT_SILU_GLU;
-  constexpr int kVals = FP8 ? 128 : 64;      // summed values a step
-  constexpr int kUnit = FP8 ? 16 : 8;        // values in 16 bytes
-  constexpr int kSize = FP8 ? 1 : 2;
-  constexpr int kCols = GLU ? kTile / 2 : kTile;  // output columns a tile
-  __shared__ u32x4 la[kTile * 8], lb[kTile * 8];
+#define MEP_LDS __attribute__((address_space(3)))
+#define MEP_GLOBAL __attribute__((address_space(1)))
+
+// 16 bytes a lane straight from memory into LDS, lane after lane from `lds` on
+// (the same address for the whole wave).
+__device__ __forceinline__ void load_to_lds(const unsigned char* p, unsigned char* lds) {
+  __builtin_amdgcn_global_load_lds((const MEP_GLOBAL uint32_t*)p, (MEP_LDS uint32_t*)lds, 16, 0, 0);
+}
+
+// All of this wave's loads have landed, then everyone's; nothing moves across.
+__device__ __forceinline__ void wait_loads_and_sync() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// How the units of a turned tile's row k are exchanged: the four rows that 16
+// lanes of a transposing read touch, and those of the next 16 lanes, fall on
+// eight different 32-byte pieces of the banks.
+__device__ __forceinline__ int turned_swizzle(int k) { return ((k & 3) | ((k >> 1) & 4)) << 1; }
+
+template <Mode MODE, bool FP8, int ACT, int WN, int WM, int TN, int TM>
+struct Tile {
+  static constexpr bool GLU = MODE == kForward && ACT == MEP_ACT_SILU_GLU;
+  static constexpr bool A_TURNED = MODE != kForward, B_TURNED = MODE == kGradW;
+  static constexpr int WAVES = WN * WM, THREADS = WAVES * 64;
+  static constexpr int BN = WN * TN * 16, BM = WM * TM * 16;
+  static constexpr int VALS = FP8 ? 128 : 64;         // summed values a step
+  static constexpr int UNIT = FP8 ? 16 : 8;           // values in 16 bytes
+  static constexpr int SIZE = FP8 ? 1 : 2;
+  static constexpr int COLS = GLU ? BN / 2 : BN;      // output columns a tile
+  static constexpr int RA = BN / 8 / WAVES;           // loads of 1 KiB a wave and step
+  static constexpr int RB = BM / 8 / WAVES;
+};
+
+template <class T, int ROWS, bool TURNED>
+__device__ __forceinline__ bf16x8 fragment(const unsigned char* lds, int at, int s, int lane) {
+  const int g = lane >> 4, r16 = lane & 15;
+  if (!TURNED) {
+    const int r = at + r16;
+    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(
+                                          lds + r * 128 + (((s * 4 + g) ^ (r & 7)) << 4)));
+  }
+  typedef short s16x4 __attribute__((ext_vector_type(4)));
+  const int k = s * 32 + g * 8 + (r16 >> 2);
+  const int u = ((at >> 3) + ((r16 & 3) >> 1)) ^ turned_swizzle(k);
+  const unsigned char* p = lds + k * (ROWS * 2) + u * 16 + (r16 & 1) * 8;
+  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MEP_LDS s16x4*)p);
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MEP_LDS s16x4*)(p + 4 * ROWS * 2));
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
+template <Mode MODE, bool FP8, int ACT, int WN, int WM, int TN, int TM>
+__global__ __launch_bounds__(WN * WM * 64) void tile_kernel(TileArgs a) {
+  using T = Tile<MODE, FP8, ACT, WN, WM, TN, TM>;
+  constexpr bool GLU = T::GLU;
+  constexpr int BN = T::BN, BM = T::BM, RA = T::RA, RB = T::RB;
+  __shared__ __attribute__((aligned(1024))) unsigned char la0[BN * 128], la1[BN * 128];
+  __shared__ __attribute__((aligned(1024))) unsigned char lb0[BM * 128], lb1[BM * 128];
   extern __shared__ int32_t first[];         // [E+1]: row tiles before each expert
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wn = wave & 1, wm = wave >> 1;   // the wave's 64 x 64 quarter
-  const int col_tiles = (a.cols + kCols - 1) / kCols;
+  const int tid = threadIdx.x, lane = tid & 63, wave = first_lane(tid >> 6);
+  const int wn = wave % WN, wm = wave / WN;
+  const int col_tiles = (a.cols + T::COLS - 1) / T::COLS;
 
-  // row tiles before each expert: the tiles of a launch follow the counts
   if (MODE != kGradW) {
     if (tid < kWave) {
       int base = 0;
       for (int e0 = 0; e0 < a.E; e0 += kWave) {
         const int e = e0 + tid;
-        const int n = e < a.E ? (segment_rows(a, e) + kTile - 1) / kTile : 0;
+        const int n = e < a.E ? (segment_rows(a, e) + BM - 1) / BM : 0;
         int s = n;
         for (int d = 1; d < kWave; d <<= 1) {
           const int o = __shfl_up(s, d);
@@ -108,162 +162,205 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(TileArgs a) {
     }
     __syncthreads();
   }
-  const int row_tiles = MODE == kGradW ? (a.rows + kTile - 1) / kTile : 0;
-  const int64_t tiles = MODE == kGradW ? (int64_t)a.E * row_tiles * col_tiles
+  const int grad_w_tiles = (a.rows + BM - 1) / BM;
+  const int64_t tiles = MODE == kGradW ? (int64_t)a.E * grad_w_tiles * col_tiles
                                        : (int64_t)first[a.E] * col_tiles;
+  // blocks go round the 8 XCDs in turn: give each XCD a run of neighbouring tiles
+  const int per = gridDim.x / 8;
+  const int64_t start = gridDim.x % 8 == 0 ? (blockIdx.x % 8) * (int64_t)per + blockIdx.x / 8
+                                           : blockIdx.x;
 
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int n = (int)(tile % col_tiles);
-    int e, m;
+  for (int64_t tile = start; tile < tiles; tile += gridDim.x) {
+    int e, m, n;
     if (MODE == kGradW) {
-      const int64_t q = tile / col_tiles;
-      e = (int)(q / row_tiles);
-      m = (int)(q % row_tiles);
+      const int per_e = grad_w_tiles * col_tiles;
+      e = (int)(tile / per_e);
+      const int q = (int)(tile % per_e);
+      m = q % grad_w_tiles;
+      n = q / grad_w_tiles;
     } else {
-      const int q = (int)(tile / col_tiles);
-      int lo = 0, hi = a.E;  // the last expert with first[e] <= q
+      int lo = 0, hi = a.E;  // the last expert whose tiles start at or before this one
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (first[mid] <= q) lo = mid; else hi = mid;
+        if ((int64_t)first[mid] * col_tiles <= tile) lo = mid; else hi = mid;
       }
-      e = lo;
-      m = q - first[e];
+      e = first_lane(lo);
+      const int mt = first[e + 1] - first[e];
+      const int q = (int)(tile - (int64_t)first[e] * col_tiles);
+      m = first_lane(q % mt);
+      n = first_lane(q / mt);
     }
     const int seg = segment_rows(a, e);
     const int64_t row0 = a.offsets[e];
     const int depth = MODE == kGradW ? seg : a.depth;
+    const int rows = MODE == kGradW ? a.rows : seg;  // output rows of this expert
+    const bool active = m * BM + wm * (TM * 16) < rows;
 
-    f32x4 acc[4][4];
+    // where this lane's pieces of the two tiles come from: for a direct operand
+    // 8 rows of 128 bytes a load, for a turned one 1 KiB of whole rows k
+    const unsigned char *pa[RA], *pb[RB];
+    const int64_t lda = (int64_t)(T::A_TURNED ? a.cols : depth) * T::SIZE;
+    const int64_t ldb = (int64_t)(T::B_TURNED ? a.rows : depth) * T::SIZE;
+    constexpr int UA = BN / 8, UB = BM / 8;  // 16-byte units in a row of a turned tile
+    const int du = (lane & 7) ^ (lane >> 3);
+    const int64_t a0 = MODE == kGradW ? row0 : (int64_t)e * a.Nz;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-
-    for (int k0 = 0; k0 < depth; k0 += kVals) {
-      __syncthreads();
-      // 128 rows x 8 units of each operand
-      if (MODE == kForward) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = tid + i * kThreads, r = c >> 3, u = c & 7;
-          const int k = k0 + u * kUnit;
-          const int wr = weight_row<GLU>(n, r, a.cols);
-          la[r * 8 + swizzle(r, u)] =
-              k < depth ? *reinterpret_cast<const u32x4*>(
-                              a.a + (((int64_t)e * a.Nz + wr) * depth + k) * kSize)
-                        : zero4();
-        }
+    for (int i = 0; i < RA; ++i) {
+      const int c = i * T::WAVES + wave;
+      if (T::A_TURNED) {
+        const int k = c * (64 / UA) + lane / UA;
+        const int col = min(n * BN + ((lane % UA) ^ turned_swizzle(k)) * 8, a.cols - 8);
+        pa[i] = a.a + (a0 + k) * lda + col * 2;
       } else {
-        // 64 summed values x 16 units of 8 columns, turned around
-        const int ld = a.cols;
-        const int64_t r0 = MODE == kGradX ? (int64_t)e * a.Nz : row0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = tid + i * kThreads, k = c >> 4, u = c & 15;
-          const int col = n * kTile + u * 8;
-          u32x4 v = zero4();
-          if (k0 + k < depth && col < a.cols)
-            v = *reinterpret_cast<const u32x4*>(a.a + ((r0 + k0 + k) * ld + col) * 2);
-          uint16_t* l16 = reinterpret_cast<uint16_t*>(la);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const int r = u * 8 + q;
-            l16[(r * 8 + swizzle(r, k >> 3)) * 8 + (k & 7)] =
-                (uint16_t)(v[q >> 1] >> ((q & 1) * 16));
-          }
-        }
-      }
-      if (MODE != kGradW) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = tid + i * kThreads, r = c >> 3, u = c & 7;
-          const int k = k0 + u * kUnit;
-          const int64_t xr = row0 + min(m * kTile + r, seg - 1);
-          lb[r * 8 + swizzle(r, u)] =
-              k < depth ? *reinterpret_cast<const u32x4*>(a.b + (xr * depth + k) * kSize)
-                        : zero4();
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = tid + i * kThreads, k = c >> 4, u = c & 15;
-          const int col = m * kTile + u * 8;
-          u32x4 v = zero4();
-          if (k0 + k < depth && col < a.rows)
-            v = *reinterpret_cast<const u32x4*>(a.b + ((row0 + k0 + k) * a.rows + col) * 2);
-          uint16_t* l16 = reinterpret_cast<uint16_t*>(lb);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const int r = u * 8 + q;
-            l16[(r * 8 + swizzle(r, k >> 3)) * 8 + (k & 7)] =
-                (uint16_t)(v[q >> 1] >> ((q & 1) * 16));
-          }
-        }
-      }
-      __syncthreads();
-
-      const int g = lane >> 4, r16 = lane & 15;
-      if (FP8) {
-        // one MFMA sums a whole scale block; the blocks join in fp32
-        i32x8 av[4], bv[4];
-        float sb[4];
-        const int kb = k0 / 128;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int ra = wn * 64 + i * 16 + r16, rb = wm * 64 + i * 16 + r16;
-          const u32x4 a0 = la[ra * 8 + swizzle(ra, 2 * g)], a1 = la[ra * 8 + swizzle(ra, 2 * g + 1)];
-          const u32x4 b0 = lb[rb * 8 + swizzle(rb, 2 * g)], b1 = lb[rb * 8 + swizzle(rb, 2 * g + 1)];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            av[i][q] = (int)a0[q]; av[i][q + 4] = (int)a1[q];
-            bv[i][q] = (int)b0[q]; bv[i][q + 4] = (int)b1[q];
-          }
-          const int64_t xr = row0 + min(m * kTile + rb, seg - 1);
-          sb[i] = a.b_scales[xr * (depth / 128) + kb];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // 16 columns of a tile lie in one block of 128 weight rows
-          const int wr = weight_row<GLU>(n, wn * 64 + i * 16, a.cols);
-          const float sa =
-              a.a_scales[((int64_t)e * (a.Nz / 128) + wr / 128) * (depth / 128) + kb];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                av[i], bv[j], f32x4{0, 0, 0, 0}, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(p[q], sa * sb[j], acc[i][j][q]);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          bf16x8 av[4], bv[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int ra = wn * 64 + i * 16 + r16, rb = wm * 64 + i * 16 + r16;
-            av[i] = __builtin_bit_cast(bf16x8, la[ra * 8 + swizzle(ra, s * 4 + g)]);
-            bv[i] = __builtin_bit_cast(bf16x8, lb[rb * 8 + swizzle(rb, s * 4 + g)]);
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[i], bv[j], acc[i][j], 0, 0, 0);
-        }
+        pa[i] = a.a + (a0 + weight_row<GLU, BN>(n, c * 8 + (lane >> 3), a.cols)) * lda + du * 16;
       }
     }
+#pragma unroll
+    for (int i = 0; i < RB; ++i) {
+      const int c = i * T::WAVES + wave;
+      if (T::B_TURNED) {
+        const int k = c * (64 / UB) + lane / UB;
+        const int col = min(m * BM + ((lane % UB) ^ turned_swizzle(k)) * 8, a.rows - 8);
+        pb[i] = a.b + (row0 + k) * ldb + col * 2;
+      } else {
+        pb[i] = a.b + (row0 + min(m * BM + c * 8 + (lane >> 3), seg - 1)) * ldb + du * 16;
+      }
+    }
+    const int64_t stepa = T::A_TURNED ? T::VALS * lda : 128;
+    const int64_t stepb = T::B_TURNED ? T::VALS * ldb : 128;
+
+    f32x4 acc[TN][TM];
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+    auto load = [&](unsigned char* la, unsigned char* lb) {
+#pragma unroll
+      for (int i = 0; i < RA; ++i) {
+        load_to_lds(pa[i], la + (i * T::WAVES + wave) * 1024);
+        pa[i] += stepa;
+      }
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        load_to_lds(pb[i], lb + (i * T::WAVES + wave) * 1024);
+        pb[i] += stepb;
+      }
+    };
+    // the same through registers, with zeros past the end of the summed index
+    auto load_tail = [&](unsigned char* la, unsigned char* lb, int left) {
+#pragma unroll
+      for (int i = 0; i < RA; ++i) {
+        const int c = i * T::WAVES + wave;
+        const bool in = T::A_TURNED ? c * (64 / UA) + lane / UA < left : du * T::UNIT < left;
+        const u32x4 v = in ? *reinterpret_cast<const u32x4*>(pa[i]) : zero4();
+        *reinterpret_cast<u32x4*>(la + c * 1024 + lane * 16) = v;
+      }
+#pragma unroll
+      for (int i = 0; i < RB; ++i) {
+        const int c = i * T::WAVES + wave;
+        const bool in = T::B_TURNED ? c * (64 / UB) + lane / UB < left : du * T::UNIT < left;
+        const u32x4 v = in ? *reinterpret_cast<const u32x4*>(pb[i]) : zero4();
+        *reinterpret_cast<u32x4*>(lb + c * 1024 + lane * 16) = v;
+      }
+    };
+    const int g = lane >> 4, r16 = lane & 15;
+    int64_t xscale[TM];
+    if (FP8) {
+#pragma unroll
+      for (int j = 0; j < TM; ++j)
+        xscale[j] = (row0 + min(m * BM + (wm * TM + j) * 16 + r16, seg - 1)) * (depth / 128);
+    }
+    auto compute = [&](const unsigned char* la, const unsigned char* lb, int kb) {
+      if (!active) return;
+      if (FP8) {
+        i32x8 bv[TM];
+        float sb[TM];
+#pragma unroll
+        for (int j = 0; j < TM; ++j) {
+          const int r = (wm * TM + j) * 16 + r16;
+          const u32x4 v0 = *reinterpret_cast<const u32x4*>(lb + r * 128 + (((2 * g) ^ (r & 7)) << 4));
+          const u32x4 v1 =
+              *reinterpret_cast<const u32x4*>(lb + r * 128 + (((2 * g + 1) ^ (r & 7)) << 4));
+          bv[j] = __builtin_bit_cast(i32x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+          sb[j] = a.b_scales[xscale[j] + kb];
+        }
+#pragma unroll
+        for (int i = 0; i < TN; ++i) {
+          const int r = (wn * TN + i) * 16 + r16;
+          const u32x4 v0 = *reinterpret_cast<const u32x4*>(la + r * 128 + (((2 * g) ^ (r & 7)) << 4));
+          const u32x4 v1 =
+              *reinterpret_cast<const u32x4*>(la + r * 128 + (((2 * g + 1) ^ (r & 7)) << 4));
+          const i32x8 av =
+              __builtin_bit_cast(i32x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
+          const int wr = weight_row<GLU, BN>(n, (wn * TN + i) * 16, a.cols);
+          const float sa = a.a_scales[((int64_t)e * (a.Nz / 128) + wr / 128) * (depth / 128) + kb];
+#pragma unroll
+          for (int j = 0; j < TM; ++j) {
+            const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                av, bv[j], f32x4{0, 0, 0, 0}, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+            const float sc = sa * sb[j];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(p[q], sc, acc[i][j][q]);
+          }
+        }
+        return;
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        bf16x8 bv[TM], av[TN];
+#pragma unroll
+        for (int j = 0; j < TM; ++j)
+          bv[j] = fragment<T, BM, T::B_TURNED>(lb, (wm * TM + j) * 16, s, lane);
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+          av[i] = fragment<T, BN, T::A_TURNED>(la, (wn * TN + i) * 16, s, lane);
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+          for (int j = 0; j < TM; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[i], bv[j], acc[i][j], 0, 0, 0);
+      }
+    };
+
+    // two buffers: while one is multiplied the next step's loads land in the
+    // other; a step's barrier says that its loads have landed and that the
+    // other buffer has been read
+    const int steps = depth / T::VALS, left = depth % T::VALS;
+    wait_loads_and_sync();
+    if (steps > 0) load(la0, lb0);
+    int k = 0;
+    for (; k + 1 < steps; k += 2) {
+      wait_loads_and_sync();
+      load(la1, lb1);
+      compute(la0, lb0, k);
+      wait_loads_and_sync();
+      if (k + 2 < steps) load(la0, lb0);
+      compute(la1, lb1, k + 1);
+    }
+    if (k < steps) {
+      wait_loads_and_sync();
+      compute(la0, lb0, k);
+    }
+    if (!FP8 && left > 0) {
+      __syncthreads();
+      load_tail(la1, lb1, left);
+      __syncthreads();
+      compute(la1, lb1, 0);
+      __syncthreads();
+    }
+    if (!active) continue;
 
     // a lane has 4 consecutive columns (4 * (lane / 16) of 16) of row lane % 16
-    const int c4 = (lane >> 4) * 4;
+    const int c4 = g * 4;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = m * kTile + wm * 64 + j * 16 + (lane & 15);
-      if (r >= (MODE == kGradW ? a.rows : seg)) continue;
-      const int64_t orow = MODE == kGradW ? (int64_t)e * a.rows + r : row0 + r;
+    for (int j = 0; j < TM; ++j) {
+      const int r = m * BM + (wm * TM + j) * 16 + r16;
+      if (r >= rows) continue;
+      const int64_t orow = MODE == kGradW ? (int64_t)e * rows + r : row0 + r;
 #pragma unroll
-      for (int i = 0; i < 4; i += GLU ? 2 : 1) {
-        const int col = GLU ? n * kCols + (wn * 4 + i) * 8 + c4 : n * kCols + wn * 64 + i * 16 + c4;
+      for (int i = 0; i < TN; i += GLU ? 2 : 1) {
+        const int col = n * T::COLS + (wn * TN + i) * (GLU ? 8 : 16) + c4;
         if (col >= a.cols) continue;
         float v[4];
         if (MODE == kForward) {
@@ -403,31 +500,38 @@ __global__ __launch_bounds__(256) void grad_bias_kernel(LinearBackwardArgs a) {
 
 // ---- launches ---------------------------------------------------------------
 
-constexpr int kBlocks = 1024;  // resident blocks of the tile kernel: 4 on each of 256 CUs
-
-unsigned grid_for(int64_t tiles) {
-  return (unsigned)std::max<int64_t>(1, std::min<int64_t>(tiles, kBlocks));
-}
+constexpr int kCus = 256;
 
 // An upper bound of the row tiles that num_rows rows in E segments make.
-int64_t row_tiles_bound(int64_t num_rows, int E) {
-  return num_rows / kTile + std::min<int64_t>(num_rows, E) + 1;
+int64_t row_tiles_bound(int64_t num_rows, int E, int bm) {
+  return num_rows / bm + std::min<int64_t>(num_rows, E);
+}
+
+// `rows`: rows expected in all segments (forward, grad_x).
+template <Mode MODE, bool FP8, int ACT, int WN, int WM, int TN, int TM>
+void run_tiles(const TileArgs& a, int64_t rows, int per_cu, hipStream_t s) {
+  using T = Tile<MODE, FP8, ACT, WN, WM, TN, TM>;
+  const int64_t cols = (a.cols + T::COLS - 1) / T::COLS;
+  const int64_t tiles = cols * (MODE == kGradW ? (int64_t)a.E * ((a.rows + T::BM - 1) / T::BM)
+                                               : row_tiles_bound(rows, a.E, T::BM));
+  const size_t lds = MODE == kGradW ? 0 : (size_t)(a.E + 1) * sizeof(int32_t);
+  const unsigned grid =
+      (unsigned)std::max<int64_t>(1, std::min<int64_t>(tiles, (int64_t)per_cu * kCus));
+  tile_kernel<MODE, FP8, ACT, WN, WM, TN, TM><<<grid, T::THREADS, lds, s>>>(a);
 }
 
 template <Mode MODE, bool FP8, int ACT>
-void run_tiles(const TileArgs& a, int64_t tiles, hipStream_t s) {
-  const size_t lds = MODE == kGradW ? 0 : (size_t)(a.E + 1) * sizeof(int32_t);
-  tile_kernel<MODE, FP8, ACT><<<grid_for(tiles), kThreads, lds, s>>>(a);
+void run_sized(const TileArgs& a, int64_t rows, hipStream_t s) {
+  run_tiles<MODE, FP8, ACT, 2, 4, 8, 4>(a, rows, 1, s);
 }
 
 template <bool FP8>
-void run_forward(const TileArgs& t, int act, int64_t row_tiles, hipStream_t s) {
-  const int64_t full = row_tiles * ((t.cols + kTile - 1) / kTile);
+void run_forward(const TileArgs& t, int act, int64_t rows, hipStream_t s) {
   switch (act) {
-    case MEP_ACT_NONE: run_tiles<kForward, FP8, MEP_ACT_NONE>(t, full, s); break;
-    case MEP_ACT_GELU: run_tiles<kForward, FP8, MEP_ACT_GELU>(t, full, s); break;
-    case MEP_ACT_SILU: run_tiles<kForward, FP8, MEP_ACT_SILU>(t, full, s); break;
-    default: run_tiles<kForward, FP8, MEP_ACT_SILU_GLU>(t, 2 * full, s);
+    case MEP_ACT_NONE: run_sized<kForward, FP8, MEP_ACT_NONE>(t, rows, s); break;
+    case MEP_ACT_GELU: run_sized<kForward, FP8, MEP_ACT_GELU>(t, rows, s); break;
+    case MEP_ACT_SILU: run_sized<kForward, FP8, MEP_ACT_SILU>(t, rows, s); break;
+    default: run_sized<kForward, FP8, MEP_ACT_SILU_GLU>(t, rows, s);
   }
 }
 
@@ -451,9 +555,9 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
   t.cols = a.N;
   t.depth = a.K;
   t.Nz = a.Nz;
-  const int64_t row_tiles = row_tiles_bound(std::min(a.num_rows, a.cap), a.E);
-  if (a.quant != MEP_QUANT_NONE) run_forward<true>(t, a.act, row_tiles, s);
-  else run_forward<false>(t, a.act, row_tiles, s);
+  const int64_t rows = std::min(a.num_rows, a.cap);
+  if (a.quant != MEP_QUANT_NONE) run_forward<true>(t, a.act, rows, s);
+  else run_forward<false>(t, a.act, rows, s);
   return hipGetLastError();
 }
 
@@ -478,20 +582,17 @@ hipError_t launch_linear_backward(const LinearBackwardArgs& a, hipStream_t s) {
   t.Nz = a.Nz;
   t.b = (const unsigned char*)a.grad_z;
   t.cols = a.K;
-  const int64_t col_tiles = (a.K + kTile - 1) / kTile;
   if (a.grad_x && a.cap > 0) {
     t.a = (const unsigned char*)a.w;
     t.out = (uint16_t*)a.grad_x;
     t.depth = a.Nz;
-    const int64_t row_tiles = row_tiles_bound(std::min(a.num_rows, a.cap), a.E);
-    run_tiles<kGradX, false, MEP_ACT_NONE>(t, row_tiles * col_tiles, s);
+    run_sized<kGradX, false, MEP_ACT_NONE>(t, std::min(a.num_rows, a.cap), s);
   }
   if (a.grad_w) {
     t.a = (const unsigned char*)a.x;
     t.out = (uint16_t*)a.grad_w;
     t.rows = a.Nz;
-    const int64_t row_tiles = (a.Nz + kTile - 1) / kTile;
-    run_tiles<kGradW, false, MEP_ACT_NONE>(t, (int64_t)a.E * row_tiles * col_tiles, s);
+    run_sized<kGradW, false, MEP_ACT_NONE>(t, 0, s);
   }
   return hipGetLastError();
 }

@@ -81,17 +81,31 @@ __device__ __forceinline__ int weight_row(int n, int r, int cols) {
 #define MEP_LDS __attribute__((address_space(3)))
 #define MEP_GLOBAL __attribute__((address_space(1)))
 
-// 16 bytes a lane straight from memory into LDS, lane after lane from `lds` on
-// (the same address for the whole wave).
-__device__ __forceinline__ void load_to_lds(const unsigned char* p, unsigned char* lds) {
-  __builtin_amdgcn_global_load_lds((const MEP_GLOBAL uint32_t*)p, (MEP_LDS uint32_t*)lds, 16, 0, 0);
+// BYTES a lane straight from memory (a base for the wave, an offset for the
+// lane) into LDS, lane after lane from `lds` on.  The empty statement keeps the
+// offset in one register: widened outside the loop it would take two.
+template <int BYTES = 16>
+__device__ __forceinline__ void load_to_lds(const unsigned char* base, uint32_t off,
+                                            unsigned char* lds) {
+  asm volatile("" : "+v"(off));
+  const auto p = (const MEP_GLOBAL uint32_t*)(base + off);
+  static_assert(BYTES == 16 || BYTES == 4, "");
+  if constexpr (BYTES == 16)
+    __builtin_amdgcn_global_load_lds(p, (MEP_LDS uint32_t*)lds, 16, 0, 0);
+  else
+    __builtin_amdgcn_global_load_lds(p, (MEP_LDS uint32_t*)lds, 4, 0, 0);
 }
 
-// All of this wave's loads have landed, then everyone's; nothing moves across.
-__device__ __forceinline__ void wait_loads_and_sync() {
+// Waits (the counters' fields as the ISA lays them out) and a barrier that
+// nothing moves across.
+constexpr int kAllLdsReads = 0xC07F;  // lgkmcnt(0)
+constexpr int loads_left(int n) { return 0x0F70 | (n & 15) | (n >> 4) << 14; }  // vmcnt(n)
+
+__device__ __forceinline__ void phase_end() {
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+  __builtin_amdgcn_sched_barrier(0);
   __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
   asm volatile("" ::: "memory");
 }
 
@@ -110,8 +124,12 @@ struct Tile {
   static constexpr int UNIT = FP8 ? 16 : 8;           // values in 16 bytes
   static constexpr int SIZE = FP8 ? 1 : 2;
   static constexpr int COLS = GLU ? BN / 2 : BN;      // output columns a tile
-  static constexpr int RA = BN / 8 / WAVES;           // loads of 1 KiB a wave and step
-  static constexpr int RB = BM / 8 / WAVES;
+  // loads of 1 KiB a wave and step: of each half of the columns, of each half
+  // of the rows
+  static constexpr int RA = BN / 16 / WAVES, RB = BM / 16 / WAVES;
+  static constexpr int SCALES = FP8 ? BM + (WAVES - BM / 64) * 64 : 0;
+  static_assert(WN == 2 && WAVES == 8 && RA > 0 && RB > 0, "");
+  static_assert(!FP8 || BM < 512, "a wave for each load of scales");
 };
 
 template <class T, int ROWS, bool TURNED>
@@ -136,8 +154,13 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(TileArgs a) {
   using T = Tile<MODE, FP8, ACT, WN, WM, TN, TM>;
   constexpr bool GLU = T::GLU;
   constexpr int BN = T::BN, BM = T::BM, RA = T::RA, RB = T::RB;
-  __shared__ __attribute__((aligned(1024))) unsigned char la0[BN * 128], la1[BN * 128];
-  __shared__ __attribute__((aligned(1024))) unsigned char lb0[BM * 128], lb1[BM * 128];
+  // separate arrays: reads of one wait for none of the loads into another.  A
+  // step's columns come in two halves (of each wave's), then its rows, with the
+  // scales of both behind them.
+  __shared__ __attribute__((aligned(1024))) unsigned char a00[BN * 64], a01[BN * 64];
+  __shared__ __attribute__((aligned(1024))) unsigned char a10[BN * 64], a11[BN * 64];
+  __shared__ __attribute__((aligned(1024))) unsigned char b0[BM * 128 + T::SCALES * 4];
+  __shared__ __attribute__((aligned(1024))) unsigned char b1[BM * 128 + T::SCALES * 4];
   extern __shared__ int32_t first[];         // [E+1]: row tiles before each expert
 
   const int tid = threadIdx.x, lane = tid & 63, wave = first_lane(tid >> 6);
@@ -196,34 +219,50 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(TileArgs a) {
     const int rows = MODE == kGradW ? a.rows : seg;  // output rows of this expert
     const bool active = m * BM + wm * (TM * 16) < rows;
 
-    // where this lane's pieces of the two tiles come from: for a direct operand
-    // 8 rows of 128 bytes a load, for a turned one 1 KiB of whole rows k
-    const unsigned char *pa[RA], *pb[RB];
+    // where this lane's pieces of the two tiles come from, as offsets from
+    // bases that move along: for a direct operand 8 rows of 128 bytes a load,
+    // for a turned one 1 KiB of whole rows k.  A tile spans at most 256 rows of
+    // 2 MiB, so 32 bits hold the offsets.
+    uint32_t oa[2][RA], ob[2 * RB];
     const int64_t lda = (int64_t)(T::A_TURNED ? a.cols : depth) * T::SIZE;
     const int64_t ldb = (int64_t)(T::B_TURNED ? a.rows : depth) * T::SIZE;
-    constexpr int UA = BN / 8, UB = BM / 8;  // 16-byte units in a row of a turned tile
+    constexpr int UA = BN / 16, UB = BM / 8;  // 16-byte units in a row of a turned tile
     const int du = (lane & 7) ^ (lane >> 3);
-    const int64_t a0 = MODE == kGradW ? row0 : (int64_t)e * a.Nz;
+    // gated: a load's 8 rows are all gate rows or all rows they gate, and the
+    // same for all of a wave's loads
+    const int64_t a_row = MODE == kGradW ? row0
+                                         : (int64_t)e * a.Nz + (GLU && (wave & 2) ? a.cols : 0);
+    const int an = T::A_TURNED ? 0 : n * T::COLS;  // first weight row of the tile
+    const unsigned char* base_a = a.a + (a_row + an) * lda + (T::A_TURNED ? n * BN * 2 : 0);
+    const unsigned char* base_b =
+        a.b + (T::B_TURNED ? row0 * ldb + m * BM * 2 : (row0 + m * BM) * ldb);
+    // column r of half h of the tile's columns
+    auto column = [](int h, int r) { return (r / (BN / 4)) * (BN / 2) + h * (BN / 4) + r % (BN / 4); };
 #pragma unroll
-    for (int i = 0; i < RA; ++i) {
-      const int c = i * T::WAVES + wave;
-      if (T::A_TURNED) {
-        const int k = c * (64 / UA) + lane / UA;
-        const int col = min(n * BN + ((lane % UA) ^ turned_swizzle(k)) * 8, a.cols - 8);
-        pa[i] = a.a + (a0 + k) * lda + col * 2;
-      } else {
-        pa[i] = a.a + (a0 + weight_row<GLU, BN>(n, c * 8 + (lane >> 3), a.cols)) * lda + du * 16;
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < RA; ++i) {
+        const int c = i * T::WAVES + wave;
+        if (T::A_TURNED) {
+          const int k = c * (64 / UA) + lane / UA;
+          const int col = column(h, ((lane % UA) ^ turned_swizzle(k)) * 8);
+          oa[h][i] = (uint32_t)(k * lda) + min(col, a.cols - 8 - n * BN) * 2;
+        } else {
+          const int r = column(h, c * 8 + (lane >> 3));
+          const int col = GLU ? (r >> 5) * 16 + (r & 15) : r;
+          oa[h][i] = (uint32_t)(min(col, a.cols - 1 - an) * lda) + du * 16;
+        }
       }
     }
 #pragma unroll
-    for (int i = 0; i < RB; ++i) {
+    for (int i = 0; i < 2 * RB; ++i) {
       const int c = i * T::WAVES + wave;
       if (T::B_TURNED) {
         const int k = c * (64 / UB) + lane / UB;
-        const int col = min(m * BM + ((lane % UB) ^ turned_swizzle(k)) * 8, a.rows - 8);
-        pb[i] = a.b + (row0 + k) * ldb + col * 2;
+        const int u = (lane % UB) ^ turned_swizzle(k);
+        ob[i] = (uint32_t)(k * ldb) + min(u * 8, a.rows - 8 - m * BM) * 2;
       } else {
-        pb[i] = a.b + (row0 + min(m * BM + c * 8 + (lane >> 3), seg - 1)) * ldb + du * 16;
+        ob[i] = (uint32_t)(min(c * 8 + (lane >> 3), seg - 1 - m * BM) * ldb) + du * 16;
       }
     }
     const int64_t stepa = T::A_TURNED ? T::VALS * lda : 128;
@@ -235,118 +274,229 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(TileArgs a) {
 #pragma unroll
       for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-    auto load = [&](unsigned char* la, unsigned char* lb) {
-#pragma unroll
-      for (int i = 0; i < RA; ++i) {
-        load_to_lds(pa[i], la + (i * T::WAVES + wave) * 1024);
-        pa[i] += stepa;
-      }
-#pragma unroll
-      for (int i = 0; i < RB; ++i) {
-        load_to_lds(pb[i], lb + (i * T::WAVES + wave) * 1024);
-        pb[i] += stepb;
-      }
-    };
-    // the same through registers, with zeros past the end of the summed index
-    auto load_tail = [&](unsigned char* la, unsigned char* lb, int left) {
-#pragma unroll
-      for (int i = 0; i < RA; ++i) {
-        const int c = i * T::WAVES + wave;
-        const bool in = T::A_TURNED ? c * (64 / UA) + lane / UA < left : du * T::UNIT < left;
-        const u32x4 v = in ? *reinterpret_cast<const u32x4*>(pa[i]) : zero4();
-        *reinterpret_cast<u32x4*>(la + c * 1024 + lane * 16) = v;
-      }
-#pragma unroll
-      for (int i = 0; i < RB; ++i) {
-        const int c = i * T::WAVES + wave;
-        const bool in = T::B_TURNED ? c * (64 / UB) + lane / UB < left : du * T::UNIT < left;
-        const u32x4 v = in ? *reinterpret_cast<const u32x4*>(pb[i]) : zero4();
-        *reinterpret_cast<u32x4*>(lb + c * 1024 + lane * 16) = v;
-      }
-    };
-    const int g = lane >> 4, r16 = lane & 15;
-    int64_t xscale[TM];
+    // E4M3: this wave's scales of a step, 64 rows of x or every 4th row of the
+    // weight's tile (a copy for each wave that has no rows)
+    const unsigned char* base_s = nullptr;
+    uint32_t os = 0;
     if (FP8) {
-#pragma unroll
-      for (int j = 0; j < TM; ++j)
-        xscale[j] = (row0 + min(m * BM + (wm * TM + j) * 16 + r16, seg - 1)) * (depth / 128);
-    }
-    auto compute = [&](const unsigned char* la, const unsigned char* lb, int kb) {
-      if (!active) return;
-      if (FP8) {
-        i32x8 bv[TM];
-        float sb[TM];
-#pragma unroll
-        for (int j = 0; j < TM; ++j) {
-          const int r = (wm * TM + j) * 16 + r16;
-          const u32x4 v0 = *reinterpret_cast<const u32x4*>(lb + r * 128 + (((2 * g) ^ (r & 7)) << 4));
-          const u32x4 v1 =
-              *reinterpret_cast<const u32x4*>(lb + r * 128 + (((2 * g + 1) ^ (r & 7)) << 4));
-          bv[j] = __builtin_bit_cast(i32x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
-          sb[j] = a.b_scales[xscale[j] + kb];
-        }
-#pragma unroll
-        for (int i = 0; i < TN; ++i) {
-          const int r = (wn * TN + i) * 16 + r16;
-          const u32x4 v0 = *reinterpret_cast<const u32x4*>(la + r * 128 + (((2 * g) ^ (r & 7)) << 4));
-          const u32x4 v1 =
-              *reinterpret_cast<const u32x4*>(la + r * 128 + (((2 * g + 1) ^ (r & 7)) << 4));
-          const i32x8 av =
-              __builtin_bit_cast(i32x8, __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7));
-          const int wr = weight_row<GLU, BN>(n, (wn * TN + i) * 16, a.cols);
-          const float sa = a.a_scales[((int64_t)e * (a.Nz / 128) + wr / 128) * (depth / 128) + kb];
-#pragma unroll
-          for (int j = 0; j < TM; ++j) {
-            const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                av, bv[j], f32x4{0, 0, 0, 0}, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
-            const float sc = sa * sb[j];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(p[q], sc, acc[i][j][q]);
-          }
-        }
-        return;
+      const int blocks = depth / 128;
+      if (wave < BM / 64) {
+        base_s = (const unsigned char*)(a.b_scales + (row0 + m * BM) * blocks);
+        os = (uint32_t)min(wave * 64 + lane, seg - 1 - m * BM) * blocks * 4;
+      } else {
+        const int wr = weight_row<GLU, BN>(n, min(lane * 4, BN - 1), a.cols);
+        base_s = (const unsigned char*)(a.a_scales + (int64_t)e * (a.Nz / 128) * blocks);
+        os = (uint32_t)(wr / 128) * blocks * 4;
       }
+    }
+    auto load_a = [&](unsigned char* la, int h) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        bf16x8 bv[TM], av[TN];
+      for (int i = 0; i < RA; ++i)
+        load_to_lds(base_a, oa[h][i], la + (i * T::WAVES + wave) * 1024);
+      if (h == 1) base_a += stepa;
+    };
+    auto load_b = [&](unsigned char* lb, int h) {
+#pragma unroll
+      for (int i = h * RB; i < (h + 1) * RB; ++i)
+        load_to_lds(base_b, ob[i], lb + (i * T::WAVES + wave) * 1024);
+      if (h == 1) base_b += stepb;
+      if (FP8 && h == 0) {
+        load_to_lds<4>(base_s, os, lb + BM * 128 + wave * 256);
+        base_s += 4;
+      }
+    };
+    // a part of a step through registers, zeros past the end of the summed index
+    auto load_tail = [&](unsigned char* lds, const unsigned char* base, uint32_t off, int c,
+                         bool in) {
+      const u32x4 v = in ? *reinterpret_cast<const u32x4*>(base + off) : zero4();
+      *reinterpret_cast<u32x4*>(lds + c * 1024 + lane * 16) = v;
+    };
+
+    // Operands: a step's rows stay in registers for both halves of the columns.
+    const int g = lane >> 4, r16 = lane & 15;
+    constexpr int HN = TN / 2;            // column fragments of a half
+    constexpr int SUB = FP8 ? 1 : 2;      // MFMAs along a step
+    using Frag = std::conditional_t<FP8, i32x8, bf16x8>;
+    Frag av[HN][SUB], bv[TM][SUB];
+    // E4M3: a wave's columns lie in one block of 128 weight rows (gated: in one
+    // of each half)
+    constexpr int BLOCKS = GLU ? 2 : 1;
+    float scale[BLOCKS][TM];
+    auto read8 = [&](const unsigned char* lds, int at) {
+      const int r = at + r16;
+      const u32x4 lo = *reinterpret_cast<const u32x4*>(lds + r * 128 + (((2 * g) ^ (r & 7)) << 4));
+      const u32x4 hi =
+          *reinterpret_cast<const u32x4*>(lds + r * 128 + (((2 * g + 1) ^ (r & 7)) << 4));
+      return __builtin_bit_cast(i32x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    auto read_b = [&](const unsigned char* lb) {
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        const int at = (wm * TM + j) * 16;
+        if constexpr (FP8) {
+          bv[j][0] = read8(lb, at);
+        } else {
+#pragma unroll
+          for (int s = 0; s < SUB; ++s) bv[j][s] = fragment<T, BM, T::B_TURNED>(lb, at, s, lane);
+        }
+      }
+      if constexpr (FP8) {
+        const float* ls = reinterpret_cast<const float*>(lb + BM * 128);
 #pragma unroll
         for (int j = 0; j < TM; ++j)
-          bv[j] = fragment<T, BM, T::B_TURNED>(lb, (wm * TM + j) * 16, s, lane);
 #pragma unroll
-        for (int i = 0; i < TN; ++i)
-          av[i] = fragment<T, BN, T::A_TURNED>(la, (wn * TN + i) * 16, s, lane);
+          for (int q = 0; q < BLOCKS; ++q)
+            scale[q][j] = ls[BM + (wn * TN + q) * 4] * ls[(wm * TM + j) * 16 + r16];
+      }
+    };
+    auto read_a = [&](const unsigned char* la) {
 #pragma unroll
-        for (int i = 0; i < TN; ++i)
+      for (int i = 0; i < HN; ++i) {
+        const int at = (wn * HN + i) * 16;
+        if constexpr (FP8) {
+          av[i][0] = read8(la, at);
+        } else {
 #pragma unroll
-          for (int j = 0; j < TM; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av[i], bv[j], acc[i][j], 0, 0, 0);
+          for (int s = 0; s < SUB; ++s)
+            av[i][s] = fragment<T, BN / 2, T::A_TURNED>(la, at, s, lane);
+        }
+      }
+    };
+    auto multiply = [&](int half) {
+      if constexpr (FP8) {
+        // a product of 128 is scaled and added while the matrix cores work on
+        // the next
+        f32x4 p[2];
+#pragma unroll
+        for (int q = 0; q < HN * TM + 1; ++q) {
+          if (q < HN * TM)
+            p[q % 2] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                av[q / TM][0], bv[q % TM][0], f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+          if (q >= 1) {
+            const int i = half * HN + (q - 1) / TM, j = (q - 1) % TM;
+            f32x4& c = acc[i][j];
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              c[v] = fmaf(p[(q - 1) % 2][v], scale[i % BLOCKS][j], c[v]);
+            // here and in this order: more products in flight would not fit
+            // the registers
+            asm volatile("" : "+v"(c));
+          }
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < SUB; ++s)
+#pragma unroll
+          for (int i = 0; i < HN; ++i)
+#pragma unroll
+            for (int j = 0; j < TM; ++j)
+              acc[half * HN + i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  av[i][s], bv[j][s], acc[half * HN + i][j], 0, 0, 0);
       }
     };
 
-    // two buffers: while one is multiplied the next step's loads land in the
-    // other; a step's barrier says that its loads have landed and that the
-    // other buffer has been read
+    // Two groups of waves, one of each on every SIMD, take turns: while one
+    // multiplies a half of its columns from registers the other reads its next
+    // operands from LDS; the second group runs one phase behind.  Rows and the
+    // first half of the columns of step k are read in the first phase of four,
+    // the other half in the third, so their places are free for step k + 2 two
+    // phases later: each phase issues a quarter of a step's loads, which have
+    // four to six phases to land.  With t = 4k the time of the first group's
+    // first phase of step k, both groups issue (each in its own phase then)
+    //   t + 2, t + 3: the rows of step k + 2,  t + 4, t + 5: its columns,
+    // and wait at t + 3 for rows and first columns of step k + 1 and at t + 1
+    // for the other columns of step k, leaving what was issued later in flight.
     const int steps = depth / T::VALS, left = depth % T::VALS;
-    wait_loads_and_sync();
-    if (steps > 0) load(la0, lb0);
-    int k = 0;
-    for (; k + 1 < steps; k += 2) {
-      wait_loads_and_sync();
-      load(la1, lb1);
-      compute(la0, lb0, k);
-      wait_loads_and_sync();
-      if (k + 2 < steps) load(la0, lb0);
-      compute(la1, lb1, k + 1);
-    }
-    if (k < steps) {
-      wait_loads_and_sync();
-      compute(la0, lb0, k);
+    constexpr int kRows = 2 * RB + (FP8 ? 1 : 0);  // loads of a step's rows
+    auto run = [&](auto late_, auto active_) {
+      constexpr bool LATE = late_(), ACTIVE = active_();
+      auto step = [&](int k, unsigned char* a_0, unsigned char* a_1, unsigned char* b,
+                      unsigned char* na_0, unsigned char* na_1) {
+        const bool more1 = k + 1 < steps, more2 = k + 2 < steps;
+        auto load_rows = [&](int h) {
+          if (more2) load_b(b, h);
+          else __builtin_amdgcn_s_waitcnt(loads_left(0));  // the last two steps drain
+        };
+        if (ACTIVE) { read_b(b); read_a(a_0); }
+        if (more1) load_a(LATE ? na_1 : na_0, LATE ? 1 : 0);
+        __builtin_amdgcn_s_waitcnt(kAllLdsReads);
+        if (LATE) __builtin_amdgcn_s_waitcnt(loads_left(kRows + 2 * RA));
+        phase_end();
+        if (LATE) load_rows(0);
+        else if (more1) load_a(na_1, 1);
+        __builtin_amdgcn_s_setprio(1);
+        if (ACTIVE) multiply(0);
+        __builtin_amdgcn_s_setprio(0);
+        if (!LATE) __builtin_amdgcn_s_waitcnt(loads_left(kRows + 2 * RA));
+        phase_end();
+        if (ACTIVE) read_a(a_1);
+        load_rows(LATE ? 1 : 0);
+        __builtin_amdgcn_s_waitcnt(kAllLdsReads);
+        if (LATE) __builtin_amdgcn_s_waitcnt(loads_left(kRows + RA));
+        phase_end();
+        if (!LATE) load_rows(1);
+        else if (more2) load_a(a_0, 0);
+        __builtin_amdgcn_s_setprio(1);
+        if (ACTIVE) multiply(1);
+        __builtin_amdgcn_s_setprio(0);
+        if (!LATE) __builtin_amdgcn_s_waitcnt(loads_left(kRows + RA));
+        phase_end();
+      };
+      load_b(b0, 0);
+      load_b(b0, 1);
+      load_a(a00, 0);
+      load_a(a01, 1);
+      if (steps > 1) {
+        load_b(b1, 0);
+        load_b(b1, 1);
+        if (LATE) load_a(a10, 0);
+        __builtin_amdgcn_s_waitcnt(loads_left(kRows + (LATE ? RA : 0)));
+      } else {
+        __builtin_amdgcn_s_waitcnt(loads_left(0));
+      }
+      phase_end();
+      if (LATE) phase_end();
+      for (int k = 0; k < steps; k += 2) {
+        step(k, a00, a01, b0, a10, a11);
+        if (k + 1 < steps) step(k + 1, a10, a11, b1, a00, a01);
+      }
+      if (!LATE) phase_end();
+    };
+    phase_end();  // the last tile's reads are done
+    if (steps > 0) {
+      const bool late = wave >= T::WAVES / 2;
+      using Yes = std::true_type;
+      using No = std::false_type;
+      if (late) {
+        if (active) run(Yes{}, Yes{}); else run(Yes{}, No{});
+      } else {
+        if (active) run(No{}, Yes{}); else run(No{}, No{});
+      }
     }
     if (!FP8 && left > 0) {
+      const auto in_a = [&](int c) {
+        return T::A_TURNED ? c * (64 / UA) + lane / UA < left : du * T::UNIT < left;
+      };
+#pragma unroll
+      for (int i = 0; i < RA; ++i) {
+        const int c = i * T::WAVES + wave;
+        load_tail(a00, base_a, oa[0][i], c, in_a(c));
+        load_tail(a01, base_a, oa[1][i], c, in_a(c));
+      }
+#pragma unroll
+      for (int i = 0; i < 2 * RB; ++i) {
+        const int c = i * T::WAVES + wave;
+        load_tail(b0, base_b, ob[i], c,
+                  T::B_TURNED ? c * (64 / UB) + lane / UB < left : du * T::UNIT < left);
+      }
       __syncthreads();
-      load_tail(la1, lb1, left);
-      __syncthreads();
-      compute(la1, lb1, 0);
+      if (active) {
+        read_b(b0);
+        read_a(a00);
+        multiply(0);
+        read_a(a01);
+        multiply(1);
+      }
       __syncthreads();
     }
     if (!active) continue;

@@ -132,22 +132,56 @@ struct Tile {
   static_assert(!FP8 || BM < 512, "a wave for each load of scales");
 };
 
-template <class T, int ROWS, bool TURNED>
-__device__ __forceinline__ bf16x8 fragment(const unsigned char* lds, int at, int s, int lane) {
-  const int g = lane >> 4, r16 = lane & 15;
-  if (!TURNED) {
-    const int r = at + r16;
-    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(
-                                          lds + r * 128 + (((s * 4 + g) ^ (r & 7)) << 4)));
+// Where a lane reads COUNT fragments of 16 rows from row `at` of a tile of ROWS
+// rows.  Direct: the two units of a step's halves (E4M3: the two halves of a
+// unit pair), the fragments 2 KiB apart.  Turned: a place for each fragment.
+template <int ROWS, bool TURNED, bool FP8, int COUNT>
+struct Reader {
+  static constexpr int N = TURNED ? COUNT : 2;
+  uint32_t off[N];
+
+  __device__ __forceinline__ Reader(int at, int lane) {
+    const int g = lane >> 4, r16 = lane & 15;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (TURNED) {
+        const int k = g * 8 + (r16 >> 2);
+        const int u = ((at + i * 16) >> 3) + ((r16 & 3) >> 1);
+        off[i] = k * (ROWS * 2) + ((u ^ turned_swizzle(k)) << 4) + (r16 & 1) * 8;
+      } else {
+        const int u = FP8 ? 2 * g + i : 4 * i + g;
+        off[i] = (at + r16) * 128 + ((u ^ (r16 & 7)) << 4);
+      }
+    }
   }
-  typedef short s16x4 __attribute__((ext_vector_type(4)));
-  const int k = s * 32 + g * 8 + (r16 >> 2);
-  const int u = ((at >> 3) + ((r16 & 3) >> 1)) ^ turned_swizzle(k);
-  const unsigned char* p = lds + k * (ROWS * 2) + u * 16 + (r16 & 1) * 8;
-  const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MEP_LDS s16x4*)p);
-  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MEP_LDS s16x4*)(p + 4 * ROWS * 2));
-  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-}
+
+  // Called before a phase's reads: without, the sums of these offsets and every
+  // array's address would be kept in registers of their own.
+  __device__ __forceinline__ void refresh() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+v"(off[i]));
+  }
+
+  __device__ __forceinline__ u32x4 unit(const unsigned char* lds, int i, int q) const {
+    return *reinterpret_cast<const u32x4*>(lds + off[q] + i * 2048);
+  }
+
+  // 8 values of the summed index: half s of a step's 64, fragment i.
+  __device__ __forceinline__ bf16x8 bf16(const unsigned char* lds, int i, int s) const {
+    if (!TURNED) return __builtin_bit_cast(bf16x8, unit(lds, i, s));
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    const unsigned char* p = lds + off[TURNED ? i : 0] + s * 32 * (ROWS * 2);
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MEP_LDS s16x4*)p);
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((MEP_LDS s16x4*)(p + 4 * ROWS * 2));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  }
+
+  // 32 E4M3 values.
+  __device__ __forceinline__ i32x8 e4m3(const unsigned char* lds, int i) const {
+    return __builtin_bit_cast(i32x8, __builtin_shufflevector(unit(lds, i, 0), unit(lds, i, 1), 0, 1,
+                                                             2, 3, 4, 5, 6, 7));
+  }
+};
 
 template <Mode MODE, bool FP8, int ACT, int WN, int WM, int TN, int TM>
 __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(TileArgs a) {
@@ -289,20 +323,25 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(TileArgs a) {
         os = (uint32_t)(wr / 128) * blocks * 4;
       }
     }
+    // behind the last step the same is loaded again, so that every step issues as
+    // many loads
+    int left_a = depth / T::VALS, left_b = left_a;
     auto load_a = [&](unsigned char* la, int h) {
 #pragma unroll
       for (int i = 0; i < RA; ++i)
         load_to_lds(base_a, oa[h][i], la + (i * T::WAVES + wave) * 1024);
-      if (h == 1) base_a += stepa;
+      if (h == 1 && --left_a > 0) base_a += stepa;
     };
     auto load_b = [&](unsigned char* lb, int h) {
 #pragma unroll
       for (int i = h * RB; i < (h + 1) * RB; ++i)
         load_to_lds(base_b, ob[i], lb + (i * T::WAVES + wave) * 1024);
-      if (h == 1) base_b += stepb;
+      if (h == 1 && --left_b > 0) {
+        base_b += stepb;
+        if (FP8) base_s += 4;
+      }
       if (FP8 && h == 0) {
         load_to_lds<4>(base_s, os, lb + BM * 128 + wave * 256);
-        base_s += 4;
       }
     };
     // a part of a step through registers, zeros past the end of the summed index
@@ -322,22 +361,17 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(TileArgs a) {
     // of each half)
     constexpr int BLOCKS = GLU ? 2 : 1;
     float scale[BLOCKS][TM];
-    auto read8 = [&](const unsigned char* lds, int at) {
-      const int r = at + r16;
-      const u32x4 lo = *reinterpret_cast<const u32x4*>(lds + r * 128 + (((2 * g) ^ (r & 7)) << 4));
-      const u32x4 hi =
-          *reinterpret_cast<const u32x4*>(lds + r * 128 + (((2 * g + 1) ^ (r & 7)) << 4));
-      return __builtin_bit_cast(i32x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-    };
+    Reader<BN / 2, T::A_TURNED, FP8, HN> reader_a(wn * HN * 16, lane);
+    Reader<BM, T::B_TURNED, FP8, TM> reader_b(wm * TM * 16, lane);
     auto read_b = [&](const unsigned char* lb) {
+      reader_b.refresh();
 #pragma unroll
       for (int j = 0; j < TM; ++j) {
-        const int at = (wm * TM + j) * 16;
         if constexpr (FP8) {
-          bv[j][0] = read8(lb, at);
+          bv[j][0] = reader_b.e4m3(lb, j);
         } else {
 #pragma unroll
-          for (int s = 0; s < SUB; ++s) bv[j][s] = fragment<T, BM, T::B_TURNED>(lb, at, s, lane);
+          for (int s = 0; s < SUB; ++s) bv[j][s] = reader_b.bf16(lb, j, s);
         }
       }
       if constexpr (FP8) {
@@ -350,19 +384,20 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(TileArgs a) {
       }
     };
     auto read_a = [&](const unsigned char* la) {
+      reader_a.refresh();
 #pragma unroll
       for (int i = 0; i < HN; ++i) {
-        const int at = (wn * HN + i) * 16;
         if constexpr (FP8) {
-          av[i][0] = read8(la, at);
+          av[i][0] = reader_a.e4m3(la, i);
         } else {
 #pragma unroll
-          for (int s = 0; s < SUB; ++s)
-            av[i][s] = fragment<T, BN / 2, T::A_TURNED>(la, at, s, lane);
+          for (int s = 0; s < SUB; ++s) av[i][s] = reader_a.bf16(la, i, s);
         }
       }
     };
-    auto multiply = [&](int half) {
+    // `meanwhile` is issued behind the first MFMAs, so that the matrix cores do
+    // not wait for it
+    auto multiply = [&](int half, auto meanwhile) {
       if constexpr (FP8) {
         // a product of 128 is scaled and added while the matrix cores work on
         // the next
@@ -372,6 +407,11 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(TileArgs a) {
           if (q < HN * TM)
             p[q % 2] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                 av[q / TM][0], bv[q % TM][0], f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+          if (q == TM) {
+            __builtin_amdgcn_sched_barrier(0);
+            meanwhile();
+            __builtin_amdgcn_sched_barrier(0);
+          }
           if (q >= 1) {
             const int i = half * HN + (q - 1) / TM, j = (q - 1) % TM;
             f32x4& c = acc[i][j];
@@ -387,11 +427,17 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(TileArgs a) {
 #pragma unroll
         for (int s = 0; s < SUB; ++s)
 #pragma unroll
-          for (int i = 0; i < HN; ++i)
+          for (int i = 0; i < HN; ++i) {
 #pragma unroll
             for (int j = 0; j < TM; ++j)
               acc[half * HN + i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
                   av[i][s], bv[j][s], acc[half * HN + i][j], 0, 0, 0);
+            if (s == 0 && i == 0) {
+              __builtin_amdgcn_sched_barrier(0);
+              meanwhile();
+              __builtin_amdgcn_sched_barrier(0);
+            }
+          }
       }
     };
 
@@ -410,35 +456,32 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(TileArgs a) {
     constexpr int kRows = 2 * RB + (FP8 ? 1 : 0);  // loads of a step's rows
     auto run = [&](auto late_, auto active_) {
       constexpr bool LATE = late_(), ACTIVE = active_();
-      auto step = [&](int k, unsigned char* a_0, unsigned char* a_1, unsigned char* b,
+      auto step = [&](unsigned char* a_0, unsigned char* a_1, unsigned char* b,
                       unsigned char* na_0, unsigned char* na_1) {
-        const bool more1 = k + 1 < steps, more2 = k + 2 < steps;
-        auto load_rows = [&](int h) {
-          if (more2) load_b(b, h);
-          else __builtin_amdgcn_s_waitcnt(loads_left(0));  // the last two steps drain
+        auto multiplying = [&](int half, auto meanwhile) {
+          __builtin_amdgcn_s_setprio(1);
+          if (ACTIVE) multiply(half, meanwhile);
+          else meanwhile();
+          __builtin_amdgcn_s_setprio(0);
         };
         if (ACTIVE) { read_b(b); read_a(a_0); }
-        if (more1) load_a(LATE ? na_1 : na_0, LATE ? 1 : 0);
+        load_a(LATE ? na_1 : na_0, LATE ? 1 : 0);
         __builtin_amdgcn_s_waitcnt(kAllLdsReads);
         if (LATE) __builtin_amdgcn_s_waitcnt(loads_left(kRows + 2 * RA));
         phase_end();
-        if (LATE) load_rows(0);
-        else if (more1) load_a(na_1, 1);
-        __builtin_amdgcn_s_setprio(1);
-        if (ACTIVE) multiply(0);
-        __builtin_amdgcn_s_setprio(0);
+        multiplying(0, [&] {
+          if (LATE) load_b(b, 0); else load_a(na_1, 1);
+        });
         if (!LATE) __builtin_amdgcn_s_waitcnt(loads_left(kRows + 2 * RA));
         phase_end();
         if (ACTIVE) read_a(a_1);
-        load_rows(LATE ? 1 : 0);
+        load_b(b, LATE ? 1 : 0);
         __builtin_amdgcn_s_waitcnt(kAllLdsReads);
         if (LATE) __builtin_amdgcn_s_waitcnt(loads_left(kRows + RA));
         phase_end();
-        if (!LATE) load_rows(1);
-        else if (more2) load_a(a_0, 0);
-        __builtin_amdgcn_s_setprio(1);
-        if (ACTIVE) multiply(1);
-        __builtin_amdgcn_s_setprio(0);
+        multiplying(1, [&] {
+          if (LATE) load_a(a_0, 0); else load_b(b, 1);
+        });
         if (!LATE) __builtin_amdgcn_s_waitcnt(loads_left(kRows + RA));
         phase_end();
       };
@@ -446,20 +489,17 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(TileArgs a) {
       load_b(b0, 1);
       load_a(a00, 0);
       load_a(a01, 1);
-      if (steps > 1) {
-        load_b(b1, 0);
-        load_b(b1, 1);
-        if (LATE) load_a(a10, 0);
-        __builtin_amdgcn_s_waitcnt(loads_left(kRows + (LATE ? RA : 0)));
-      } else {
-        __builtin_amdgcn_s_waitcnt(loads_left(0));
-      }
+      load_b(b1, 0);
+      load_b(b1, 1);
+      if (LATE) load_a(a10, 0);
+      __builtin_amdgcn_s_waitcnt(loads_left(kRows + (LATE ? RA : 0)));
       phase_end();
       if (LATE) phase_end();
-      for (int k = 0; k < steps; k += 2) {
-        step(k, a00, a01, b0, a10, a11);
-        if (k + 1 < steps) step(k + 1, a10, a11, b1, a00, a01);
+      for (int k = steps; k > 1; k -= 2) {
+        step(a00, a01, b0, a10, a11);
+        step(a10, a11, b1, a00, a01);
       }
+      if (steps & 1) step(a00, a01, b0, a10, a11);
       if (!LATE) phase_end();
     };
     phase_end();  // the last tile's reads are done
@@ -473,29 +513,33 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(TileArgs a) {
         if (active) run(No{}, Yes{}); else run(No{}, No{});
       }
     }
+    __builtin_amdgcn_s_waitcnt(loads_left(0));
     if (!FP8 && left > 0) {
+      const unsigned char* tail_a = base_a + (steps > 0 ? stepa : 0);
+      const unsigned char* tail_b = base_b + (steps > 0 ? stepb : 0);
+      phase_end();
       const auto in_a = [&](int c) {
         return T::A_TURNED ? c * (64 / UA) + lane / UA < left : du * T::UNIT < left;
       };
 #pragma unroll
       for (int i = 0; i < RA; ++i) {
         const int c = i * T::WAVES + wave;
-        load_tail(a00, base_a, oa[0][i], c, in_a(c));
-        load_tail(a01, base_a, oa[1][i], c, in_a(c));
+        load_tail(a00, tail_a, oa[0][i], c, in_a(c));
+        load_tail(a01, tail_a, oa[1][i], c, in_a(c));
       }
 #pragma unroll
       for (int i = 0; i < 2 * RB; ++i) {
         const int c = i * T::WAVES + wave;
-        load_tail(b0, base_b, ob[i], c,
+        load_tail(b0, tail_b, ob[i], c,
                   T::B_TURNED ? c * (64 / UB) + lane / UB < left : du * T::UNIT < left);
       }
       __syncthreads();
       if (active) {
         read_b(b0);
         read_a(a00);
-        multiply(0);
+        multiply(0, [] {});
         read_a(a01);
-        multiply(1);
+        multiply(1, [] {});
       }
       __syncthreads();
     }

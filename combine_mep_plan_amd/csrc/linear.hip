@@ -10,7 +10,7 @@
 // (w in grad_x, both in grad_w) are "turned": the hardware's transposing LDS
 // reads give MFMA the values that lie along the summed index.
 //
-// A tile of 256 x 256 outputs takes 64 bf16 (128 E4M3) values of the summed index
+// A tile of 256 x 256 (small problems: 128 x 128) outputs takes 64 bf16 (128 E4M3) values of the summed index
 // a step: 32 KiB of each operand, moved from memory straight into LDS (no
 // registers), in two buffers of each, so that the next step's loads run while
 // this step's 64 MFMAs a wave do.  A step reads (256 + 256) x 128 bytes from
@@ -109,10 +109,14 @@ __device__ __forceinline__ void phase_end() {
   asm volatile("" ::: "memory");
 }
 
-// How the units of a turned tile's row k are exchanged: the four rows that 16
-// lanes of a transposing read touch, and those of the next 16 lanes, fall on
-// eight different 32-byte pieces of the banks.
-__device__ __forceinline__ int turned_swizzle(int k) { return ((k & 3) | ((k >> 1) & 4)) << 1; }
+// How the units of row k of a turned tile of ROWS columns are exchanged: the
+// four rows that 16 lanes of a transposing read touch, and those of the next 16
+// lanes, fall on eight different 32-byte pieces of the 256 bytes of banks (rows
+// of 128 bytes already alternate between the two halves).
+template <int ROWS>
+__device__ __forceinline__ int turned_swizzle(int k) {
+  return ROWS >= 128 ? ((k & 3) | ((k >> 1) & 4)) << 1 : (((k >> 1) & 1) | ((k >> 2) & 2)) << 1;
+}
 
 template <Mode MODE, bool FP8, int ACT, int WN, int WM, int TN, int TM>
 struct Tile {
@@ -147,7 +151,7 @@ struct Reader {
       if (TURNED) {
         const int k = g * 8 + (r16 >> 2);
         const int u = ((at + i * 16) >> 3) + ((r16 & 3) >> 1);
-        off[i] = k * (ROWS * 2) + ((u ^ turned_swizzle(k)) << 4) + (r16 & 1) * 8;
+        off[i] = k * (ROWS * 2) + ((u ^ turned_swizzle<ROWS>(k)) << 4) + (r16 & 1) * 8;
       } else {
         const int u = FP8 ? 2 * g + i : 4 * i + g;
         off[i] = (at + r16) * 128 + ((u ^ (r16 & 7)) << 4);
@@ -183,8 +187,20 @@ struct Reader {
   }
 };
 
-template <Mode MODE, bool FP8, int ACT, int WN, int WM, int TN, int TM>
-__global__ __launch_bounds__(WN * WM * 64) void tile_kernel(TileArgs a) {
+// grad_w is written once and large: it passes L2 by, where the operands stay.
+__device__ __forceinline__ void store16(uint16_t* p, u32x4 v, bool stream) {
+  if (stream) __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
+  else *reinterpret_cast<u32x4*>(p) = v;
+}
+
+// A tile's place: expert, row and column tile, and the segment it lies in.
+struct Place {
+  int e, m, n, seg;
+  int64_t row0;
+};
+
+template <Mode MODE, bool FP8, int ACT, int WN, int WM, int TN, int TM, int PER_CU>
+__global__ __launch_bounds__(WN * WM * 64, 2 * PER_CU) void tile_kernel(TileArgs a) {
   using T = Tile<MODE, FP8, ACT, WN, WM, TN, TM>;
   constexpr bool GLU = T::GLU;
   constexpr int BN = T::BN, BM = T::BM, RA = T::RA, RB = T::RB;
@@ -199,6 +215,8 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(TileArgs a) {
 
   const int tid = threadIdx.x, lane = tid & 63, wave = first_lane(tid >> 6);
   const int wn = wave % WN, wm = wave / WN;
+  const int g = lane >> 4, r16 = lane & 15;
+  const bool late = wave >= T::WAVES / 2;
   const int col_tiles = (a.cols + T::COLS - 1) / T::COLS;
 
   if (MODE != kGradW) {
@@ -224,54 +242,75 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(TileArgs a) {
                                        : (int64_t)first[a.E] * col_tiles;
   // blocks go round the 8 XCDs in turn: give each XCD a run of neighbouring tiles
   const int per = gridDim.x / 8;
-  const int64_t start = gridDim.x % 8 == 0 ? (blockIdx.x % 8) * (int64_t)per + blockIdx.x / 8
-                                           : blockIdx.x;
+  int64_t tile = gridDim.x % 8 == 0 ? (blockIdx.x % 8) * (int64_t)per + blockIdx.x / 8
+                                    : blockIdx.x;
+  if (tile >= tiles) return;
 
-  for (int64_t tile = start; tile < tiles; tile += gridDim.x) {
-    int e, m, n;
+  Place at;
+  auto locate = [&] {
     if (MODE == kGradW) {
       const int per_e = grad_w_tiles * col_tiles;
-      e = (int)(tile / per_e);
+      at.e = (int)(tile / per_e);
       const int q = (int)(tile % per_e);
-      m = q % grad_w_tiles;
-      n = q / grad_w_tiles;
+      // bands of 4 row tiles, column after column: the 32 tiles that an XCD works
+      // on share 4 tiles of dz and 8 of x (1465 -> 1332 us at 2048 tokens, 32
+      // experts, 4096 x 7168)
+      const int band = q / (4 * col_tiles), h = min(4, grad_w_tiles - band * 4);
+      const int r = q - band * (4 * col_tiles);
+      at.m = band * 4 + r % h;
+      at.n = r / h;
     } else {
       int lo = 0, hi = a.E;  // the last expert whose tiles start at or before this one
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if ((int64_t)first[mid] * col_tiles <= tile) lo = mid; else hi = mid;
       }
-      e = first_lane(lo);
-      const int mt = first[e + 1] - first[e];
-      const int q = (int)(tile - (int64_t)first[e] * col_tiles);
-      m = first_lane(q % mt);
-      n = first_lane(q / mt);
+      at.e = first_lane(lo);
+      const int mt = first[at.e + 1] - first[at.e];
+      const int q = (int)(tile - (int64_t)first[at.e] * col_tiles);
+      at.m = first_lane(q % mt);
+      at.n = first_lane(q / mt);
     }
-    const int seg = segment_rows(a, e);
-    const int64_t row0 = a.offsets[e];
-    const int depth = MODE == kGradW ? seg : a.depth;
-    const int rows = MODE == kGradW ? a.rows : seg;  // output rows of this expert
-    const bool active = m * BM + wm * (TM * 16) < rows;
+    at.seg = segment_rows(a, at.e);
+    at.row0 = a.offsets[at.e];
+  };
 
-    // where this lane's pieces of the two tiles come from, as offsets from
-    // bases that move along: for a direct operand 8 rows of 128 bytes a load,
-    // for a turned one 1 KiB of whole rows k.  A tile spans at most 256 rows of
-    // 2 MiB, so 32 bits hold the offsets.
-    uint32_t oa[2][RA], ob[2 * RB];
+  // Where this lane's pieces of the two tiles come from, as offsets from bases
+  // that move along: for a direct operand 8 rows of 128 bytes a load, for a
+  // turned one 1 KiB of whole rows k.  A tile spans at most 256 rows of 2 MiB,
+  // so 32 bits hold the offsets.  Rows and columns past the end repeat the last.
+  uint32_t oa[2][RA], ob[2 * RB], os = 0;
+  const unsigned char *base_a, *base_b, *base_s = nullptr;
+  int64_t stepa, stepb;
+  int steps, left;    // whole steps; what is left of the summed index behind them
+  constexpr int UA = BN / 16, UB = BM / 8;  // 16-byte units in a row of a turned tile
+  const int du = (lane & 7) ^ (lane >> 3);
+  auto setup = [&] {
+    const int depth = MODE == kGradW ? at.seg : a.depth;
+    steps = depth / T::VALS;
+    left = depth % T::VALS;
+    // grad_w: where the rows behind the segment exist, the last step takes them
+    // too and leaves them out of its products
+    if (MODE == kGradW && left > 0 && at.row0 + (steps + 1) * T::VALS <= a.cap) {
+      ++steps;
+      left -= T::VALS;
+    }
     const int64_t lda = (int64_t)(T::A_TURNED ? a.cols : depth) * T::SIZE;
     const int64_t ldb = (int64_t)(T::B_TURNED ? a.rows : depth) * T::SIZE;
-    constexpr int UA = BN / 16, UB = BM / 8;  // 16-byte units in a row of a turned tile
-    const int du = (lane & 7) ^ (lane >> 3);
+    stepa = T::A_TURNED ? T::VALS * lda : 128;
+    stepb = T::B_TURNED ? T::VALS * ldb : 128;
     // gated: a load's 8 rows are all gate rows or all rows they gate, and the
     // same for all of a wave's loads
-    const int64_t a_row = MODE == kGradW ? row0
-                                         : (int64_t)e * a.Nz + (GLU && (wave & 2) ? a.cols : 0);
-    const int an = T::A_TURNED ? 0 : n * T::COLS;  // first weight row of the tile
-    const unsigned char* base_a = a.a + (a_row + an) * lda + (T::A_TURNED ? n * BN * 2 : 0);
-    const unsigned char* base_b =
-        a.b + (T::B_TURNED ? row0 * ldb + m * BM * 2 : (row0 + m * BM) * ldb);
+    const int64_t a_row = MODE == kGradW
+                              ? at.row0
+                              : (int64_t)at.e * a.Nz + (GLU && (wave & 2) ? a.cols : 0);
+    const int an = T::A_TURNED ? 0 : at.n * T::COLS;  // first weight row of the tile
+    base_a = a.a + (a_row + an) * lda + (T::A_TURNED ? at.n * BN * 2 : 0);
+    base_b = a.b + (T::B_TURNED ? at.row0 * ldb + at.m * BM * 2 : (at.row0 + at.m * BM) * ldb);
     // column r of half h of the tile's columns
-    auto column = [](int h, int r) { return (r / (BN / 4)) * (BN / 2) + h * (BN / 4) + r % (BN / 4); };
+    auto column = [](int h, int r) {
+      return (r / (BN / 4)) * (BN / 2) + h * (BN / 4) + r % (BN / 4);
+    };
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -279,8 +318,8 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(TileArgs a) {
         const int c = i * T::WAVES + wave;
         if (T::A_TURNED) {
           const int k = c * (64 / UA) + lane / UA;
-          const int col = column(h, ((lane % UA) ^ turned_swizzle(k)) * 8);
-          oa[h][i] = (uint32_t)(k * lda) + min(col, a.cols - 8 - n * BN) * 2;
+          const int col = column(h, ((lane % UA) ^ turned_swizzle<BN / 2>(k)) * 8);
+          oa[h][i] = (uint32_t)(k * lda) + min(col, a.cols - 8 - at.n * BN) * 2;
         } else {
           const int r = column(h, c * 8 + (lane >> 3));
           const int col = GLU ? (r >> 5) * 16 + (r & 15) : r;
@@ -293,218 +332,326 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(TileArgs a) {
       const int c = i * T::WAVES + wave;
       if (T::B_TURNED) {
         const int k = c * (64 / UB) + lane / UB;
-        const int u = (lane % UB) ^ turned_swizzle(k);
-        ob[i] = (uint32_t)(k * ldb) + min(u * 8, a.rows - 8 - m * BM) * 2;
+        const int u = (lane % UB) ^ turned_swizzle<BM>(k);
+        ob[i] = (uint32_t)(k * ldb) + min(u * 8, a.rows - 8 - at.m * BM) * 2;
       } else {
-        ob[i] = (uint32_t)(min(c * 8 + (lane >> 3), seg - 1 - m * BM) * ldb) + du * 16;
+        ob[i] = (uint32_t)(min(c * 8 + (lane >> 3), at.seg - 1 - at.m * BM) * ldb) + du * 16;
       }
     }
-    const int64_t stepa = T::A_TURNED ? T::VALS * lda : 128;
-    const int64_t stepb = T::B_TURNED ? T::VALS * ldb : 128;
-
-    f32x4 acc[TN][TM];
-#pragma unroll
-    for (int i = 0; i < TN; ++i)
-#pragma unroll
-      for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-
-    // E4M3: this wave's scales of a step, 64 rows of x or every 4th row of the
-    // weight's tile (a copy for each wave that has no rows)
-    const unsigned char* base_s = nullptr;
-    uint32_t os = 0;
     if (FP8) {
+      // this wave's scales of a step: 64 rows of x, or every 4th row of the
+      // weight's tile (a copy for each wave that has no rows)
       const int blocks = depth / 128;
       if (wave < BM / 64) {
-        base_s = (const unsigned char*)(a.b_scales + (row0 + m * BM) * blocks);
-        os = (uint32_t)min(wave * 64 + lane, seg - 1 - m * BM) * blocks * 4;
+        base_s = (const unsigned char*)(a.b_scales + (at.row0 + at.m * BM) * blocks);
+        os = (uint32_t)min(wave * 64 + lane, at.seg - 1 - at.m * BM) * blocks * 4;
       } else {
-        const int wr = weight_row<GLU, BN>(n, min(lane * 4, BN - 1), a.cols);
-        base_s = (const unsigned char*)(a.a_scales + (int64_t)e * (a.Nz / 128) * blocks);
+        const int wr = weight_row<GLU, BN>(at.n, min(lane * 4, BN - 1), a.cols);
+        base_s = (const unsigned char*)(a.a_scales + (int64_t)at.e * (a.Nz / 128) * blocks);
         os = (uint32_t)(wr / 128) * blocks * 4;
       }
     }
-    // behind the last step the same is loaded again, so that every step issues as
-    // many loads
-    int left_a = depth / T::VALS, left_b = left_a;
-    auto load_a = [&](unsigned char* la, int h) {
+  };
+  auto load_a = [&](unsigned char* la, int h) {
 #pragma unroll
-      for (int i = 0; i < RA; ++i)
-        load_to_lds(base_a, oa[h][i], la + (i * T::WAVES + wave) * 1024);
-      if (h == 1 && --left_a > 0) base_a += stepa;
-    };
-    auto load_b = [&](unsigned char* lb, int h) {
+    for (int i = 0; i < RA; ++i)
+      load_to_lds(base_a, oa[h][i], la + (i * T::WAVES + wave) * 1024);
+    if (h == 1) base_a += stepa;
+  };
+  auto load_b = [&](unsigned char* lb, int h) {
 #pragma unroll
-      for (int i = h * RB; i < (h + 1) * RB; ++i)
-        load_to_lds(base_b, ob[i], lb + (i * T::WAVES + wave) * 1024);
-      if (h == 1 && --left_b > 0) {
-        base_b += stepb;
-        if (FP8) base_s += 4;
-      }
-      if (FP8 && h == 0) {
-        load_to_lds<4>(base_s, os, lb + BM * 128 + wave * 256);
-      }
-    };
-    // a part of a step through registers, zeros past the end of the summed index
-    auto load_tail = [&](unsigned char* lds, const unsigned char* base, uint32_t off, int c,
-                         bool in) {
-      const u32x4 v = in ? *reinterpret_cast<const u32x4*>(base + off) : zero4();
-      *reinterpret_cast<u32x4*>(lds + c * 1024 + lane * 16) = v;
-    };
-
-    // Operands: a step's rows stay in registers for both halves of the columns.
-    const int g = lane >> 4, r16 = lane & 15;
-    constexpr int HN = TN / 2;            // column fragments of a half
-    constexpr int SUB = FP8 ? 1 : 2;      // MFMAs along a step
-    using Frag = std::conditional_t<FP8, i32x8, bf16x8>;
-    Frag av[HN][SUB], bv[TM][SUB];
-    // E4M3: a wave's columns lie in one block of 128 weight rows (gated: in one
-    // of each half)
-    constexpr int BLOCKS = GLU ? 2 : 1;
-    float scale[BLOCKS][TM];
-    Reader<BN / 2, T::A_TURNED, FP8, HN> reader_a(wn * HN * 16, lane);
-    Reader<BM, T::B_TURNED, FP8, TM> reader_b(wm * TM * 16, lane);
-    auto read_b = [&](const unsigned char* lb) {
-      reader_b.refresh();
-#pragma unroll
-      for (int j = 0; j < TM; ++j) {
-        if constexpr (FP8) {
-          bv[j][0] = reader_b.e4m3(lb, j);
-        } else {
-#pragma unroll
-          for (int s = 0; s < SUB; ++s) bv[j][s] = reader_b.bf16(lb, j, s);
-        }
-      }
-      if constexpr (FP8) {
-        const float* ls = reinterpret_cast<const float*>(lb + BM * 128);
-#pragma unroll
-        for (int j = 0; j < TM; ++j)
-#pragma unroll
-          for (int q = 0; q < BLOCKS; ++q)
-            scale[q][j] = ls[BM + (wn * TN + q) * 4] * ls[(wm * TM + j) * 16 + r16];
-      }
-    };
-    auto read_a = [&](const unsigned char* la) {
-      reader_a.refresh();
-#pragma unroll
-      for (int i = 0; i < HN; ++i) {
-        if constexpr (FP8) {
-          av[i][0] = reader_a.e4m3(la, i);
-        } else {
-#pragma unroll
-          for (int s = 0; s < SUB; ++s) av[i][s] = reader_a.bf16(la, i, s);
-        }
-      }
-    };
-    // `meanwhile` is issued behind the first MFMAs, so that the matrix cores do
-    // not wait for it
-    auto multiply = [&](int half, auto meanwhile) {
-      if constexpr (FP8) {
-        // a product of 128 is scaled and added while the matrix cores work on
-        // the next
-        f32x4 p[2];
-#pragma unroll
-        for (int q = 0; q < HN * TM + 1; ++q) {
-          if (q < HN * TM)
-            p[q % 2] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                av[q / TM][0], bv[q % TM][0], f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
-          if (q == TM) {
-            __builtin_amdgcn_sched_barrier(0);
-            meanwhile();
-            __builtin_amdgcn_sched_barrier(0);
-          }
-          if (q >= 1) {
-            const int i = half * HN + (q - 1) / TM, j = (q - 1) % TM;
-            f32x4& c = acc[i][j];
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-              c[v] = fmaf(p[(q - 1) % 2][v], scale[i % BLOCKS][j], c[v]);
-            // here and in this order: more products in flight would not fit
-            // the registers
-            asm volatile("" : "+v"(c));
-          }
-        }
-      } else {
-#pragma unroll
-        for (int s = 0; s < SUB; ++s)
-#pragma unroll
-          for (int i = 0; i < HN; ++i) {
-#pragma unroll
-            for (int j = 0; j < TM; ++j)
-              acc[half * HN + i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                  av[i][s], bv[j][s], acc[half * HN + i][j], 0, 0, 0);
-            if (s == 0 && i == 0) {
-              __builtin_amdgcn_sched_barrier(0);
-              meanwhile();
-              __builtin_amdgcn_sched_barrier(0);
-            }
-          }
-      }
-    };
-
-    // Two groups of waves, one of each on every SIMD, take turns: while one
-    // multiplies a half of its columns from registers the other reads its next
-    // operands from LDS; the second group runs one phase behind.  Rows and the
-    // first half of the columns of step k are read in the first phase of four,
-    // the other half in the third, so their places are free for step k + 2 two
-    // phases later: each phase issues a quarter of a step's loads, which have
-    // four to six phases to land.  With t = 4k the time of the first group's
-    // first phase of step k, both groups issue (each in its own phase then)
-    //   t + 2, t + 3: the rows of step k + 2,  t + 4, t + 5: its columns,
-    // and wait at t + 3 for rows and first columns of step k + 1 and at t + 1
-    // for the other columns of step k, leaving what was issued later in flight.
-    const int steps = depth / T::VALS, left = depth % T::VALS;
-    constexpr int kRows = 2 * RB + (FP8 ? 1 : 0);  // loads of a step's rows
-    auto run = [&](auto late_, auto active_) {
-      constexpr bool LATE = late_(), ACTIVE = active_();
-      auto step = [&](unsigned char* a_0, unsigned char* a_1, unsigned char* b,
-                      unsigned char* na_0, unsigned char* na_1) {
-        auto multiplying = [&](int half, auto meanwhile) {
-          __builtin_amdgcn_s_setprio(1);
-          if (ACTIVE) multiply(half, meanwhile);
-          else meanwhile();
-          __builtin_amdgcn_s_setprio(0);
-        };
-        if (ACTIVE) { read_b(b); read_a(a_0); }
-        load_a(LATE ? na_1 : na_0, LATE ? 1 : 0);
-        __builtin_amdgcn_s_waitcnt(kAllLdsReads);
-        if (LATE) __builtin_amdgcn_s_waitcnt(loads_left(kRows + 2 * RA));
-        phase_end();
-        multiplying(0, [&] {
-          if (LATE) load_b(b, 0); else load_a(na_1, 1);
-        });
-        if (!LATE) __builtin_amdgcn_s_waitcnt(loads_left(kRows + 2 * RA));
-        phase_end();
-        if (ACTIVE) read_a(a_1);
-        load_b(b, LATE ? 1 : 0);
-        __builtin_amdgcn_s_waitcnt(kAllLdsReads);
-        if (LATE) __builtin_amdgcn_s_waitcnt(loads_left(kRows + RA));
-        phase_end();
-        multiplying(1, [&] {
-          if (LATE) load_a(a_0, 0); else load_b(b, 1);
-        });
-        if (!LATE) __builtin_amdgcn_s_waitcnt(loads_left(kRows + RA));
-        phase_end();
-      };
+    for (int i = h * RB; i < (h + 1) * RB; ++i)
+      load_to_lds(base_b, ob[i], lb + (i * T::WAVES + wave) * 1024);
+    if (FP8 && h == 0) {
+      load_to_lds<4>(base_s, os, lb + BM * 128 + wave * 256);
+      base_s += 4;
+    }
+    if (h == 1) base_b += stepb;
+  };
+  constexpr int kRows = 2 * RB + (FP8 ? 1 : 0);  // loads of a step's rows
+  // a tile's loads before its first phase
+  auto prologue = [&] {
+    if (steps > 0) {
       load_b(b0, 0);
       load_b(b0, 1);
       load_a(a00, 0);
       load_a(a01, 1);
+    }
+    if (steps > 1) {
       load_b(b1, 0);
       load_b(b1, 1);
-      if (LATE) load_a(a10, 0);
-      __builtin_amdgcn_s_waitcnt(loads_left(kRows + (LATE ? RA : 0)));
-      phase_end();
-      if (LATE) phase_end();
-      for (int k = steps; k > 1; k -= 2) {
-        step(a00, a01, b0, a10, a11);
-        step(a10, a11, b1, a00, a01);
+      if (late) load_a(a10, 0);
+    }
+  };
+  // a part of a step through registers, zeros past the end of the summed index
+  auto load_tail = [&](unsigned char* lds, const unsigned char* base, uint32_t off, int c,
+                       bool in) {
+    const u32x4 v = in ? *reinterpret_cast<const u32x4*>(base + off) : zero4();
+    *reinterpret_cast<u32x4*>(lds + c * 1024 + lane * 16) = v;
+  };
+
+  // Operands: a step's rows stay in registers for both halves of the columns.
+  constexpr int HN = TN / 2;            // column fragments of a half
+  constexpr int SUB = FP8 ? 1 : 2;      // MFMAs along a step
+  using Frag = std::conditional_t<FP8, i32x8, bf16x8>;
+  f32x4 acc[TN][TM];
+  Frag av[HN][SUB], bv[TM][SUB];
+  // E4M3: a wave's columns lie in one block of 128 weight rows (gated: in one
+  // of each half)
+  constexpr int BLOCKS = GLU ? 2 : 1;
+  float scale[BLOCKS][TM];
+  Reader<BN / 2, T::A_TURNED, FP8, HN> reader_a(wn * HN * 16, lane);
+  Reader<BM, T::B_TURNED, FP8, TM> reader_b(wm * TM * 16, lane);
+  auto read_b = [&](const unsigned char* lb) {
+    reader_b.refresh();
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+      if constexpr (FP8) {
+        bv[j][0] = reader_b.e4m3(lb, j);
+      } else {
+#pragma unroll
+        for (int s = 0; s < SUB; ++s) bv[j][s] = reader_b.bf16(lb, j, s);
       }
-      if (steps & 1) step(a00, a01, b0, a10, a11);
-      if (!LATE) phase_end();
+    }
+    if constexpr (FP8) {
+      const float* ls = reinterpret_cast<const float*>(lb + BM * 128);
+#pragma unroll
+      for (int j = 0; j < TM; ++j)
+#pragma unroll
+        for (int q = 0; q < BLOCKS; ++q)
+          scale[q][j] = ls[BM + (wn * TN + q) * 4] * ls[(wm * TM + j) * 16 + r16];
+    }
+  };
+  auto read_a = [&](const unsigned char* la) {
+    reader_a.refresh();
+#pragma unroll
+    for (int i = 0; i < HN; ++i) {
+      if constexpr (FP8) {
+        av[i][0] = reader_a.e4m3(la, i);
+      } else {
+#pragma unroll
+        for (int s = 0; s < SUB; ++s) av[i][s] = reader_a.bf16(la, i, s);
+      }
+    }
+  };
+  // zeros for the values from `valid` of the step's 64 on: what lies there may
+  // be anything, infinities included
+  auto mask_values = [&](auto& frags, int valid) {
+    if constexpr (!FP8) {
+#pragma unroll
+      for (int s = 0; s < SUB; ++s) {
+        const int v = valid - s * 32 - g * 8;
+        u32x4 mask;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+          mask[d] = v >= 2 * d + 2 ? 0xffffffffu : v == 2 * d + 1 ? 0xffffu : 0u;
+#pragma unroll
+        for (auto& f : frags)
+          f[s] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, f[s]) & mask);
+      }
+    }
+  };
+  // `meanwhile` is issued behind the first MFMAs, so that the matrix cores do
+  // not wait for it
+  auto multiply = [&](int half, auto meanwhile) {
+    if constexpr (FP8) {
+      // a product of 128 is scaled and added while the matrix cores work on
+      // the next
+      f32x4 p[2];
+#pragma unroll
+      for (int q = 0; q < HN * TM + 1; ++q) {
+        if (q < HN * TM)
+          p[q % 2] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              av[q / TM][0], bv[q % TM][0], f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+        if (q == TM) {
+          __builtin_amdgcn_sched_barrier(0);
+          meanwhile();
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (q >= 1) {
+          const int i = half * HN + (q - 1) / TM, j = (q - 1) % TM;
+          f32x4& c = acc[i][j];
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            c[v] = fmaf(p[(q - 1) % 2][v], scale[i % BLOCKS][j], c[v]);
+          // here and in this order: more products in flight would not fit
+          // the registers
+          asm volatile("" : "+v"(c));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int s = 0; s < SUB; ++s)
+#pragma unroll
+        for (int i = 0; i < HN; ++i) {
+#pragma unroll
+          for (int j = 0; j < TM; ++j)
+            acc[half * HN + i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                av[i][s], bv[j][s], acc[half * HN + i][j], 0, 0, 0);
+          if (s == 0 && i == 0) {
+            __builtin_amdgcn_sched_barrier(0);
+            meanwhile();
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+    }
+  };
+
+  // Two groups of waves, one of each on every SIMD, take turns: while one
+  // multiplies a half of its columns from registers the other reads its next
+  // operands from LDS; the second group runs one phase behind.  Rows and the
+  // first half of the columns of step k are read in the first phase of four,
+  // the other half in the third, so their places are free for step k + 2 two
+  // phases later: each phase issues a quarter of a step's loads, which have
+  // four to six phases to land.  With t = 4k the time of the first group's
+  // first phase of step k, both groups issue (each in its own phase then)
+  //   t + 2, t + 3: the rows of step k + 2,  t + 4, t + 5: its columns,
+  // and wait at t + 3 for rows and first columns of step k + 1 and at t + 1
+  // for the other columns of step k, leaving what was issued later in flight.
+  // DRAIN: the last steps, `togo` of them behind this one, where the loads end.
+  auto run = [&](auto late_, auto active_) {
+    constexpr bool LATE = late_(), ACTIVE = active_();
+    auto step = [&](auto drain_, int togo, unsigned char* a_0, unsigned char* a_1,
+                    unsigned char* b, unsigned char* na_0, unsigned char* na_1) {
+      constexpr bool DRAIN = drain_();
+      const bool more1 = !DRAIN || togo >= 1, more2 = !DRAIN || togo >= 2;
+      const bool mask = MODE == kGradW && DRAIN && togo == 0 && left < 0;
+      auto multiplying = [&](int half, auto meanwhile) {
+        __builtin_amdgcn_s_setprio(1);
+        if (ACTIVE) multiply(half, meanwhile);
+        else meanwhile();
+        __builtin_amdgcn_s_setprio(0);
+      };
+      auto wait_second = [&] {
+        if (more1) __builtin_amdgcn_s_waitcnt(loads_left(kRows + 2 * RA));
+        else __builtin_amdgcn_s_waitcnt(loads_left(0));
+      };
+      auto wait_first = [&] {
+        if (more2) __builtin_amdgcn_s_waitcnt(loads_left(kRows + RA));
+        else __builtin_amdgcn_s_waitcnt(loads_left(RA));
+      };
+      if (ACTIVE) { read_b(b); read_a(a_0); }
+      if (more1) load_a(LATE ? na_1 : na_0, LATE ? 1 : 0);
+      __builtin_amdgcn_s_waitcnt(kAllLdsReads);
+      if (ACTIVE && mask) { mask_values(bv, left + T::VALS); mask_values(av, left + T::VALS); }
+      if (LATE) wait_second();
+      phase_end();
+      multiplying(0, [&] {
+        if (LATE) { if (more2) load_b(b, 0); }
+        else if (more1) load_a(na_1, 1);
+      });
+      if (!LATE) wait_second();
+      phase_end();
+      if (ACTIVE) read_a(a_1);
+      if (more2) load_b(b, LATE ? 1 : 0);
+      __builtin_amdgcn_s_waitcnt(kAllLdsReads);
+      if (ACTIVE && mask) mask_values(av, left + T::VALS);
+      if (LATE) wait_first();
+      phase_end();
+      multiplying(1, [&] {
+        if (more2) { if (LATE) load_a(a_0, 0); else load_b(b, 1); }
+      });
+      if (!LATE) wait_first();
+      phase_end();
     };
-    phase_end();  // the last tile's reads are done
+    using Yes = std::true_type;
+    using No = std::false_type;
+    if (LATE) phase_end();
+    int togo = steps - 1;
+    for (; togo > 2; togo -= 2) {
+      step(No{}, togo, a00, a01, b0, a10, a11);
+      step(No{}, togo - 1, a10, a11, b1, a00, a01);
+    }
+    while (true) {
+      step(Yes{}, togo, a00, a01, b0, a10, a11);
+      if (--togo < 0) break;
+      step(Yes{}, togo, a10, a11, b1, a00, a01);
+      if (--togo < 0) break;
+    }
+    if (!LATE) phase_end();
+  };
+
+  // A tile's rows and columns in place: activation and what goes with it, and
+  // the stores.  A lane has 4 consecutive columns of row r16 in each fragment;
+  // two fragments exchange rows of 16 lanes so that it stores 8 of one.
+  auto finish = [&](const Place& at) {
+    const int rows = MODE == kGradW ? a.rows : at.seg;
+    const int64_t out0 = MODE == kGradW ? (int64_t)at.e * rows : at.row0;
+#pragma unroll
+    for (int i = 0; i < TN; i += GLU ? 4 : 2) {
+      const int col = at.n * T::COLS + (wn * TN + i) * (GLU ? 8 : 16);
+      // bias of the two output fragments (gated: of both halves of each)
+      f32x4 bias[2][GLU ? 2 : 1];
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int h = 0; h < (GLU ? 2 : 1); ++h) {
+          bias[f][h] = f32x4{0, 0, 0, 0};
+          const int c = col + f * 16 + g * 4;
+          if (MODE == kForward && a.bias && c < a.cols)
+            bias[f][h] = *reinterpret_cast<const f32x4*>(a.bias + (int64_t)at.e * a.Nz +
+                                                         h * a.cols + c);
+        }
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        const int r = at.m * BM + (wm * TM + j) * 16 + r16;
+        const bool in = r < rows;
+        const int64_t row = out0 + r;
+        u32x2 y[2], zv[2][GLU ? 2 : 1];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          f32x4 v = acc[i + (GLU ? 2 * f : f)][j];
+          if (MODE == kForward) {
+            v += bias[f][0];
+            f32x4 up = f32x4{0, 0, 0, 0};
+            if (GLU) up = acc[i + (GLU ? 2 * f + 1 : 0)][j] + bias[f][GLU ? 1 : 0];
+            zv[f][0] = u32x2{pack_bf16_rne(v[0], v[1]), pack_bf16_rne(v[2], v[3])};
+            if (GLU) zv[f][GLU ? 1 : 0] = u32x2{pack_bf16_rne(up[0], up[1]), pack_bf16_rne(up[2], up[3])};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              v[q] = ACT == MEP_ACT_GELU   ? gelu(v[q])
+                     : ACT == MEP_ACT_SILU ? silu(v[q])
+                     : GLU                 ? silu(v[q]) * up[q]
+                                           : v[q];
+            const int c = col + f * 16 + g * 4;
+            if (a.residual && in && c < a.cols) {
+              const u32x2 res = *reinterpret_cast<const u32x2*>(a.residual + row * a.cols + c);
+              v[0] += bf16_lo(res[0]); v[1] += bf16_hi(res[0]);
+              v[2] += bf16_lo(res[1]); v[3] += bf16_hi(res[1]);
+            }
+          }
+          y[f] = u32x2{pack_bf16_rne(v[0], v[1]), pack_bf16_rne(v[2], v[3])};
+        }
+        auto put = [&](uint16_t* p, int ld, int at_col, int end, u32x2 x0, u32x2 x1) {
+          const auto lo = __builtin_amdgcn_permlane16_swap(x0[0], x1[0], false, false);
+          const auto hi = __builtin_amdgcn_permlane16_swap(x0[1], x1[1], false, false);
+          const int c = (g & 1) * 16 + (g >> 1) * 8;
+          if (in && at_col + c < end)
+            store16(p + row * ld + at_col + c, u32x4{lo[0], hi[0], lo[1], hi[1]},
+                    MODE == kGradW);
+        };
+        if (MODE == kForward && a.z) {
+          put(a.z, a.Nz, col, a.cols, zv[0][0], zv[1][0]);
+          if (GLU) put(a.z, a.Nz, a.cols + col, 2 * a.cols, zv[0][GLU ? 1 : 0], zv[1][GLU ? 1 : 0]);
+        }
+        put(a.out, a.cols, col, a.cols, y[0], y[1]);
+      }
+    }
+  };
+
+  locate();
+  setup();
+  prologue();
+  while (true) {
+    const int rows = MODE == kGradW ? a.rows : at.seg;
+    const bool active = at.m * BM + wm * (TM * 16) < rows;
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    __builtin_amdgcn_s_waitcnt(loads_left(0));
+    phase_end();
     if (steps > 0) {
-      const bool late = wave >= T::WAVES / 2;
       using Yes = std::true_type;
       using No = std::false_type;
       if (late) {
@@ -513,24 +660,21 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(TileArgs a) {
         if (active) run(No{}, Yes{}); else run(No{}, No{});
       }
     }
-    __builtin_amdgcn_s_waitcnt(loads_left(0));
     if (!FP8 && left > 0) {
-      const unsigned char* tail_a = base_a + (steps > 0 ? stepa : 0);
-      const unsigned char* tail_b = base_b + (steps > 0 ? stepb : 0);
-      phase_end();
+      // bases stand behind the last whole step
       const auto in_a = [&](int c) {
         return T::A_TURNED ? c * (64 / UA) + lane / UA < left : du * T::UNIT < left;
       };
 #pragma unroll
       for (int i = 0; i < RA; ++i) {
         const int c = i * T::WAVES + wave;
-        load_tail(a00, tail_a, oa[0][i], c, in_a(c));
-        load_tail(a01, tail_a, oa[1][i], c, in_a(c));
+        load_tail(a00, base_a, oa[0][i], c, in_a(c));
+        load_tail(a01, base_a, oa[1][i], c, in_a(c));
       }
 #pragma unroll
       for (int i = 0; i < 2 * RB; ++i) {
         const int c = i * T::WAVES + wave;
-        load_tail(b0, tail_b, ob[i], c,
+        load_tail(b0, base_b, ob[i], c,
                   T::B_TURNED ? c * (64 / UB) + lane / UB < left : du * T::UNIT < left);
       }
       __syncthreads();
@@ -543,58 +687,18 @@ __global__ __launch_bounds__(WN * WM * 64) void tile_kernel(TileArgs a) {
       }
       __syncthreads();
     }
-    if (!active) continue;
-
-    // a lane has 4 consecutive columns (4 * (lane / 16) of 16) of row lane % 16
-    const int c4 = g * 4;
-#pragma unroll
-    for (int j = 0; j < TM; ++j) {
-      const int r = m * BM + (wm * TM + j) * 16 + r16;
-      if (r >= rows) continue;
-      const int64_t orow = MODE == kGradW ? (int64_t)e * rows + r : row0 + r;
-#pragma unroll
-      for (int i = 0; i < TN; i += GLU ? 2 : 1) {
-        const int col = n * T::COLS + (wn * TN + i) * (GLU ? 8 : 16) + c4;
-        if (col >= a.cols) continue;
-        float v[4];
-        if (MODE == kForward) {
-          f32x4 z = acc[i][j], up = f32x4{0, 0, 0, 0};
-          if (GLU) up = acc[i + (GLU ? 1 : 0)][j];
-          if (a.bias) {
-            const float* b = a.bias + (int64_t)e * a.Nz + col;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              z[q] += b[q];
-              if (GLU) up[q] += b[a.cols + q];
-            }
-          }
-          if (a.z) {
-            uint16_t* zp = a.z + orow * a.Nz + col;
-            *reinterpret_cast<u32x2*>(zp) =
-                u32x2{pack_bf16_rne(z[0], z[1]), pack_bf16_rne(z[2], z[3])};
-            if (GLU)
-              *reinterpret_cast<u32x2*>(zp + a.cols) =
-                  u32x2{pack_bf16_rne(up[0], up[1]), pack_bf16_rne(up[2], up[3])};
-          }
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            v[q] = ACT == MEP_ACT_GELU   ? gelu(z[q])
-                   : ACT == MEP_ACT_SILU ? silu(z[q])
-                   : GLU                 ? silu(z[q]) * up[q]
-                                         : z[q];
-          if (a.residual) {
-            const u32x2 res = *reinterpret_cast<const u32x2*>(a.residual + orow * a.cols + col);
-            v[0] += bf16_lo(res[0]); v[1] += bf16_hi(res[0]);
-            v[2] += bf16_lo(res[1]); v[3] += bf16_hi(res[1]);
-          }
-        } else {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = acc[i][j][q];
-        }
-        *reinterpret_cast<u32x2*>(a.out + orow * a.cols + col) =
-            u32x2{pack_bf16_rne(v[0], v[1]), pack_bf16_rne(v[2], v[3])};
-      }
+    // every read of the buffers is done: the next tile's first loads run while
+    // this one is stored
+    const Place done = at;
+    tile += gridDim.x;
+    const bool more = tile < tiles;
+    if (more) {
+      locate();
+      setup();
+      prologue();
     }
+    if (active) finish(done);
+    if (!more) break;
   }
 }
 
@@ -702,21 +806,36 @@ int64_t row_tiles_bound(int64_t num_rows, int E, int bm) {
 }
 
 // `rows`: rows expected in all segments (forward, grad_x).
-template <Mode MODE, bool FP8, int ACT, int WN, int WM, int TN, int TM>
-void run_tiles(const TileArgs& a, int64_t rows, int per_cu, hipStream_t s) {
-  using T = Tile<MODE, FP8, ACT, WN, WM, TN, TM>;
+template <class T>
+int64_t count_tiles(const TileArgs& a, Mode mode, int64_t rows) {
   const int64_t cols = (a.cols + T::COLS - 1) / T::COLS;
-  const int64_t tiles = cols * (MODE == kGradW ? (int64_t)a.E * ((a.rows + T::BM - 1) / T::BM)
-                                               : row_tiles_bound(rows, a.E, T::BM));
-  const size_t lds = MODE == kGradW ? 0 : (size_t)(a.E + 1) * sizeof(int32_t);
-  const unsigned grid =
-      (unsigned)std::max<int64_t>(1, std::min<int64_t>(tiles, (int64_t)per_cu * kCus));
-  tile_kernel<MODE, FP8, ACT, WN, WM, TN, TM><<<grid, T::THREADS, lds, s>>>(a);
+  return cols * (mode == kGradW ? (int64_t)a.E * ((a.rows + T::BM - 1) / T::BM)
+                                : row_tiles_bound(rows, a.E, T::BM));
 }
 
+template <Mode MODE, bool FP8, int ACT, int TN, int TM, int PER_CU>
+void run_tiles(const TileArgs& a, int64_t rows, hipStream_t s) {
+  using T = Tile<MODE, FP8, ACT, 2, 4, TN, TM>;
+  const int64_t tiles = count_tiles<T>(a, MODE, rows);
+  const size_t lds = MODE == kGradW ? 0 : (size_t)(a.E + 1) * sizeof(int32_t);
+  const unsigned grid =
+      (unsigned)std::max<int64_t>(1, std::min<int64_t>(tiles, (int64_t)PER_CU * kCus));
+  tile_kernel<MODE, FP8, ACT, 2, 4, TN, TM, PER_CU><<<grid, T::THREADS, lds, s>>>(a);
+}
+
+// Tiles of 256 x 256, one block a CU, or of 128 x 128, two, which have twice the
+// traffic for a product but four times the tiles, and waste less on short
+// segments.  Measured (2048 -> 7168, one segment): 1000 rows, 116 large tiles,
+// 42.4 us large and 31.9 small; 1536 rows, 168 tiles, 45.0 and 64.8.  7168 ->
+// 2048 gated over 64 experts: 2 rows an expert 609 and 574 us, 32 rows 638 and
+// 620; over 256 experts 64 rows 1333 and 1326, 128 rows 1492 and 2102.
 template <Mode MODE, bool FP8, int ACT>
 void run_sized(const TileArgs& a, int64_t rows, hipStream_t s) {
-  run_tiles<MODE, FP8, ACT, 2, 4, 8, 4>(a, rows, 1, s);
+  using Large = Tile<MODE, FP8, ACT, 2, 4, 8, 4>;
+  const bool enough = count_tiles<Large>(a, MODE, rows) >= 144;
+  const bool long_segments = MODE == kGradW || rows > 64 * std::min<int64_t>(a.E, rows);
+  if (enough && long_segments) run_tiles<MODE, FP8, ACT, 8, 4, 1>(a, rows, s);
+  else run_tiles<MODE, FP8, ACT, 4, 2, 2>(a, rows, s);
 }
 
 template <bool FP8>

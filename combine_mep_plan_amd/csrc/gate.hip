@@ -84,16 +84,31 @@ __device__ __forceinline__ uint64_t order_key(double v) {
   return v != v ? 1ull : k;
 }
 
+// A packed key's value part as the value's own key.
+__device__ __forceinline__ uint32_t unpack_key(uint32_t k) {
+  const uint32_t v = k & 0xffff0000u;
+  return v == 0u ? 1u : v & 0x80000000u ? v : v | 0xffffu;
+}
+
 __device__ __forceinline__ float key_value(uint32_t k) {
   if (k == 1u) return __uint_as_float(0x7fc00000u);
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+// exp(x) in two instructions: the hardware's power of two of the rounded x log2 e,
+// so within 1 + 1.5 |x| half-steps of fp32 (relative).  Arguments here are
+// differences to a maximum, where large |x| means a negligible term.
+__device__ __forceinline__ float fast_exp(float x) {
+  return __builtin_amdgcn_exp2f(x * 1.44269504088896341f);
+}
+
+__device__ __forceinline__ float sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + fast_exp(-x));
+}
 
 // The sigmoid and its slope s (1 - s), neither with a cancellation.
 __device__ __forceinline__ float sigmoid(float x, float& slope) {
-  const float e = expf(-fabsf(x)), r = 1.0f / (1.0f + e);
+  const float e = fast_exp(-fabsf(x)), r = __builtin_amdgcn_rcpf(1.0f + e);
   slope = e * r * r;
   return x < 0.0f ? e * r : r;
 }
@@ -146,28 +161,42 @@ __device__ __forceinline__ int expert_of(int i, int l) {
   return ((i / V) * LPT + l) * V + i % V;
 }
 
-// A token's logits (row p of E); registers past E get -inf.  `wide`: E is a
-// multiple of V, so rows are 16-byte aligned and a load never straddles E.
+// A row p of E values, T as stored; registers past E get `none`.  `wide`: E is a
+// multiple of the logits' V (so of 4), rows are whole 16-byte units and a load
+// never straddles E.  Without, single loads, past the end of the last value
+// again: no load hides behind a branch, so all of them are in flight together.
 template <class TL, int LPT, int EPL>
-__device__ __forceinline__ void load_row(const TL* p, int E, int l, bool wide, float (&x)[EPL]) {
+__device__ __forceinline__ void load_row(const TL* p, int E, int l, bool wide, float none,
+                                         float (&x)[EPL]) {
   constexpr int V = Vec<TL>::V;
   if (wide) {
 #pragma unroll
-    for (int c = 0; c < EPL / V; ++c) {
-      const int e = (c * LPT + l) * V;
-      if (e < E) {
-        Vec<TL>::load(p + e, &x[c * V]);
-      } else {
+    for (int c = 0; c < EPL / V; ++c)
+      Vec<TL>::load(p + min((c * LPT + l) * V, E - V), &x[c * V]);
+  } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) x[c * V + v] = -__builtin_inff();
-      }
+    for (int i = 0; i < EPL; ++i) x[i] = load_logit(p + min(expert_of<TL, LPT>(i, l), E - 1));
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i)
+    if (expert_of<TL, LPT>(i, l) >= E) x[i] = none;
+}
+
+// The same registers of a row of E 32-bit values per expert (a bias, counts).
+template <class TL, int LPT, int EPL, class U>
+__device__ __forceinline__ void load_per_expert(const U* p, int E, int l, bool wide, U (&x)[EPL]) {
+  static_assert(sizeof(U) == 4, "");
+  if (wide) {
+#pragma unroll
+    for (int c = 0; c < EPL / 4; ++c) {
+      const int e = min(expert_of<TL, LPT>(c * 4, l), E - 4);
+      const u32x4 q = *reinterpret_cast<const u32x4*>(p + e);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) x[c * 4 + v] = __builtin_bit_cast(U, (uint32_t)q[v]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      const int e = expert_of<TL, LPT>(i, l);
-      x[i] = e < E ? load_logit(p + e) : -__builtin_inff();
-    }
+    for (int i = 0; i < EPL; ++i) x[i] = p[min(expert_of<TL, LPT>(i, l), E - 1)];
   }
 }
 
@@ -176,91 +205,159 @@ __device__ __forceinline__ void load_row(const TL* p, int E, int l, bool wide, f
 constexpr int kGateThreads = 256;
 
 // How far apart two fp32 scores sigmoid(x) + b must be for their order to be
-// the order of the exact scores: the sigmoid is within 3 units of 2^-24 (its
-// value is at most 1) and the sum rounds once more, so each score is within
-// 2^-22 (1 + |score|) and two of them within twice that.
+// the order of the exact scores.  The sigmoid's error: s (1 - s) <= 1/4 of the
+// exponential's relative one, which is at most 1 + 1.5 |x| half-steps, in all
+// below a half-step and a half, 2 for the reciprocal; the sum rounds once more.
+// So each score is within 2^-22 (1 + |score|), and two within twice that.
 __device__ __forceinline__ bool scores_apart(float hi, float lo) {
   return hi - lo > 4.76837158203125e-07f * (1.0f + fabsf(hi));
 }
 
-// k rounds of "largest key, lowest expert among equals, take it out".  What
-// bounds the kernel for many experts is these rounds (about 5 EPL + 8
-// instructions each, for 64 / LPT tokens), not the one pass over the logits.
-//
-// The selection with a bias is on sigmoid(x) + b in fp32.  Where neighbours of
-// the first k + 1 are too close for fp32 to order them (about 1 token in 2000
-// at 256 experts) the token's selection is done again in fp64; equal logits
-// with equal biases are equal scores and need no second look.
+// k rounds of "largest first, the lowest expert among equals".  The rounds and
+// not the one pass over the logits bound the kernel for many experts, so they
+// are cut down to one subtraction and half a minimum a value: with all keys of
+// a token different, the next key below the last one is last - 1 minus the
+// smallest of last - 1 - key, where keys already taken wrap around to large
+// numbers and need no removal.
+//   bf16 logits: value and expert together fill the 32 bits, and that is all.
+//   fp32 values: the low bits are given up for the register's number; the lane
+// that has the key is found by a vote.  Where two lanes have it, or neighbours
+// among the first k + 1 are equal but for those bits (about 1 token in 300 at
+// 256 experts), the token's rounds are run again on the whole values, with
+// removal.
+//   Biased scores: where neighbours of the first k + 1 are too close for fp32 to
+// order sigmoid(x) + b, the selection is done in fp64; equal logits with equal
+// biases are equal scores and need no second look.
 template <class TL, int LPT, int EPL, bool BIAS>
 __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
   constexpr int SLOTS = (kMaxTopk + LPT - 1) / LPT;  // results a lane may hold
+  constexpr bool PACKED = !BIAS && sizeof(TL) == 2;
   const int l = threadIdx.x % LPT;
   const int64_t t = ((int64_t)blockIdx.x * kGateThreads + threadIdx.x) / LPT;
   const bool live = t < a.T;
   const int E = a.E, k = a.k;
   const TL* row = reinterpret_cast<const TL*>(a.logits) + (live ? t : a.T - 1) * (int64_t)E;
 
-  float x[EPL];
-  load_row<TL, LPT, EPL>(row, E, l, a.wide, x);
+  float x[EPL], bias[BIAS ? EPL : 1];
+  load_row<TL, LPT, EPL>(row, E, l, a.wide, -__builtin_inff(), x);
+  if constexpr (BIAS) load_per_expert<TL, LPT, EPL>(a.bias, E, l, a.wide, bias);
   uint32_t key[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = expert_of<TL, LPT>(i, l);
     float s = x[i];
-    if (BIAS) s = e < E ? sigmoid(s) + a.bias[e] : 0.0f;
+    if constexpr (BIAS) s = sigmoid(s) + bias[i];
     key[i] = e < E ? order_key(s) : 0u;
+    if (PACKED && e < E) key[i] = (key[i] & 0xffff0000u) | (uint32_t)(0xffff - e);
   }
 
   uint32_t got_key[SLOTS];
   int got[SLOTS];
 #pragma unroll
   for (int s = 0; s < SLOTS; ++s) { got_key[s] = 1u; got[s] = 0; }
-  uint32_t first = 0;
-  uint32_t last = 0;
-  int last_e = 0;
-  bool unsure = false;
+  [[maybe_unused]] uint32_t first = 0;  // the largest value's key
+  bool unsure = false;  // biased: the order needs 64 bits
+  bool again = false;   // the short keys did not decide
+  if constexpr (PACKED) {
+    uint32_t last = 0xffffffffu;
 #pragma unroll
-  for (int s = 0; s < SLOTS; ++s) {
-    for (int jj = 0; jj < LPT; ++jj) {
-      const int j = s * LPT + jj;
-      if (j >= k) break;
-      uint32_t m = 0;
+    for (int s = 0; s < SLOTS; ++s) {
+      for (int jj = 0; jj < LPT; ++jj) {
+        const int j = s * LPT + jj;
+        if (j >= k) break;
+        uint32_t d = 0xffffffffu;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) m = key[i] > m ? key[i] : m;
-      m = group_max<LPT>(m);
-      uint32_t e = 0xffffffffu;
-#pragma unroll
-      for (int i = EPL - 1; i >= 0; --i) {
-        if (key[i] == m) e = (uint32_t)expert_of<TL, LPT>(i, l);
-      }
-      e = group_min<LPT>(e);
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if ((uint32_t)expert_of<TL, LPT>(i, l) == e) key[i] = 0u;
-      if (j == 0) first = m;
-      if (BIAS) {
-        if (j > 0 && !scores_apart(key_value(last), key_value(m))) {
-          // row and bias loads hit the cache; equal inputs need no second look
-          const bool same = load_logit(row + last_e) == load_logit(row + e) &&
-                            a.bias[last_e] == a.bias[e];
-          unsure |= !same;
+        for (int i = 0; i < EPL; ++i) d = min(d, last - 1u - key[i]);
+        last = last - 1u - group_min<LPT>(d);
+        if (j == 0) first = last | 0xffffu;
+        if (l == jj) {
+          got_key[s] = last;
+          got[s] = 0xffff - (int)(last & 0xffffu);
         }
-        last = m;
-        last_e = (int)e;
       }
-      if (l == jj) {
-        got_key[s] = m;
-        got[s] = (int)e;
+    }
+    // the values back: a bf16's low half of the order's bits is all ones below
+    // zero and all zeros from there on; NaN's key is 1 with the expert over it
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) got_key[s] = unpack_key(got_key[s]);
+    first = unpack_key(first);
+  } else {
+    constexpr uint32_t LOW = EPL - 1;
+    static_assert((EPL & (EPL - 1)) == 0, "");
+    uint32_t last = 0xffffffffu;
+    // one round more than k: the border has to be decided too
+#pragma unroll
+    for (int s = 0; s < SLOTS + 1; ++s) {
+      for (int jj = 0; jj < LPT; ++jj) {
+        const int j = s * LPT + jj;
+        if (j > k || j >= E) break;
+        uint32_t d = 0xffffffffu;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          d = min(d, last - 1u - ((key[i] & ~LOW) | (LOW - i)));
+        const uint32_t m = group_min<LPT>(d);
+        const uint32_t now = last - 1u - m;
+        uint64_t vote = ballot(d == m);
+        if (LPT < 64) vote = vote >> (lane_id() & (64 - LPT)) & ((1ull << (LPT & 63)) - 1);
+        again |= (vote & (vote - 1)) != 0 || now <= LOW;  // NaN and absent alike
+        if (j > 0) {
+          if (BIAS) {
+            // what the low bits may hide is less than LOW + 1 units of the larger
+            const float hi = key_value(last & ~LOW), lo = key_value(now | LOW);
+            again |= !scores_apart(hi, lo);
+          } else {
+            again |= (last & ~LOW) == (now & ~LOW);
+          }
+        }
+        last = now;
+        if (s < SLOTS && j < k && l == jj)
+          got[s < SLOTS ? s : 0] =
+              expert_of<TL, LPT>(LOW - (int)(now & LOW), __builtin_ctzll(vote));
       }
     }
   }
-
-  if (BIAS) {
-    uint32_t m = 0;
+  if (!PACKED && again) {
+    uint32_t last = 0;
+    int last_e = 0;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) m = key[i] > m ? key[i] : m;
-    m = group_max<LPT>(m);  // the best score left out; 0 when k == E
-    if (m != 0u && !scores_apart(key_value(last), key_value(m))) unsure = true;
+    for (int s = 0; s < SLOTS; ++s) {
+      for (int jj = 0; jj < LPT; ++jj) {
+        const int j = s * LPT + jj;
+        if (j >= k) break;
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) m = key[i] > m ? key[i] : m;
+        m = group_max<LPT>(m);
+        uint32_t e = 0xffffffffu;
+#pragma unroll
+        for (int i = EPL - 1; i >= 0; --i) {
+          if (key[i] == m) e = (uint32_t)expert_of<TL, LPT>(i, l);
+        }
+        e = group_min<LPT>(e);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if ((uint32_t)expert_of<TL, LPT>(i, l) == e) key[i] = 0u;
+        if (BIAS) {
+          if (j > 0 && !scores_apart(key_value(last), key_value(m))) {
+            const bool same = load_logit(row + last_e) == load_logit(row + e) &&
+                              a.bias[last_e] == a.bias[e];
+            unsure |= !same;
+          }
+          last = m;
+          last_e = (int)e;
+        }
+        if (l == jj) got[s] = (int)e;
+      }
+    }
+    if (BIAS) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) m = key[i] > m ? key[i] : m;
+      m = group_max<LPT>(m);  // the best score left out; 0 when k == E
+      if (m != 0u && !scores_apart(key_value(last), key_value(m))) unsure = true;
+    }
+  }
+  if constexpr (BIAS) {
     if (unsure) {  // the same for all lanes of the group
       uint64_t out = 0;  // this lane's registers already taken
 #pragma unroll
@@ -275,7 +372,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
             const int e = expert_of<TL, LPT>(i, l);
             if (e < E && !((out >> i) & 1)) {
               const uint64_t q =
-                  order_key(1.0 / (1.0 + exp(-(double)x[i])) + (double)a.bias[e]);
+                  order_key(1.0 / (1.0 + exp(-(double)x[i])) + (double)bias[i]);
               if (q > best) {  // registers hold ascending experts: the lowest wins
                 best = q;
                 be = e;
@@ -301,17 +398,22 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
 
   // weights: lane l holds positions l, l + LPT, ...
   float w[SLOTS];
-  const float m = key_value(first);  // the largest logit (softmax only)
+  // the largest logit (softmax only): the first position's
+  float m;
+  if constexpr (PACKED) m = key_value(first);
+  else m = load_logit(row + __shfl(got[0], 0, LPT));
   float sum = 0.0f;
 #pragma unroll
   for (int s = 0; s < SLOTS; ++s) {
     const int j = s * LPT + l;
     w[s] = 0.0f;
     if (j < k) {
-      const float v = BIAS ? load_logit(row + got[s]) : key_value(got_key[s]);
+      float v;
+      if constexpr (PACKED) v = key_value(got_key[s]);
+      else v = load_logit(row + got[s]);  // a cache hit
       w[s] = a.score == MEP_SCORE_SIGMOID ? sigmoid(v)
              : m == -__builtin_inff()     ? 0.0f
-                                          : expf(v - m);
+                                          : fast_exp(v - m);
     }
     sum += w[s];
   }
@@ -321,7 +423,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
       sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
-        if (expert_of<TL, LPT>(i, l) < E) sum += expf(x[i] - m);
+        if (expert_of<TL, LPT>(i, l) < E) sum += fast_exp(x[i] - m);
     }
     sum = group_sum<LPT>(sum);
     // nothing selectable (every logit -inf): all weights are 0
@@ -359,7 +461,7 @@ __device__ __forceinline__ void probabilities(float (&x)[EPL], int score, float 
     const float shift = m == -__builtin_inff() ? 0.0f : m;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {  // registers past E hold -inf: exp gives 0
-      p[i] = expf(x[i] - shift);
+      p[i] = fast_exp(x[i] - shift);
       sum += p[i];
     }
   } else {
@@ -375,18 +477,22 @@ __device__ __forceinline__ void probabilities(float (&x)[EPL], int score, float 
 
 // ---- balance loss ---------------------------------------------------------
 
-// Blocks of up to 16 tokens a round sum their tokens' probabilities in
-// registers (a group's lanes keep their experts), join the groups through LDS
-// in a fixed order, count the named experts with LDS integer atomics, and
-// write one row of partial sums and counts.  The block that finishes last adds
-// the rows up in order, so the result does not depend on the blocks' timing.
-constexpr int kBalanceThreads = 256;
+// Groups of lanes sum their tokens' probabilities in registers (a lane keeps its
+// experts); a wave's groups join by exchanges, a block's waves through LDS, all
+// in a fixed order; named experts are counted with LDS integer atomics.  Each
+// block writes a row of partial sums and counts, and the one that finishes last
+// adds the rows up in order, so the result does not depend on timing.  What
+// bounds it at 4096 x 256 is latency: a pass of loads, the rows' way to memory
+// and back (a second launch would cost more), and the last block's loads, which
+// 512 threads keep in flight eight at a time.
+constexpr int kBalanceThreads = 512;
 
 template <class TL, int LPT, int EPL>
 __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a) {
   constexpr int GROUPS = kBalanceThreads / LPT;
   extern __shared__ float lds[];  // [E] sums, then [E] counts and the valid tokens
   const int E = a.E, l = threadIdx.x % LPT, g = threadIdx.x / LPT;
+  const int lane = lane_id(), wave = threadIdx.x / kWave;
   float* sums = lds;
   int* cnt = reinterpret_cast<int*>(lds + E);
   for (int e = threadIdx.x; e <= E; e += kBalanceThreads) cnt[e] = 0;
@@ -395,21 +501,28 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
   float acc[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) acc[i] = 0.0f;
-  for (int64_t t = (int64_t)blockIdx.x * GROUPS + g; t < a.T; t += (int64_t)gridDim.x * GROUPS) {
+  const int64_t step = (int64_t)gridDim.x * GROUPS;
+  for (int64_t t = (int64_t)blockIdx.x * GROUPS + g; t < a.T; t += step) {
     if (a.mask && a.mask[t] == 0) continue;  // the same for all lanes of the group
     float x[EPL], p[EPL], m, inv;
-    load_row<TL, LPT, EPL>(reinterpret_cast<const TL*>(a.logits) + t * E, E, l, a.wide, x);
-    probabilities<LPT, EPL, false>(x, a.score, p, m, inv);
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) acc[i] += p[i] * inv;
+    load_row<TL, LPT, EPL>(reinterpret_cast<const TL*>(a.logits) + t * E, E, l, a.wide,
+                           -__builtin_inff(), x);
     for (int j = l; j < a.k; j += LPT) {
       const int e = a.indices[t * a.k + j];
       if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
     }
     if (l == 0) atomicAdd(&cnt[E], 1);
+    probabilities<LPT, EPL, false>(x, a.score, p, m, inv);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) acc[i] += p[i] * inv;
   }
-  for (int q = 0; q < GROUPS; ++q) {
-    if (q == g) {
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+#pragma unroll
+    for (int d = LPT; d < kWave; d <<= 1) acc[i] += __shfl_xor(acc[i], d);
+  }
+  for (int q = 0; q < kBalanceThreads / kWave; ++q) {
+    if (q == wave && lane < LPT) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         const int e = expert_of<TL, LPT>(i, l);
@@ -433,30 +546,71 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
   __syncthreads();
   if (!is_last) return;
   __threadfence();
-  double* dot = reinterpret_cast<double*>(lds);  // the sums are done with
-  int64_t n = 0;
-  for (unsigned b = 0; b < gridDim.x; ++b) n += a.part_cnt[(size_t)b * (E + 1) + E];
-  double mine = 0.0;
-  for (int e = threadIdx.x; e < E; e += kBalanceThreads) {
-    double s = 0.0;
-    int32_t c = 0;
-    for (unsigned b = 0; b < gridDim.x; ++b) {
-      s += (double)a.part_sum[(size_t)b * E + e];
-      c += a.part_cnt[(size_t)b * (E + 1) + e];
-    }
-    const double mean = n > 0 ? s / (double)n : 0.0;
-    a.counts[e] = c;
-    a.prob_mean[e] = (float)mean;
-    mine += (double)c * mean;
+  __shared__ double join[kBalanceThreads];
+  __shared__ int32_t join_cnt[kBalanceThreads];
+  const int rows = (int)gridDim.x;
+  // valid tokens
+  int32_t n = 0;
+  if (threadIdx.x < kWave) {
+    for (int r = lane; r < rows; r += kWave) n += a.part_cnt[(size_t)r * (E + 1) + E];
+    for (int d = 1; d < kWave; d <<= 1) n += __shfl_xor(n, d);
+    if (threadIdx.x == 0) join_cnt[0] = n;
   }
   __syncthreads();
-  dot[threadIdx.x] = mine;
+  n = join_cnt[0];
+  const double inv_n = n > 0 ? 1.0 / (double)n : 0.0;
+  // `share` threads a column, each every share-th row
+  const int share = E <= 64 ? 8 : E <= 128 ? 4 : E <= 256 ? 2 : 1;
+  const int width = kBalanceThreads / share;
+  const int c = threadIdx.x % width, part_of = threadIdx.x / width;
+  double mine = 0.0;
+  for (int e0 = 0; e0 < E; e0 += width) {
+    const int e = e0 + c;
+    double s = 0.0;
+    int32_t q = 0;
+    if (e < E) {
+      for (int r0 = part_of; r0 < rows; r0 += 8 * share) {
+        float v[8];
+        int32_t w[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int r = min(r0 + u * share, rows - 1);
+          v[u] = a.part_sum[(size_t)r * E + e];
+          w[u] = a.part_cnt[(size_t)r * (E + 1) + e];
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          if (r0 + u * share < rows) {
+            s += (double)v[u];
+            q += w[u];
+          }
+        }
+      }
+    }
+    __syncthreads();
+    join[threadIdx.x] = s;
+    join_cnt[threadIdx.x] = q;
+    __syncthreads();
+    if (part_of == 0 && e < E) {
+      for (int u = 1; u < share; ++u) {
+        s += join[u * width + c];
+        q += join_cnt[u * width + c];
+      }
+      const double mean = s * inv_n;
+      a.counts[e] = q;
+      a.prob_mean[e] = (float)mean;
+      mine += (double)q * mean;
+    }
+  }
+  __syncthreads();
+  for (int d = 1; d < kWave; d <<= 1) mine += __shfl_xor(mine, d);
+  if (lane == 0) join[wave] = mine;
   __syncthreads();
   if (threadIdx.x == 0) {
     double s = 0.0;
-    for (int i = 0; i < kBalanceThreads; ++i) s += dot[i];
-    a.counts[E] = (int32_t)n;
-    a.loss[0] = n > 0 ? (float)(s * (double)a.coef * (double)E / ((double)a.k * (double)n)) : 0.0f;
+    for (int i = 0; i < kBalanceThreads / kWave; ++i) s += join[i];
+    a.counts[E] = n;
+    a.loss[0] = (float)(s * inv_n * (double)a.coef * (double)E / (double)a.k);
     *a.done = 0u;  // ready for the next call on this workspace
   }
 }
@@ -485,24 +639,27 @@ __global__ __launch_bounds__(kGradThreads) void gate_backward_kernel(GateBackwar
   float* extra = lds + (size_t)g * E;
 
   float x[EPL], p[EPL], m, inv;
-  load_row<TL, LPT, EPL>(row, E, l, a.wide, x);
+  load_row<TL, LPT, EPL>(row, E, l, a.wide, -__builtin_inff(), x);
   probabilities<LPT, EPL, true>(x, a.score, p, m, inv);
   const bool softmax = a.score == MEP_SCORE_SOFTMAX;
 
   // the loss' gradient for each expert's probability
   float u[EPL], dot = 0.0f;
-  float coef = 0.0f;
-  if (a.counts) {
-    const double n = (double)a.counts[E];
-    coef = n > 0 ? (float)((double)a.grad_loss[0] * (double)a.coef * E / (k * n * n)) : 0.0f;
-  }
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = expert_of<TL, LPT>(i, l);
-    u[i] = a.counts && e < E ? coef * (float)a.counts[e] : 0.0f;
-    dot += u[i] * (p[i] * inv);
+  for (int i = 0; i < EPL; ++i) u[i] = 0.0f;
+  if (a.counts) {
+    int32_t cnt[EPL];
+    load_per_expert<TL, LPT, EPL>(a.counts, E, l, a.wide, cnt);
+    const double n = (double)a.counts[E];
+    const float coef =
+        n > 0 ? (float)((double)a.grad_loss[0] * (double)a.coef * E / (k * n * n)) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      u[i] = coef * (float)cnt[i];
+      dot += u[i] * (p[i] * inv);  // p is 0 past E
+    }
+    dot = group_sum<LPT>(dot);
   }
-  dot = group_sum<LPT>(dot);
 
   // the weights' gradient for each position
   float shift = 0.0f;  // unnormalised softmax: sum over positions of g p, taken off every expert
@@ -523,7 +680,7 @@ __global__ __launch_bounds__(kGradThreads) void gate_backward_kernel(GateBackwar
           gw[s] = a.scale * a.grad_weights[tt * k + j];
           const float xe = load_logit(row + e);
           if (softmax) {
-            v[s] = m == -__builtin_inff() ? 0.0f : expf(xe - m);
+            v[s] = m == -__builtin_inff() ? 0.0f : fast_exp(xe - m);
           } else {
             v[s] = sigmoid(xe, d[s]);
           }
@@ -645,7 +802,7 @@ hipError_t launch_gate(const GateArgs& a0, hipStream_t s) {
 
 int balance_blocks(int E, int64_t T) {
   const int64_t groups = kBalanceThreads / lanes_of(E);
-  const int64_t want = (T + 4 * groups - 1) / (4 * groups);
+  const int64_t want = (T + groups - 1) / groups;
   return (int)(want < 1 ? 1 : want > 64 ? 64 : want);
 }
 
@@ -654,7 +811,7 @@ hipError_t launch_balance(const BalanceArgs& a0, hipStream_t s) {
   a.wide = is_wide(a.E, a.dtype);
   const unsigned blocks = (unsigned)balance_blocks(a.E, a.T);
   by_experts(a.E, [&](auto lpt, auto epl) {
-    const size_t lds = std::max((size_t)(2 * a.E + 1) * 4, (size_t)kBalanceThreads * 8);
+    const size_t lds = (size_t)(2 * a.E + 1) * 4;
     if (a.dtype == MEP_BF16)
       balance_kernel<uint16_t, lpt(), epl()><<<blocks, kBalanceThreads, lds, s>>>(a);
     else

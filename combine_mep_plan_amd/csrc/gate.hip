@@ -68,6 +68,19 @@ __device__ __forceinline__ float group_fmax(float v) {
   }));
 }
 
+// The largest key of the lanes, the lowest expert among equals.
+template <int LPT>
+__device__ __forceinline__ void group_best(uint64_t& key, int& e) {
+  for (int d = 1; d < LPT; d <<= 1) {
+    const uint64_t ok = __shfl_xor((unsigned long long)key, d);
+    const int oe = __shfl_xor(e, d);
+    if (ok > key || (ok == key && oe < e)) {
+      key = ok;
+      e = oe;
+    }
+  }
+}
+
 // ---- values ---------------------------------------------------------------
 
 // Unsigned keys in the order of the values: -inf < ... < -0 = +0 < ... < +inf
@@ -225,9 +238,9 @@ __device__ __forceinline__ bool scores_apart(float hi, float lo) {
 // among the first k + 1 are equal but for those bits (about 1 token in 300 at
 // 256 experts), the token's rounds are run again on the whole values, with
 // removal.
-//   Biased scores: where neighbours of the first k + 1 are too close for fp32 to
-// order sigmoid(x) + b, the selection is done in fp64; equal logits with equal
-// biases are equal scores and need no second look.
+//   Biased scores: the same in place of "equal" with neighbours too close for
+// fp32 to order sigmoid(x) + b (about 1 token in 150), and the second time in
+// fp64 over those that may be among the first k.
 template <class TL, int LPT, int EPL, bool BIAS>
 __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
   constexpr int SLOTS = (kMaxTopk + LPT - 1) / LPT;  // results a lane may hold
@@ -256,8 +269,8 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
 #pragma unroll
   for (int s = 0; s < SLOTS; ++s) { got_key[s] = 1u; got[s] = 0; }
   [[maybe_unused]] uint32_t first = 0;  // the largest value's key
-  bool unsure = false;  // biased: the order needs 64 bits
-  bool again = false;   // the short keys did not decide
+  bool again = false;  // the short keys did not decide
+  [[maybe_unused]] uint32_t border = 0;  // biased: below this key nobody is among the first k
   if constexpr (PACKED) {
     uint32_t last = 0xffffffffu;
 #pragma unroll
@@ -310,15 +323,106 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
           }
         }
         last = now;
+        if (BIAS && j == k - 1) {
+          const float lo = key_value(now & ~LOW);
+          border = lo > -__builtin_inff()
+                       ? order_key(lo - 1.9073486328125e-06f * (1.0f + fabsf(lo)))
+                       : 0u;
+        }
         if (s < SLOTS && j < k && l == jj)
           got[s < SLOTS ? s : 0] =
               expert_of<TL, LPT>(LOW - (int)(now & LOW), __builtin_ctzll(vote));
       }
     }
   }
-  if (!PACKED && again) {
-    uint32_t last = 0;
-    int last_e = 0;
+  if constexpr (BIAS) {
+    // Where the order needs 64 bits: every expert whose score may be among the
+    // first k goes into a list, a lane works out its entries' scores in fp64, and
+    // the rounds run over those.  A list that overflows (very many equal scores)
+    // is replaced by all experts.
+    constexpr int CAP = 64, HAVE = CAP / LPT;
+    __shared__ uint16_t lists[kGateThreads / LPT][CAP];
+    if (again) {
+      uint16_t* list = lists[threadIdx.x / LPT];
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = expert_of<TL, LPT>(i, l);
+        const bool in = e < E && key[i] >= border;
+        uint64_t vote = ballot(in) >> (lane_id() & (64 - LPT));
+        if (LPT < 64) vote &= (1ull << (LPT & 63)) - 1;
+        const int at = n + __popcll(vote & ((1ull << l) - 1));
+        if (in && at < CAP) list[at] = (uint16_t)e;
+        n += __popcll(vote);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      if (n <= CAP) {
+        uint64_t sk[HAVE];
+        int se[HAVE];
+#pragma unroll
+        for (int h = 0; h < HAVE; ++h) {
+          const int c = h * LPT + l;
+          sk[h] = 0;
+          se[h] = 0xffff;
+          if (c < n) {
+            const int e = list[c];
+            se[h] = e;
+            sk[h] = order_key(1.0 / (1.0 + exp(-(double)load_logit(row + e))) + (double)a.bias[e]);
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+          for (int jj = 0; jj < LPT; ++jj) {
+            const int j = s * LPT + jj;
+            if (j >= k) break;
+            uint64_t best = 0;
+            int be = 0xffff;
+#pragma unroll
+            for (int h = 0; h < HAVE; ++h) {
+              if (sk[h] > best || (sk[h] == best && se[h] < be)) {
+                best = sk[h];
+                be = se[h];
+              }
+            }
+            group_best<LPT>(best, be);
+#pragma unroll
+            for (int h = 0; h < HAVE; ++h)
+              if (se[h] == be) sk[h] = 0;
+            if (l == jj) got[s] = be;
+          }
+        }
+      } else {
+        uint64_t out = 0;  // this lane's registers already taken
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+          for (int jj = 0; jj < LPT; ++jj) {
+            const int j = s * LPT + jj;
+            if (j >= k) break;
+            uint64_t best = 0;
+            int be = 0;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+              const int e = expert_of<TL, LPT>(i, l);
+              if (e < E && !((out >> i) & 1)) {
+                const uint64_t q =
+                    order_key(1.0 / (1.0 + exp(-(double)x[i])) + (double)bias[i]);
+                if (q > best) {  // registers hold ascending experts: the lowest wins
+                  best = q;
+                  be = e;
+                }
+              }
+            }
+            group_best<LPT>(best, be);
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+              if (expert_of<TL, LPT>(i, l) == be) out |= 1ull << i;
+            if (l == jj) got[s] = be;
+          }
+        }
+      }
+    }
+  } else if (!PACKED && again) {
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
       for (int jj = 0; jj < LPT; ++jj) {
@@ -337,61 +441,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
           if ((uint32_t)expert_of<TL, LPT>(i, l) == e) key[i] = 0u;
-        if (BIAS) {
-          if (j > 0 && !scores_apart(key_value(last), key_value(m))) {
-            const bool same = load_logit(row + last_e) == load_logit(row + e) &&
-                              a.bias[last_e] == a.bias[e];
-            unsure |= !same;
-          }
-          last = m;
-          last_e = (int)e;
-        }
         if (l == jj) got[s] = (int)e;
-      }
-    }
-    if (BIAS) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) m = key[i] > m ? key[i] : m;
-      m = group_max<LPT>(m);  // the best score left out; 0 when k == E
-      if (m != 0u && !scores_apart(key_value(last), key_value(m))) unsure = true;
-    }
-  }
-  if constexpr (BIAS) {
-    if (unsure) {  // the same for all lanes of the group
-      uint64_t out = 0;  // this lane's registers already taken
-#pragma unroll
-      for (int s = 0; s < SLOTS; ++s) {
-        for (int jj = 0; jj < LPT; ++jj) {
-          const int j = s * LPT + jj;
-          if (j >= k) break;
-          uint64_t best = 0;
-          int be = 0;
-#pragma unroll
-          for (int i = 0; i < EPL; ++i) {
-            const int e = expert_of<TL, LPT>(i, l);
-            if (e < E && !((out >> i) & 1)) {
-              const uint64_t q =
-                  order_key(1.0 / (1.0 + exp(-(double)x[i])) + (double)bias[i]);
-              if (q > best) {  // registers hold ascending experts: the lowest wins
-                best = q;
-                be = e;
-              }
-            }
-          }
-          for (int d = 1; d < LPT; d <<= 1) {
-            const uint64_t oq = __shfl_xor((unsigned long long)best, d);
-            const int oe = __shfl_xor(be, d);
-            if (oq > best || (oq == best && oe < be)) {
-              best = oq;
-              be = oe;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < EPL; ++i)
-            if (expert_of<TL, LPT>(i, l) == be) out |= 1ull << i;
-          if (l == jj) got[s] = be;
-        }
       }
     }
   }
@@ -484,29 +534,44 @@ __device__ __forceinline__ void probabilities(float (&x)[EPL], int score, float 
 // adds the rows up in order, so the result does not depend on timing.  What
 // bounds it at 4096 x 256 is latency: a pass of loads, the rows' way to memory
 // and back (a second launch would cost more), and the last block's loads, which
-// 512 threads keep in flight eight at a time.
+// 512 threads keep in flight 16 rows each.
 constexpr int kBalanceThreads = 512;
+constexpr int kRowsAhead = 16;  // partial rows a thread of the last block has in flight
+
+// Threads of the last block that share a column.
+__host__ __device__ constexpr int column_share(int E) {
+  return E <= 64 ? 8 : E <= 128 ? 4 : E <= 256 ? 2 : 1;
+}
 
 template <class TL, int LPT, int EPL>
 __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a) {
   constexpr int GROUPS = kBalanceThreads / LPT;
-  extern __shared__ float lds[];  // [E] sums, then [E] counts and the valid tokens
+  __shared__ __attribute__((aligned(16)))
+  float sums[kBalanceThreads / kWave * LPT * (LPT == 64 ? 16 : EPL)];
+  extern __shared__ int cnt[];  // [E] counts and the valid tokens
   const int E = a.E, l = threadIdx.x % LPT, g = threadIdx.x / LPT;
   const int lane = lane_id(), wave = threadIdx.x / kWave;
-  float* sums = lds;
-  int* cnt = reinterpret_cast<int*>(lds + E);
   for (int e = threadIdx.x; e <= E; e += kBalanceThreads) cnt[e] = 0;
   __syncthreads();
 
   float acc[EPL];
 #pragma unroll
   for (int i = 0; i < EPL; ++i) acc[i] = 0.0f;
+  const TL* logits = reinterpret_cast<const TL*>(a.logits);
   const int64_t step = (int64_t)gridDim.x * GROUPS;
-  for (int64_t t = (int64_t)blockIdx.x * GROUPS + g; t < a.T; t += step) {
-    if (a.mask && a.mask[t] == 0) continue;  // the same for all lanes of the group
+  auto load = [&](int64_t t, float (&x)[EPL]) {
+    load_row<TL, LPT, EPL>(logits + min(t, (int64_t)a.T - 1) * E, E, l, a.wide, -__builtin_inff(),
+                           x);
+  };
+  float next[EPL];
+  int64_t t = (int64_t)blockIdx.x * GROUPS + g;
+  if (t < a.T) load(t, next);
+  for (; t < a.T; t += step) {
     float x[EPL], p[EPL], m, inv;
-    load_row<TL, LPT, EPL>(reinterpret_cast<const TL*>(a.logits) + t * E, E, l, a.wide,
-                           -__builtin_inff(), x);
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) x[i] = next[i];
+    load(t + step, next);  // while this row is worked on
+    if (a.mask && a.mask[t] == 0) continue;  // the same for all lanes of the group
     for (int j = l; j < a.k; j += LPT) {
       const int e = a.indices[t * a.k + j];
       if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
@@ -521,22 +586,31 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
 #pragma unroll
     for (int d = LPT; d < kWave; d <<= 1) acc[i] += __shfl_xor(acc[i], d);
   }
-  for (int q = 0; q < kBalanceThreads / kWave; ++q) {
-    if (q == wave && lane < LPT) {
+  // waves: CHUNK registers of each at a time, which hold WIDTH neighbouring experts
+  constexpr int WAVES = kBalanceThreads / kWave;
+  constexpr int CHUNK = LPT == 64 ? 16 : EPL, WIDTH = CHUNK * LPT;
+  float* part = a.part_sum + (size_t)blockIdx.x * E;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const int e = expert_of<TL, LPT>(i, l);
-        if (e < E) sums[e] = q == 0 ? acc[i] : sums[e] + acc[i];
-      }
+  for (int c = 0; c < EPL; c += CHUNK) {
+    const int e0 = c * LPT;
+    if (e0 >= E) break;
+    if (c > 0) __syncthreads();
+    if (lane < LPT) {
+#pragma unroll
+      for (int i = 0; i < CHUNK; i += 4)
+        *reinterpret_cast<float4*>(sums + wave * WIDTH + expert_of<TL, LPT>(c + i, l) - e0) =
+            make_float4(acc[c + i], acc[c + i + 1], acc[c + i + 2], acc[c + i + 3]);
     }
     __syncthreads();
+    for (int e = threadIdx.x; e < WIDTH && e0 + e < E; e += kBalanceThreads) {
+      float s = sums[e];
+#pragma unroll
+      for (int q = 1; q < WAVES; ++q) s += sums[q * WIDTH + e];
+      part[e0 + e] = s;
+    }
   }
-  float* part = a.part_sum + (size_t)blockIdx.x * E;
   int32_t* pcnt = a.part_cnt + (size_t)blockIdx.x * (E + 1);
-  for (int e = threadIdx.x; e <= E; e += kBalanceThreads) {
-    if (e < E) part[e] = sums[e];
-    pcnt[e] = cnt[e];
-  }
+  for (int e = threadIdx.x; e <= E; e += kBalanceThreads) pcnt[e] = cnt[e];
 
   // the last block to arrive joins the partial rows
   __shared__ int is_last;
@@ -560,7 +634,7 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
   n = join_cnt[0];
   const double inv_n = n > 0 ? 1.0 / (double)n : 0.0;
   // `share` threads a column, each every share-th row
-  const int share = E <= 64 ? 8 : E <= 128 ? 4 : E <= 256 ? 2 : 1;
+  const int share = column_share(E);
   const int width = kBalanceThreads / share;
   const int c = threadIdx.x % width, part_of = threadIdx.x / width;
   double mine = 0.0;
@@ -569,17 +643,17 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
     double s = 0.0;
     int32_t q = 0;
     if (e < E) {
-      for (int r0 = part_of; r0 < rows; r0 += 8 * share) {
-        float v[8];
-        int32_t w[8];
+      for (int r0 = part_of; r0 < rows; r0 += kRowsAhead * share) {
+        float v[kRowsAhead];
+        int32_t w[kRowsAhead];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < kRowsAhead; ++u) {
           const int r = min(r0 + u * share, rows - 1);
           v[u] = a.part_sum[(size_t)r * E + e];
           w[u] = a.part_cnt[(size_t)r * (E + 1) + e];
         }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
+        for (int u = 0; u < kRowsAhead; ++u) {
           if (r0 + u * share < rows) {
             s += (double)v[u];
             q += w[u];
@@ -800,10 +874,17 @@ hipError_t launch_gate(const GateArgs& a0, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Blocks: a pass over one token a group takes about 0.6 us, and each block's
+// arrival at the counter, which they reach one by one, about 0.08, so the square
+// root of 7.5 passes.  Measured at 4096 tokens (us): 256 experts 16.5 with 32
+// blocks and 19.7 with 64, 60 experts at 16384 tokens 18.4 with 64 and 25.9 with
+// 128.
 int balance_blocks(int E, int64_t T) {
   const int64_t groups = kBalanceThreads / lanes_of(E);
-  const int64_t want = (T + groups - 1) / groups;
-  return (int)(want < 1 ? 1 : want > 64 ? 64 : want);
+  const int64_t passes = std::max<int64_t>(1, (T + groups - 1) / groups);
+  int64_t b = 1;
+  while (b < 256 && 2 * b * b < 15 * passes) ++b;
+  return (int)std::min(passes, b);
 }
 
 hipError_t launch_balance(const BalanceArgs& a0, hipStream_t s) {
@@ -811,7 +892,7 @@ hipError_t launch_balance(const BalanceArgs& a0, hipStream_t s) {
   a.wide = is_wide(a.E, a.dtype);
   const unsigned blocks = (unsigned)balance_blocks(a.E, a.T);
   by_experts(a.E, [&](auto lpt, auto epl) {
-    const size_t lds = (size_t)(2 * a.E + 1) * 4;
+    const size_t lds = (size_t)(a.E + 1) * 4;
     if (a.dtype == MEP_BF16)
       balance_kernel<uint16_t, lpt(), epl()><<<blocks, kBalanceThreads, lds, s>>>(a);
     else

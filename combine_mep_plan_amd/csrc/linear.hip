@@ -199,6 +199,56 @@ struct Place {
   int64_t row0;
 };
 
+// Row tiles of `size` rows before each expert, by the block's first wave;
+// everyone waits.
+__device__ __forceinline__ void count_row_tiles(const TileArgs& a, int size, int32_t* first) {
+  const int tid = threadIdx.x;
+  if (tid < kWave) {
+    int base = 0;
+    for (int e0 = 0; e0 < a.E; e0 += kWave) {
+      const int e = e0 + tid;
+      const int n = e < a.E ? (segment_rows(a, e) + size - 1) / size : 0;
+      int s = n;
+      for (int d = 1; d < kWave; d <<= 1) {
+        const int o = __shfl_up(s, d);
+        if (tid >= d) s += o;
+      }
+      if (e < a.E) first[e] = base + s - n;
+      base += __shfl(s, kWave - 1);
+    }
+    if (tid == 0) first[a.E] = base;
+  }
+  __syncthreads();
+}
+
+// The tile'th tile: experts in order, an expert's column tiles in order, the row
+// tiles that share a column tile next to each other.
+__device__ __forceinline__ Place find_tile(const TileArgs& a, const int32_t* first, int col_tiles,
+                                           int64_t tile) {
+  Place at;
+  int lo = 0, hi = a.E;  // the last expert whose tiles start at or before this one
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((int64_t)first[mid] * col_tiles <= tile) lo = mid; else hi = mid;
+  }
+  at.e = first_lane(lo);
+  const int mt = first[at.e + 1] - first[at.e];
+  const int q = (int)(tile - (int64_t)first[at.e] * col_tiles);
+  at.m = first_lane(q % mt);
+  at.n = first_lane(q / mt);
+  at.seg = segment_rows(a, at.e);
+  at.row0 = a.offsets[at.e];
+  return at;
+}
+
+template <int ACT>
+__device__ __forceinline__ float activate(float z, float up) {
+  return ACT == MEP_ACT_GELU       ? gelu(z)
+         : ACT == MEP_ACT_SILU     ? silu(z)
+         : ACT == MEP_ACT_SILU_GLU ? silu(z) * up
+                                   : z;
+}
+
 template <Mode MODE, bool FP8, int ACT, int WN, int WM, int TN, int TM, int PER_CU>
 __global__ __launch_bounds__(WN * WM * 64, 2 * PER_CU) void tile_kernel(TileArgs a) {
   using T = Tile<MODE, FP8, ACT, WN, WM, TN, TM>;
@@ -219,24 +269,7 @@ __global__ __launch_bounds__(WN * WM * 64, 2 * PER_CU) void tile_kernel(TileArgs
   const bool late = wave >= T::WAVES / 2;
   const int col_tiles = (a.cols + T::COLS - 1) / T::COLS;
 
-  if (MODE != kGradW) {
-    if (tid < kWave) {
-      int base = 0;
-      for (int e0 = 0; e0 < a.E; e0 += kWave) {
-        const int e = e0 + tid;
-        const int n = e < a.E ? (segment_rows(a, e) + BM - 1) / BM : 0;
-        int s = n;
-        for (int d = 1; d < kWave; d <<= 1) {
-          const int o = __shfl_up(s, d);
-          if (tid >= d) s += o;
-        }
-        if (e < a.E) first[e] = base + s - n;
-        base += __shfl(s, kWave - 1);
-      }
-      if (tid == 0) first[a.E] = base;
-    }
-    __syncthreads();
-  }
+  if (MODE != kGradW) count_row_tiles(a, BM, first);
   const int grad_w_tiles = (a.rows + BM - 1) / BM;
   const int64_t tiles = MODE == kGradW ? (int64_t)a.E * grad_w_tiles * col_tiles
                                        : (int64_t)first[a.E] * col_tiles;
@@ -259,20 +292,11 @@ __global__ __launch_bounds__(WN * WM * 64, 2 * PER_CU) void tile_kernel(TileArgs
       const int r = q - band * (4 * col_tiles);
       at.m = band * 4 + r % h;
       at.n = r / h;
+      at.seg = segment_rows(a, at.e);
+      at.row0 = a.offsets[at.e];
     } else {
-      int lo = 0, hi = a.E;  // the last expert whose tiles start at or before this one
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((int64_t)first[mid] * col_tiles <= tile) lo = mid; else hi = mid;
-      }
-      at.e = first_lane(lo);
-      const int mt = first[at.e + 1] - first[at.e];
-      const int q = (int)(tile - (int64_t)first[at.e] * col_tiles);
-      at.m = first_lane(q % mt);
-      at.n = first_lane(q / mt);
+      at = find_tile(a, first, col_tiles, tile);
     }
-    at.seg = segment_rows(a, at.e);
-    at.row0 = a.offsets[at.e];
   };
 
   // Where this lane's pieces of the two tiles come from, as offsets from bases
@@ -608,11 +632,7 @@ __global__ __launch_bounds__(WN * WM * 64, 2 * PER_CU) void tile_kernel(TileArgs
             zv[f][0] = u32x2{pack_bf16_rne(v[0], v[1]), pack_bf16_rne(v[2], v[3])};
             if (GLU) zv[f][GLU ? 1 : 0] = u32x2{pack_bf16_rne(up[0], up[1]), pack_bf16_rne(up[2], up[3])};
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              v[q] = ACT == MEP_ACT_GELU   ? gelu(v[q])
-                     : ACT == MEP_ACT_SILU ? silu(v[q])
-                     : GLU                 ? silu(v[q]) * up[q]
-                                           : v[q];
+            for (int q = 0; q < 4; ++q) v[q] = activate<ACT>(v[q], up[q]);
             const int c = col + f * 16 + g * 4;
             if (a.residual && in && c < a.cols) {
               const u32x2 res = *reinterpret_cast<const u32x2*>(a.residual + row * a.cols + c);
@@ -699,6 +719,146 @@ __global__ __launch_bounds__(WN * WM * 64, 2 * PER_CU) void tile_kernel(TileArgs
     }
     if (active) finish(done);
     if (!more) break;
+  }
+}
+
+// ---- few rows -----------------------------------------------------------------
+
+// A block takes 16 rows of a segment and 32 weight rows (gated: 16 and the 16
+// they gate) and splits the summed index over its 8 waves; operands go from
+// memory straight to registers, 8 loads of 1 KiB of the weight a wave in flight,
+// and the waves join in order through LDS.  For single tokens there is nothing
+// to share in LDS, and what counts is that every CU reads weights from the first
+// moment on: one token, 2 experts of 1024 x 7168, took 37.5 us in 16 tiles of
+// 128 x 128.
+constexpr int kFewRows = 16, kFewWaves = 8;
+
+template <bool FP8, int ACT>
+__global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(TileArgs a) {
+  constexpr bool GLU = ACT == MEP_ACT_SILU_GLU;
+  constexpr int COLS = GLU ? 16 : 32;
+  constexpr int STEP = FP8 ? 128 : 32, AHEAD = FP8 ? 2 : 4;
+  constexpr int SIZE = FP8 ? 1 : 2;
+  __shared__ f32x4 join[kFewWaves][2][kWave];
+  extern __shared__ int32_t first[];
+  const int lane = threadIdx.x & 63, wave = first_lane(threadIdx.x >> 6);
+  const int g = lane >> 4, r16 = lane & 15;
+  count_row_tiles(a, kFewRows, first);
+  const int col_tiles = (a.cols + COLS - 1) / COLS;
+  const int64_t tiles = (int64_t)first[a.E] * col_tiles;
+  const int depth = a.depth, blocks = depth / 128;
+  const int steps = (depth + STEP - 1) / STEP;
+  const int k0 = (int)((int64_t)steps * wave / kFewWaves);
+  const int k1 = (int)((int64_t)steps * (wave + 1) / kFewWaves);
+
+  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const Place at = find_tile(a, first, col_tiles, tile);
+    const int64_t xr = at.row0 + min(at.m * kFewRows + r16, at.seg - 1);
+    const unsigned char* px = a.b + xr * depth * SIZE;
+    int wr[2];
+    const unsigned char* pw[2];
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      const int c = min(at.n * COLS + (GLU ? 0 : f * 16) + r16, a.cols - 1);
+      wr[f] = GLU && f ? a.cols + c : c;
+      pw[f] = a.a + ((int64_t)at.e * a.Nz + wr[f]) * depth * SIZE;
+    }
+    f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
+    for (int k = k0; k < k1; k += AHEAD) {
+      if constexpr (FP8) {
+        i32x8 x[AHEAD], w[2][AHEAD];
+        float sx[AHEAD], sw[2][AHEAD];
+        auto get = [&](const unsigned char* p, int kk) {
+          const u32x4 lo = *reinterpret_cast<const u32x4*>(p + (int64_t)kk * 128 + g * 32);
+          const u32x4 hi = *reinterpret_cast<const u32x4*>(p + (int64_t)kk * 128 + g * 32 + 16);
+          return __builtin_bit_cast(i32x8,
+                                    __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        };
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+          const int kk = min(k + u, k1 - 1);
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            w[f][u] = get(pw[f], kk);
+            sw[f][u] = a.a_scales[((int64_t)at.e * (a.Nz / 128) + wr[f] / 128) * blocks + kk];
+          }
+          x[u] = get(px, kk);
+          sx[u] = a.b_scales[xr * blocks + kk];
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            const f32x4 p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                w[f][u], x[u], f32x4{0, 0, 0, 0}, 0, 0, 0, 0, 0, 0);
+            // all 16 weight rows lie in one block of 128
+            const float sc = k + u < k1 ? sw[f][u] * sx[u] : 0.0f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[f][q] = k + u < k1 ? fmaf(p[q], sc, acc[f][q]) : acc[f][q];
+          }
+        }
+      } else {
+        u32x4 x[AHEAD], w[2][AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+          const int kk = (k + u) * 32 + g * 8;
+          const int64_t at_k = (int64_t)min(kk, depth - 8) * 2;
+#pragma unroll
+          for (int f = 0; f < 2; ++f) w[f][u] = *reinterpret_cast<const u32x4*>(pw[f] + at_k);
+          x[u] = *reinterpret_cast<const u32x4*>(px + at_k);
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+          const bool in = k + u < k1 && (k + u) * 32 + g * 8 < depth;
+          const bf16x8 xv = __builtin_bit_cast(bf16x8, in ? x[u] : zero4());
+#pragma unroll
+          for (int f = 0; f < 2; ++f)
+            acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                __builtin_bit_cast(bf16x8, in ? w[f][u] : zero4()), xv, acc[f], 0, 0, 0);
+        }
+      }
+    }
+    join[wave][0][lane] = acc[0];
+    join[wave][1][lane] = acc[1];
+    __syncthreads();
+    // gated: one wave has both halves; otherwise a wave for each fragment
+    if (wave < (GLU ? 1 : 2)) {
+      const int f = GLU ? 0 : wave;
+      f32x4 z = join[0][f][lane], up = join[0][1][lane];
+#pragma unroll
+      for (int q = 1; q < kFewWaves; ++q) {
+        z += join[q][f][lane];
+        if (GLU) up += join[q][1][lane];
+      }
+      const int r = at.m * kFewRows + r16, col = at.n * COLS + f * 16 + g * 4;
+      if (r < at.seg && col < a.cols) {
+        const int64_t row = at.row0 + r;
+        if (a.bias) {
+          const float* b = a.bias + (int64_t)at.e * a.Nz + col;
+          z += *reinterpret_cast<const f32x4*>(b);
+          if (GLU) up += *reinterpret_cast<const f32x4*>(b + a.cols);
+        }
+        if (a.z) {
+          uint16_t* zp = a.z + row * a.Nz + col;
+          *reinterpret_cast<u32x2*>(zp) =
+              u32x2{pack_bf16_rne(z[0], z[1]), pack_bf16_rne(z[2], z[3])};
+          if (GLU)
+            *reinterpret_cast<u32x2*>(zp + a.cols) =
+                u32x2{pack_bf16_rne(up[0], up[1]), pack_bf16_rne(up[2], up[3])};
+        }
+        float v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = activate<ACT>(z[q], up[q]);
+        if (a.residual) {
+          const u32x2 res = *reinterpret_cast<const u32x2*>(a.residual + row * a.cols + col);
+          v[0] += bf16_lo(res[0]); v[1] += bf16_hi(res[0]);
+          v[2] += bf16_lo(res[1]); v[3] += bf16_hi(res[1]);
+        }
+        *reinterpret_cast<u32x2*>(a.out + row * a.cols + col) =
+            u32x2{pack_bf16_rne(v[0], v[1]), pack_bf16_rne(v[2], v[3])};
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -838,13 +998,35 @@ void run_sized(const TileArgs& a, int64_t rows, hipStream_t s) {
   else run_tiles<MODE, FP8, ACT, 4, 2, 2>(a, rows, s);
 }
 
+// Few rows: up to 16 an expert where small tiles are no more than the CUs.
+// Measured (us, tiles / few rows): one token over 8 experts of 4096 x 7168, 256
+// tiles, 103 and 94 (E4M3 38.5 and 40.3), 2 experts of 1024 x 7168 36.5 and 19.2
+// (28.1 and 12.2), one of 7168 x 2048 13.7 and 8.8 (11.2 and 5.8); 16 tokens over
+// 64 experts of 4096 x 7168, 2048 tiles, 566 and 637; 33 rows of one expert 15.9
+// and 20.7.
+template <bool FP8, int ACT>
+void run_forward(const TileArgs& a, int64_t rows, hipStream_t s) {
+  using Small = Tile<kForward, FP8, ACT, 2, 4, 4, 2>;
+  if (rows <= kFewRows * std::min<int64_t>(a.E, rows) &&
+      count_tiles<Small>(a, kForward, rows) <= kCus) {
+    constexpr int COLS = ACT == MEP_ACT_SILU_GLU ? 16 : 32;
+    const int64_t tiles =
+        (a.cols + COLS - 1) / COLS * row_tiles_bound(rows, a.E, kFewRows);
+    const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(tiles, 4 * kCus));
+    few_rows_kernel<FP8, ACT>
+        <<<grid, kFewWaves * 64, (size_t)(a.E + 1) * sizeof(int32_t), s>>>(a);
+  } else {
+    run_sized<kForward, FP8, ACT>(a, rows, s);
+  }
+}
+
 template <bool FP8>
 void run_forward(const TileArgs& t, int act, int64_t rows, hipStream_t s) {
   switch (act) {
-    case MEP_ACT_NONE: run_sized<kForward, FP8, MEP_ACT_NONE>(t, rows, s); break;
-    case MEP_ACT_GELU: run_sized<kForward, FP8, MEP_ACT_GELU>(t, rows, s); break;
-    case MEP_ACT_SILU: run_sized<kForward, FP8, MEP_ACT_SILU>(t, rows, s); break;
-    default: run_sized<kForward, FP8, MEP_ACT_SILU_GLU>(t, rows, s);
+    case MEP_ACT_NONE: run_forward<FP8, MEP_ACT_NONE>(t, rows, s); break;
+    case MEP_ACT_GELU: run_forward<FP8, MEP_ACT_GELU>(t, rows, s); break;
+    case MEP_ACT_SILU: run_forward<FP8, MEP_ACT_SILU>(t, rows, s); break;
+    default: run_forward<FP8, MEP_ACT_SILU_GLU>(t, rows, s);
   }
 }
 

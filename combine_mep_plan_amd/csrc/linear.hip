@@ -54,6 +54,14 @@ struct TileArgs {
   int32_t Nz;
 };
 
+// The lane's number, worked out anew where it stands: kept in registers over the
+// products, it and what follows from it would push others out to memory.
+__device__ __forceinline__ int fresh_lane() {
+  int l;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=&v"(l));
+  return l;
+}
+
 // Rows of segment e that exist (rows past cap_em are left out).
 __device__ __forceinline__ int segment_rows(const TileArgs& a, int e) {
   const int64_t off = a.offsets[e], left = a.cap - off;
@@ -121,6 +129,11 @@ __device__ __forceinline__ int turned_swizzle(int k) {
 template <Mode MODE, bool FP8, int ACT, int WN, int WM, int TN, int TM>
 struct Tile {
   static constexpr bool GLU = MODE == kForward && ACT == MEP_ACT_SILU_GLU;
+  // Forward: an odd last step runs outside the phases, with what is left of the
+  // summed index; as another way into the loops the compiler would add waits
+  // for it there.  Its depth is a layer's, most often a multiple of two steps;
+  // the gradients' are the rows of a segment.
+  static constexpr bool EVEN = MODE == kForward;
   static constexpr bool A_TURNED = MODE != kForward, B_TURNED = MODE == kGradW;
   static constexpr int WAVES = WN * WM, THREADS = WAVES * 64;
   static constexpr int BN = WN * TN * 16, BM = WM * TM * 16;
@@ -263,9 +276,8 @@ __global__ __launch_bounds__(WN * WM * 64, 2 * PER_CU) void tile_kernel(TileArgs
   __shared__ __attribute__((aligned(1024))) unsigned char b1[BM * 128 + T::SCALES * 4];
   extern __shared__ int32_t first[];         // [E+1]: row tiles before each expert
 
-  const int tid = threadIdx.x, lane = tid & 63, wave = first_lane(tid >> 6);
+  const int wave = first_lane(threadIdx.x >> 6);
   const int wn = wave % WN, wm = wave / WN;
-  const int g = lane >> 4, r16 = lane & 15;
   const bool late = wave >= T::WAVES / 2;
   const int col_tiles = (a.cols + T::COLS - 1) / T::COLS;
 
@@ -280,7 +292,7 @@ __global__ __launch_bounds__(WN * WM * 64, 2 * PER_CU) void tile_kernel(TileArgs
   if (tile >= tiles) return;
 
   Place at;
-  auto locate = [&] {
+  auto locate = [&]() __attribute__((always_inline)) {
     if (MODE == kGradW) {
       const int per_e = grad_w_tiles * col_tiles;
       at.e = (int)(tile / per_e);
@@ -308,8 +320,8 @@ __global__ __launch_bounds__(WN * WM * 64, 2 * PER_CU) void tile_kernel(TileArgs
   int64_t stepa, stepb;
   int steps, left;    // whole steps; what is left of the summed index behind them
   constexpr int UA = BN / 16, UB = BM / 8;  // 16-byte units in a row of a turned tile
-  const int du = (lane & 7) ^ (lane >> 3);
-  auto setup = [&] {
+  auto setup = [&]() __attribute__((always_inline)) {
+    const int lane = fresh_lane(), du = (lane & 7) ^ (lane >> 3);
     const int depth = MODE == kGradW ? at.seg : a.depth;
     steps = depth / T::VALS;
     left = depth % T::VALS;
@@ -376,13 +388,13 @@ __global__ __launch_bounds__(WN * WM * 64, 2 * PER_CU) void tile_kernel(TileArgs
       }
     }
   };
-  auto load_a = [&](unsigned char* la, int h) {
+  auto load_a = [&](unsigned char* la, int h) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < RA; ++i)
       load_to_lds(base_a, oa[h][i], la + (i * T::WAVES + wave) * 1024);
     if (h == 1) base_a += stepa;
   };
-  auto load_b = [&](unsigned char* lb, int h) {
+  auto load_b = [&](unsigned char* lb, int h) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = h * RB; i < (h + 1) * RB; ++i)
       load_to_lds(base_b, ob[i], lb + (i * T::WAVES + wave) * 1024);
@@ -393,25 +405,36 @@ __global__ __launch_bounds__(WN * WM * 64, 2 * PER_CU) void tile_kernel(TileArgs
     if (h == 1) base_b += stepb;
   };
   constexpr int kRows = 2 * RB + (FP8 ? 1 : 0);  // loads of a step's rows
-  // a tile's loads before its first phase
+  // A tile's loads before its first phase.  Steps alternate between the two
+  // buffers so that the last one finds the second, the first one therefore
+  // either.
   auto prologue = [&] {
-    if (steps > 0) {
-      load_b(b0, 0);
-      load_b(b0, 1);
-      load_a(a00, 0);
-      load_a(a01, 1);
-    }
-    if (steps > 1) {
-      load_b(b1, 0);
-      load_b(b1, 1);
-      if (late) load_a(a10, 0);
+    auto both = [&](unsigned char* a_0, unsigned char* a_1, unsigned char* b,
+                    unsigned char* nb) __attribute__((always_inline)) {
+      load_b(b, 0);
+      load_b(b, 1);
+      load_a(a_0, 0);
+      load_a(a_1, 1);
+      if (steps > 1) {
+        load_b(nb, 0);
+        load_b(nb, 1);
+      }
+    };
+    // the comments keep the compiler from joining the two ways' ends, which
+    // would hide from it which arrays the loads fill
+    if (!T::EVEN && (steps & 1)) {
+      both(a10, a11, b1, b0);
+      asm volatile("; second buffer first" ::: "memory");
+    } else if (steps > (T::EVEN ? 1 : 0)) {
+      both(a00, a01, b0, b1);
+      asm volatile("; first buffer first" ::: "memory");
     }
   };
   // a part of a step through registers, zeros past the end of the summed index
   auto load_tail = [&](unsigned char* lds, const unsigned char* base, uint32_t off, int c,
                        bool in) {
     const u32x4 v = in ? *reinterpret_cast<const u32x4*>(base + off) : zero4();
-    *reinterpret_cast<u32x4*>(lds + c * 1024 + lane * 16) = v;
+    *reinterpret_cast<u32x4*>(lds + c * 1024 + fresh_lane() * 16) = v;
   };
 
   // Operands: a step's rows stay in registers for both halves of the columns.
@@ -424,9 +447,10 @@ __global__ __launch_bounds__(WN * WM * 64, 2 * PER_CU) void tile_kernel(TileArgs
   // of each half)
   constexpr int BLOCKS = GLU ? 2 : 1;
   float scale[BLOCKS][TM];
-  Reader<BN / 2, T::A_TURNED, FP8, HN> reader_a(wn * HN * 16, lane);
-  Reader<BM, T::B_TURNED, FP8, TM> reader_b(wm * TM * 16, lane);
-  auto read_b = [&](const unsigned char* lb) {
+  Reader<BN / 2, T::A_TURNED, FP8, HN> reader_a(wn * HN * 16, fresh_lane());
+  Reader<BM, T::B_TURNED, FP8, TM> reader_b(wm * TM * 16, fresh_lane());
+  uint32_t scale_off = BM * 128 + (wm * TM * 16 + (fresh_lane() & 15)) * 4;
+  auto read_b = [&](const unsigned char* lb) __attribute__((always_inline)) {
     reader_b.refresh();
 #pragma unroll
     for (int j = 0; j < TM; ++j) {
@@ -438,15 +462,17 @@ __global__ __launch_bounds__(WN * WM * 64, 2 * PER_CU) void tile_kernel(TileArgs
       }
     }
     if constexpr (FP8) {
+      asm volatile("" : "+v"(scale_off));
       const float* ls = reinterpret_cast<const float*>(lb + BM * 128);
 #pragma unroll
       for (int j = 0; j < TM; ++j)
 #pragma unroll
         for (int q = 0; q < BLOCKS; ++q)
-          scale[q][j] = ls[BM + (wn * TN + q) * 4] * ls[(wm * TM + j) * 16 + r16];
+          scale[q][j] = ls[BM + (wn * TN + q) * 4] *
+                        *reinterpret_cast<const float*>(lb + scale_off + j * 64);
     }
   };
-  auto read_a = [&](const unsigned char* la) {
+  auto read_a = [&](const unsigned char* la) __attribute__((always_inline)) {
     reader_a.refresh();
 #pragma unroll
     for (int i = 0; i < HN; ++i) {
@@ -460,11 +486,11 @@ __global__ __launch_bounds__(WN * WM * 64, 2 * PER_CU) void tile_kernel(TileArgs
   };
   // zeros for the values from `valid` of the step's 64 on: what lies there may
   // be anything, infinities included
-  auto mask_values = [&](auto& frags, int valid) {
+  auto mask_values = [&](auto& frags, int valid) __attribute__((always_inline)) {
     if constexpr (!FP8) {
 #pragma unroll
       for (int s = 0; s < SUB; ++s) {
-        const int v = valid - s * 32 - g * 8;
+        const int v = valid - s * 32 - (fresh_lane() >> 4) * 8;
         u32x4 mask;
 #pragma unroll
         for (int d = 0; d < 4; ++d)
@@ -477,7 +503,7 @@ __global__ __launch_bounds__(WN * WM * 64, 2 * PER_CU) void tile_kernel(TileArgs
   };
   // `meanwhile` is issued behind the first MFMAs, so that the matrix cores do
   // not wait for it
-  auto multiply = [&](int half, auto meanwhile) {
+  auto multiply = [&](int half, auto meanwhile) __attribute__((always_inline)) {
     if constexpr (FP8) {
       // a product of 128 is scaled and added while the matrix cores work on
       // the next
@@ -532,73 +558,77 @@ __global__ __launch_bounds__(WN * WM * 64, 2 * PER_CU) void tile_kernel(TileArgs
   //   t + 2, t + 3: the rows of step k + 2,  t + 4, t + 5: its columns,
   // and wait at t + 3 for rows and first columns of step k + 1 and at t + 1
   // for the other columns of step k, leaving what was issued later in flight.
-  // DRAIN: the last steps, `togo` of them behind this one, where the loads end.
-  auto run = [&](auto late_, auto active_) {
+  // MORE: how many steps follow, as far as loads for them are concerned (2, or
+  // in the last two steps, where the loads drain, 1 and 0).
+  auto run = [&](auto late_, auto active_) __attribute__((always_inline)) {
     constexpr bool LATE = late_(), ACTIVE = active_();
-    auto step = [&](auto drain_, int togo, unsigned char* a_0, unsigned char* a_1,
-                    unsigned char* b, unsigned char* na_0, unsigned char* na_1) {
-      constexpr bool DRAIN = drain_();
-      const bool more1 = !DRAIN || togo >= 1, more2 = !DRAIN || togo >= 2;
-      const bool mask = MODE == kGradW && DRAIN && togo == 0 && left < 0;
-      auto multiplying = [&](int half, auto meanwhile) {
+    auto step = [&](auto more_, unsigned char* a_0, unsigned char* a_1, unsigned char* b,
+                    unsigned char* na_0, unsigned char* na_1) __attribute__((always_inline)) {
+      constexpr int MORE = more_();
+      const bool mask = MODE == kGradW && MORE == 0 && left < 0;
+      auto multiplying = [&](int half, auto meanwhile) __attribute__((always_inline)) {
         __builtin_amdgcn_s_setprio(1);
         if (ACTIVE) multiply(half, meanwhile);
         else meanwhile();
         __builtin_amdgcn_s_setprio(0);
       };
-      auto wait_second = [&] {
-        if (more1) __builtin_amdgcn_s_waitcnt(loads_left(kRows + 2 * RA));
-        else __builtin_amdgcn_s_waitcnt(loads_left(0));
-      };
-      auto wait_first = [&] {
-        if (more2) __builtin_amdgcn_s_waitcnt(loads_left(kRows + RA));
-        else __builtin_amdgcn_s_waitcnt(loads_left(RA));
-      };
+      constexpr int kSecond = MORE >= 1 ? kRows + 2 * RA : 0;
+      constexpr int kFirst = MORE >= 2 ? kRows + RA : RA;
       if (ACTIVE) { read_b(b); read_a(a_0); }
-      if (more1) load_a(LATE ? na_1 : na_0, LATE ? 1 : 0);
+      if (MORE >= 1) load_a(LATE ? na_1 : na_0, LATE ? 1 : 0);
       __builtin_amdgcn_s_waitcnt(kAllLdsReads);
       if (ACTIVE && mask) { mask_values(bv, left + T::VALS); mask_values(av, left + T::VALS); }
-      if (LATE) wait_second();
+      if (LATE) __builtin_amdgcn_s_waitcnt(loads_left(kSecond));
       phase_end();
       multiplying(0, [&] {
-        if (LATE) { if (more2) load_b(b, 0); }
-        else if (more1) load_a(na_1, 1);
+        if (LATE) { if (MORE >= 2) load_b(b, 0); }
+        else if (MORE >= 1) load_a(na_1, 1);
       });
-      if (!LATE) wait_second();
+      if (!LATE) __builtin_amdgcn_s_waitcnt(loads_left(kSecond));
       phase_end();
       if (ACTIVE) read_a(a_1);
-      if (more2) load_b(b, LATE ? 1 : 0);
+      if (MORE >= 2) load_b(b, LATE ? 1 : 0);
       __builtin_amdgcn_s_waitcnt(kAllLdsReads);
       if (ACTIVE && mask) mask_values(av, left + T::VALS);
-      if (LATE) wait_first();
+      if (LATE) __builtin_amdgcn_s_waitcnt(loads_left(kFirst));
       phase_end();
       multiplying(1, [&] {
-        if (more2) { if (LATE) load_a(a_0, 0); else load_b(b, 1); }
+        if (MORE >= 2) { if (LATE) load_a(a_0, 0); else load_b(b, 1); }
       });
-      if (!LATE) wait_first();
+      if (!LATE) __builtin_amdgcn_s_waitcnt(loads_left(kFirst));
       phase_end();
     };
-    using Yes = std::true_type;
-    using No = std::false_type;
-    if (LATE) phase_end();
-    int togo = steps - 1;
-    for (; togo > 2; togo -= 2) {
-      step(No{}, togo, a00, a01, b0, a10, a11);
-      step(No{}, togo - 1, a10, a11, b1, a00, a01);
+    using Two = std::integral_constant<int, 2>;
+    using One = std::integral_constant<int, 1>;
+    using None = std::integral_constant<int, 0>;
+    if (LATE) {
+      if (!T::EVEN && (steps & 1)) {
+        if (steps > 1) load_a(a00, 0);
+        asm volatile("; second buffer first" ::: "memory");
+      } else {
+        load_a(a10, 0);
+        asm volatile("; first buffer first" ::: "memory");
+      }
+      phase_end();
     }
-    while (true) {
-      step(Yes{}, togo, a00, a01, b0, a10, a11);
-      if (--togo < 0) break;
-      step(Yes{}, togo, a10, a11, b1, a00, a01);
-      if (--togo < 0) break;
+    if (!T::EVEN && (steps & 1) && steps > 1) step(Two{}, a10, a11, b1, a00, a01);
+    for (int k = steps & ~1; k > 2; k -= 2) {
+      step(Two{}, a00, a01, b0, a10, a11);
+      step(Two{}, a10, a11, b1, a00, a01);
     }
+    if (steps > 1) step(One{}, a00, a01, b0, a10, a11);
+    step(None{}, a10, a11, b1, a00, a01);
     if (!LATE) phase_end();
+    // nothing is left in flight; said here, the compiler knows it on every way
+    // that leads to the other groups' loops and inserts no waits of its own
+    __builtin_amdgcn_s_waitcnt(loads_left(0));
   };
 
   // A tile's rows and columns in place: activation and what goes with it, and
   // the stores.  A lane has 4 consecutive columns of row r16 in each fragment;
   // two fragments exchange rows of 16 lanes so that it stores 8 of one.
-  auto finish = [&](const Place& at) {
+  auto finish = [&](const Place& at) __attribute__((always_inline)) {
+    const int lane = fresh_lane(), g = lane >> 4, r16 = lane & 15;
     const int rows = MODE == kGradW ? a.rows : at.seg;
     const int64_t out0 = MODE == kGradW ? (int64_t)at.e * rows : at.row0;
 #pragma unroll
@@ -671,7 +701,7 @@ __global__ __launch_bounds__(WN * WM * 64, 2 * PER_CU) void tile_kernel(TileArgs
       for (int j = 0; j < TM; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
     __builtin_amdgcn_s_waitcnt(loads_left(0));
     phase_end();
-    if (steps > 0) {
+    if (steps > (T::EVEN ? 1 : 0)) {
       using Yes = std::true_type;
       using No = std::false_type;
       if (late) {
@@ -680,24 +710,35 @@ __global__ __launch_bounds__(WN * WM * 64, 2 * PER_CU) void tile_kernel(TileArgs
         if (active) run(No{}, Yes{}); else run(No{}, No{});
       }
     }
-    if (!FP8 && left > 0) {
-      // bases stand behind the last whole step
-      const auto in_a = [&](int c) {
-        return T::A_TURNED ? c * (64 / UA) + lane / UA < left : du * T::UNIT < left;
-      };
+    // bases stand behind the last step of the phases
+    int whole = T::EVEN ? steps & 1 : 0;
+    for (int rest = whole + (left > 0 ? 1 : 0); rest > 0; --rest, whole = 0) {
+      if (whole) {
+        load_b(b0, 0);
+        load_b(b0, 1);
+        load_a(a00, 0);
+        load_a(a01, 1);
+        __builtin_amdgcn_s_waitcnt(loads_left(0));
+      } else {
+        const int lane = fresh_lane(), du = (lane & 7) ^ (lane >> 3);
+        const auto in_a = [&](int c) {
+          return T::A_TURNED ? c * (64 / UA) + lane / UA < left : du * T::UNIT < left;
+        };
 #pragma unroll
-      for (int i = 0; i < RA; ++i) {
-        const int c = i * T::WAVES + wave;
-        load_tail(a00, base_a, oa[0][i], c, in_a(c));
-        load_tail(a01, base_a, oa[1][i], c, in_a(c));
-      }
+        for (int i = 0; i < RA; ++i) {
+          const int c = i * T::WAVES + wave;
+          load_tail(a00, base_a, oa[0][i], c, in_a(c));
+          load_tail(a01, base_a, oa[1][i], c, in_a(c));
+        }
 #pragma unroll
-      for (int i = 0; i < 2 * RB; ++i) {
-        const int c = i * T::WAVES + wave;
-        load_tail(b0, base_b, ob[i], c,
-                  T::B_TURNED ? c * (64 / UB) + lane / UB < left : du * T::UNIT < left);
+        for (int i = 0; i < 2 * RB; ++i) {
+          const int c = i * T::WAVES + wave;
+          load_tail(b0, base_b, ob[i], c,
+                    T::B_TURNED ? c * (64 / UB) + lane / UB < left : du * T::UNIT < left);
+        }
+        __builtin_amdgcn_s_waitcnt(kAllLdsReads);  // LDS writes count there too
       }
-      __syncthreads();
+      phase_end();
       if (active) {
         read_b(b0);
         read_a(a00);
@@ -705,7 +746,8 @@ __global__ __launch_bounds__(WN * WM * 64, 2 * PER_CU) void tile_kernel(TileArgs
         read_a(a01);
         multiply(1, [] {});
       }
-      __syncthreads();
+      __builtin_amdgcn_s_waitcnt(kAllLdsReads);
+      phase_end();
     }
     // every read of the buffers is done: the next tile's first loads run while
     // this one is stored
@@ -890,40 +932,52 @@ __global__ __launch_bounds__(256) void grad_z_kernel(LinearBackwardArgs a) {
       const uint16_t* z = reinterpret_cast<const uint16_t*>(a.z);
       uint16_t* gz = reinterpret_cast<uint16_t*>(a.grad_z);
       const int64_t stop = min(end, r0 + wave * 32 + 32);
-      for (int64_t r = r0 + wave * 32; r < stop; ++r) {
-        const u32x4 gq = *reinterpret_cast<const u32x4*>(gy + r * a.N + col);
-        u32x4 zq = zero4(), uq = zero4();
-        if (ACT != MEP_ACT_NONE) zq = *reinterpret_cast<const u32x4*>(z + r * a.Nz + col);
-        if (GLU) uq = *reinterpret_cast<const u32x4*>(z + r * a.Nz + a.N + col);
-        float d[8], du[8];
+      // AHEAD rows' loads in flight: one at a time, a block waits 32 times
+      constexpr int AHEAD = ACT == MEP_ACT_NONE ? 8 : 4;
+      for (int64_t r1 = r0 + wave * 32; r1 < stop; r1 += AHEAD) {
+        u32x4 gq[AHEAD], zq[AHEAD], uq[AHEAD];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          const float g = q & 1 ? bf16_hi(gq[q >> 1]) : bf16_lo(gq[q >> 1]);
-          const float v = q & 1 ? bf16_hi(zq[q >> 1]) : bf16_lo(zq[q >> 1]);
-          const float u = q & 1 ? bf16_hi(uq[q >> 1]) : bf16_lo(uq[q >> 1]);
-          du[q] = 0.0f;
-          if (ACT == MEP_ACT_GELU) {
-            d[q] = g * (0.5f * (1.0f + erff(v * 0.70710678118654752f)) +
-                        v * expf(-0.5f * v * v) * 0.39894228040143268f);
-          } else if (ACT == MEP_ACT_SILU || GLU) {
-            const float sg = 1.0f / (1.0f + expf(-v));
-            const float slope = sg * (1.0f + v * (1.0f - sg));
-            d[q] = GLU ? g * u * slope : g * slope;
-            if (GLU) du[q] = g * (v * sg);
-          } else {
-            d[q] = g;
-          }
-          s0[q] += d[q];
-          s1[q] += du[q];
+        for (int t = 0; t < AHEAD; ++t) {
+          const int64_t r = min(r1 + t, stop - 1);
+          gq[t] = *reinterpret_cast<const u32x4*>(gy + r * a.N + col);
+          zq[t] = uq[t] = zero4();
+          if (ACT != MEP_ACT_NONE) zq[t] = *reinterpret_cast<const u32x4*>(z + r * a.Nz + col);
+          if (GLU) uq[t] = *reinterpret_cast<const u32x4*>(z + r * a.Nz + a.N + col);
         }
-        if (ACT != MEP_ACT_NONE)
-          *reinterpret_cast<u32x4*>(gz + r * a.Nz + col) =
-              u32x4{pack_bf16_rne(d[0], d[1]), pack_bf16_rne(d[2], d[3]), pack_bf16_rne(d[4], d[5]),
-                    pack_bf16_rne(d[6], d[7])};
-        if (GLU)
-          *reinterpret_cast<u32x4*>(gz + r * a.Nz + a.N + col) =
-              u32x4{pack_bf16_rne(du[0], du[1]), pack_bf16_rne(du[2], du[3]),
-                    pack_bf16_rne(du[4], du[5]), pack_bf16_rne(du[6], du[7])};
+#pragma unroll
+        for (int t = 0; t < AHEAD; ++t) {
+          const int64_t r = r1 + t;
+          if (r >= stop) break;
+          float d[8], du[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float g = q & 1 ? bf16_hi(gq[t][q >> 1]) : bf16_lo(gq[t][q >> 1]);
+            const float v = q & 1 ? bf16_hi(zq[t][q >> 1]) : bf16_lo(zq[t][q >> 1]);
+            const float u = q & 1 ? bf16_hi(uq[t][q >> 1]) : bf16_lo(uq[t][q >> 1]);
+            du[q] = 0.0f;
+            if (ACT == MEP_ACT_GELU) {
+              d[q] = g * (0.5f * (1.0f + erff(v * 0.70710678118654752f)) +
+                          v * expf(-0.5f * v * v) * 0.39894228040143268f);
+            } else if (ACT == MEP_ACT_SILU || GLU) {
+              const float sg = 1.0f / (1.0f + expf(-v));
+              const float slope = sg * (1.0f + v * (1.0f - sg));
+              d[q] = GLU ? g * u * slope : g * slope;
+              if (GLU) du[q] = g * (v * sg);
+            } else {
+              d[q] = g;
+            }
+            s0[q] += d[q];
+            s1[q] += du[q];
+          }
+          if (ACT != MEP_ACT_NONE)
+            *reinterpret_cast<u32x4*>(gz + r * a.Nz + col) =
+                u32x4{pack_bf16_rne(d[0], d[1]), pack_bf16_rne(d[2], d[3]),
+                      pack_bf16_rne(d[4], d[5]), pack_bf16_rne(d[6], d[7])};
+          if (GLU)
+            *reinterpret_cast<u32x4*>(gz + r * a.Nz + a.N + col) =
+                u32x4{pack_bf16_rne(du[0], du[1]), pack_bf16_rne(du[2], du[3]),
+                      pack_bf16_rne(du[4], du[5]), pack_bf16_rne(du[6], du[7])};
+        }
       }
     }
     if (!a.grad_bias) continue;

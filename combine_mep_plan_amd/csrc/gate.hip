@@ -543,7 +543,7 @@ __host__ __device__ constexpr int column_share(int E) {
   return E <= 64 ? 8 : E <= 128 ? 4 : E <= 256 ? 2 : 1;
 }
 
-template <class TL, int LPT, int EPL>
+template <class TL, int LPT, int EPL, bool WIDE>
 __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a) {
   constexpr int GROUPS = kBalanceThreads / LPT;
   __shared__ __attribute__((aligned(16)))
@@ -559,20 +559,42 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
   for (int i = 0; i < EPL; ++i) acc[i] = 0.0f;
   const TL* logits = reinterpret_cast<const TL*>(a.logits);
   const int64_t step = (int64_t)gridDim.x * GROUPS;
-  auto load = [&](int64_t t, float (&x)[EPL]) {
-    load_row<TL, LPT, EPL>(logits + min(t, (int64_t)a.T - 1) * E, E, l, a.wide, -__builtin_inff(),
-                           x);
+  // Two rows in turn: one is worked on while the other's loads run.  They are
+  // taken as they lie in memory, without a branch, and looked at only when it is
+  // their turn: anything else would wait for them at once.
+  constexpr int V = Vec<TL>::V;
+  struct Row {
+    std::conditional_t<WIDE, u32x4, TL> raw[WIDE ? EPL / V : EPL];
+    int32_t e;  // the lane's named expert
+    uint8_t valid;
   };
-  float next[EPL];
-  int64_t t = (int64_t)blockIdx.x * GROUPS + g;
-  if (t < a.T) load(t, next);
-  for (; t < a.T; t += step) {
+  const uint8_t* mask = a.mask ? a.mask : reinterpret_cast<const uint8_t*>(a.indices);
+  auto load = [&](int64_t t, Row& r) __attribute__((always_inline)) {
+    const int64_t at = min(t, (int64_t)a.T - 1);
+    const TL* p = logits + at * E;
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int c = 0; c < EPL / V; ++c)
+        r.raw[c] = *reinterpret_cast<const u32x4*>(p + min((c * LPT + l) * V, E - V));
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) r.raw[i] = p[min(expert_of<TL, LPT>(i, l), E - 1)];
+    }
+    r.e = a.indices[at * a.k + min(l, a.k - 1)];
+    r.valid = mask[a.mask ? at : 0];
+  };
+  auto work = [&](int64_t t, const Row& r) __attribute__((always_inline)) {
+    if (a.mask && r.valid == 0) return;  // the same for all lanes of the group
     float x[EPL], p[EPL], m, inv;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) x[i] = next[i];
-    load(t + step, next);  // while this row is worked on
-    if (a.mask && a.mask[t] == 0) continue;  // the same for all lanes of the group
-    for (int j = l; j < a.k; j += LPT) {
+    for (int i = 0; i < EPL; ++i) {
+      if constexpr (!WIDE) x[i] = load_logit(&r.raw[i]);
+      else if constexpr (V == 4) x[i] = __uint_as_float(r.raw[i / V][i % V]);
+      else x[i] = i & 1 ? bf16_hi(r.raw[i / V][i % V / 2]) : bf16_lo(r.raw[i / V][i % V / 2]);
+      if (expert_of<TL, LPT>(i, l) >= E) x[i] = -__builtin_inff();
+    }
+    if (l < a.k && r.e >= 0 && r.e < E) atomicAdd(&cnt[r.e], 1);
+    for (int j = l + LPT; j < a.k; j += LPT) {
       const int e = a.indices[t * a.k + j];
       if (e >= 0 && e < E) atomicAdd(&cnt[e], 1);
     }
@@ -580,6 +602,25 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
     probabilities<LPT, EPL, false>(x, a.score, p, m, inv);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) acc[i] += p[i] * inv;
+  };
+  int64_t t = (int64_t)blockIdx.x * GROUPS + g;
+  if constexpr (EPL == 64) {  // two would not fit the registers
+    for (; t < a.T; t += step) {
+      Row row;
+      load(t, row);
+      work(t, row);
+    }
+  } else if (t < a.T) {
+    Row even, odd;
+    load(t, even);
+    while (true) {
+      load(t + step, odd);
+      work(t, even);
+      if ((t += step) >= a.T) break;
+      load(t + step, even);
+      work(t, odd);
+      if ((t += step) >= a.T) break;
+    }
   }
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
@@ -623,16 +664,9 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
   __shared__ double join[kBalanceThreads];
   __shared__ int32_t join_cnt[kBalanceThreads];
   const int rows = (int)gridDim.x;
-  // valid tokens
+  // valid tokens: needed at the end, loaded now
   int32_t n = 0;
-  if (threadIdx.x < kWave) {
-    for (int r = lane; r < rows; r += kWave) n += a.part_cnt[(size_t)r * (E + 1) + E];
-    for (int d = 1; d < kWave; d <<= 1) n += __shfl_xor(n, d);
-    if (threadIdx.x == 0) join_cnt[0] = n;
-  }
-  __syncthreads();
-  n = join_cnt[0];
-  const double inv_n = n > 0 ? 1.0 / (double)n : 0.0;
+  for (int r = lane; r < rows; r += kWave) n += a.part_cnt[(size_t)r * (E + 1) + E];
   // `share` threads a column, each every share-th row
   const int share = column_share(E);
   const int width = kBalanceThreads / share;
@@ -661,6 +695,9 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
         }
       }
     }
+    if (e0 == 0)
+      for (int d = 1; d < kWave; d <<= 1) n += __shfl_xor(n, d);
+    const double inv_n = n > 0 ? 1.0 / (double)n : 0.0;
     __syncthreads();
     join[threadIdx.x] = s;
     join_cnt[threadIdx.x] = q;
@@ -684,6 +721,7 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
     double s = 0.0;
     for (int i = 0; i < kBalanceThreads / kWave; ++i) s += join[i];
     a.counts[E] = n;
+    const double inv_n = n > 0 ? 1.0 / (double)n : 0.0;
     a.loss[0] = (float)(s * inv_n * (double)a.coef * (double)E / (double)a.k);
     *a.done = 0u;  // ready for the next call on this workspace
   }
@@ -876,9 +914,9 @@ hipError_t launch_gate(const GateArgs& a0, hipStream_t s) {
 
 // Blocks: a pass over one token a group takes about 0.6 us, and each block's
 // arrival at the counter, which they reach one by one, about 0.08, so the square
-// root of 7.5 passes.  Measured at 4096 tokens (us): 256 experts 16.5 with 32
-// blocks and 19.7 with 64, 60 experts at 16384 tokens 18.4 with 64 and 25.9 with
-// 128.
+// root of 7.5 passes.  Measured with the square root of 4, of 7.5 and of 10 (us):
+// 4096 tokens over 256 experts 16.2, 15.9 and 17.6, 65536 tokens 39.9, 41.5 and
+// 43.6, 1024 tokens over 512 experts 16.0, 15.2 and 16.6.
 int balance_blocks(int E, int64_t T) {
   const int64_t groups = kBalanceThreads / lanes_of(E);
   const int64_t passes = std::max<int64_t>(1, (T + groups - 1) / groups);
@@ -887,16 +925,22 @@ int balance_blocks(int E, int64_t T) {
   return (int)std::min(passes, b);
 }
 
-hipError_t launch_balance(const BalanceArgs& a0, hipStream_t s) {
-  BalanceArgs a = a0;
-  a.wide = is_wide(a.E, a.dtype);
+hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
   const unsigned blocks = (unsigned)balance_blocks(a.E, a.T);
   by_experts(a.E, [&](auto lpt, auto epl) {
     const size_t lds = (size_t)(a.E + 1) * 4;
-    if (a.dtype == MEP_BF16)
-      balance_kernel<uint16_t, lpt(), epl()><<<blocks, kBalanceThreads, lds, s>>>(a);
-    else
-      balance_kernel<float, lpt(), epl()><<<blocks, kBalanceThreads, lds, s>>>(a);
+    auto launch = [&](auto type, auto wide) {
+      balance_kernel<decltype(type), lpt(), epl(), wide()>
+          <<<blocks, kBalanceThreads, lds, s>>>(a);
+    };
+    const bool wide = is_wide(a.E, a.dtype);
+    using Yes = std::true_type;
+    using No = std::false_type;
+    if (a.dtype == MEP_BF16) {
+      if (wide) launch(uint16_t{}, Yes{}); else launch(uint16_t{}, No{});
+    } else {
+      if (wide) launch(float{}, Yes{}); else launch(float{}, No{});
+    }
   });
   return hipGetLastError();
 }

@@ -231,7 +231,6 @@ struct BalanceArgs {
   int32_t* part_cnt;            // [blocks][E+1]
   int32_t T, E, k, score, dtype;
   float coef;
-  bool wide;
 };
 
 struct GateBackwardArgs {

@@ -906,21 +906,25 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(TileArgs a) {
 
 // ---- gradient before the activation, and the bias' gradient -----------------
 
-// A block takes 128 rows of a segment and 512 columns of grad_y (8 a lane, 16
-// rows a wave) at a time: grad_z in bf16, and, where the bias wants it, the
-// column sums of the unrounded grad_z over those rows.  Bound by memory where it
-// is large: 16384 rows, 2 x 2048 gated columns, 335 MB in 115 us; where it is
-// small by the rows' loads one after the other, so 8 waves share them (602 rows
-// of 520 columns 8.4 us; 4 waves 12.3, and 108 in the large case).
-constexpr int kGradZWaves = 8, kGradZRows = kSegRows / kGradZWaves;
+// A block takes rows of a segment and 512 columns of grad_y (8 a lane) at a time:
+// grad_z in bf16, and, where the bias wants it, the column sums of the unrounded
+// grad_z over those rows, 128 then.  Without, 32 rows: smaller blocks fill the
+// CUs more evenly (16384 rows of 2 x 2048 gated columns, 335 MB: 97 us; 64 rows
+// 107, 128 rows 112).  Few rows are bound by the loads that follow one another,
+// so 8 waves share them (602 rows of 520 columns 7.8 us; 4 waves 12.3).
+constexpr int kGradZWaves = 8;
+
+// Rows a block takes.
+__host__ __device__ constexpr int grad_z_rows(bool bias) { return bias ? kSegRows : 32; }
 
 template <int ACT>
 __global__ __launch_bounds__(kGradZWaves * 64) void grad_z_kernel(LinearBackwardArgs a) {
   constexpr bool GLU = ACT == MEP_ACT_SILU_GLU;
   __shared__ float part[kGradZWaves][GLU ? 2 : 1][512];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int turn = 0; (blockIdx.x + (int64_t)turn * gridDim.x) * kSegRows < a.cap; ++turn) {
-    const int64_t blk = blockIdx.x + (int64_t)turn * gridDim.x, r0 = blk * kSegRows;
+  const int rows = grad_z_rows(a.grad_bias), share = rows / kGradZWaves;
+  for (int64_t blk = blockIdx.x; blk * rows < a.cap; blk += gridDim.x) {
+    const int64_t r0 = blk * rows;
     int lo = 0;  // the last segment that starts at or before r0
     for (int e0 = 0; e0 < a.E; e0 += kWave) {
       const bool before = e0 + lane < a.E && a.offsets[min(e0 + lane, a.E - 1)] <= r0;
@@ -938,10 +942,10 @@ __global__ __launch_bounds__(kGradZWaves * 64) void grad_z_kernel(LinearBackward
       const uint16_t* gy = reinterpret_cast<const uint16_t*>(a.grad_y);
       const uint16_t* z = reinterpret_cast<const uint16_t*>(a.z);
       uint16_t* gz = reinterpret_cast<uint16_t*>(a.grad_z);
-      const int64_t stop = min(end, r0 + (wave + 1) * kGradZRows);
+      const int64_t stop = min(end, r0 + (wave + 1) * share);
       // AHEAD rows' loads in flight: one at a time, a wave waits 16 times
       constexpr int AHEAD = ACT == MEP_ACT_NONE ? 8 : 4;
-      for (int64_t r1 = r0 + wave * kGradZRows; r1 < stop; r1 += AHEAD) {
+      for (int64_t r1 = r0 + wave * share; r1 < stop; r1 += AHEAD) {
         u32x4 gq[AHEAD], zq[AHEAD], uq[AHEAD];
 #pragma unroll
         for (int t = 0; t < AHEAD; ++t) {
@@ -1124,7 +1128,8 @@ hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {
 
 hipError_t launch_linear_backward(const LinearBackwardArgs& a, hipStream_t s) {
   if (a.cap > 0 && (a.act != MEP_ACT_NONE || a.grad_bias)) {
-    const int64_t blocks = (a.cap + kSegRows - 1) / kSegRows;
+    const int rows = grad_z_rows(a.grad_bias);
+    const int64_t blocks = (a.cap + rows - 1) / rows;
     const dim3 grid((unsigned)std::min<int64_t>(blocks, 1 << 16), (unsigned)((a.N + 511) / 512));
     switch (a.act) {
       case MEP_ACT_NONE: grad_z_kernel<MEP_ACT_NONE><<<grid, kGradZWaves * 64, 0, s>>>(a); break;

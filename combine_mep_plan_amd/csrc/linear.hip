@@ -10,7 +10,8 @@
 // (w in grad_x, both in grad_w) are "turned": the hardware's transposing LDS
 // reads give MFMA the values that lie along the summed index.
 //
-// A tile of 256 x 256 (small problems: 128 x 128) outputs takes 64 bf16 (128 E4M3) values of the summed index
+// A tile of 256 x 256 outputs (small problems: 128 x 128) takes 64 bf16 (128
+// E4M3) values of the summed index
 // a step: 32 KiB of each operand, moved from memory straight into LDS (no
 // registers), in two buffers of each, so that the next step's loads run while
 // this step's 64 MFMAs a wave do.  A step reads (256 + 256) x 128 bytes from
@@ -238,9 +239,14 @@ __device__ __forceinline__ void count_row_tiles(const TileArgs& a, int size, int
 }
 
 // The tile'th tile: experts in order, an expert's column tiles in order, the row
-// tiles that share a column tile next to each other.
-__device__ __forceinline__ Place find_tile(const TileArgs& a, const int32_t* first, int col_tiles,
-                                           int64_t tile) {
+// tiles that share a column tile next to each other.  From four whole row tiles
+// (`size` rows) on, the last one, which has fewer rows, comes behind all of them:
+// neighbouring blocks then take equally long and stay close enough together to
+// share what they load in L2 (4096 tokens, 8 of 32 experts of 4096 x 7168, about
+// 1024 rows each: 1573 -> 1520 us).  With fewer, the columns loaded once more
+// cost more (512 rows each, gradient of x: 857 -> 882 us).
+__device__ __forceinline__ Place find_tile(const TileArgs& a, const int32_t* first, int size,
+                                           int col_tiles, int64_t tile) {
   Place at;
   int lo = 0, hi = a.E;  // the last expert whose tiles start at or before this one
   while (hi - lo > 1) {
@@ -248,11 +254,13 @@ __device__ __forceinline__ Place find_tile(const TileArgs& a, const int32_t* fir
     if ((int64_t)first[mid] * col_tiles <= tile) lo = mid; else hi = mid;
   }
   at.e = first_lane(lo);
-  const int mt = first[at.e + 1] - first[at.e];
-  const int q = (int)(tile - (int64_t)first[at.e] * col_tiles);
-  at.m = first_lane(q % mt);
-  at.n = first_lane(q / mt);
   at.seg = segment_rows(a, at.e);
+  const int all = first[at.e + 1] - first[at.e], whole = at.seg / size;
+  const int together = whole >= 4 ? whole : all;
+  const int q = (int)(tile - (int64_t)first[at.e] * col_tiles);
+  const int behind = q - together * col_tiles;
+  at.m = first_lane(behind >= 0 ? whole : q % together);
+  at.n = first_lane(behind >= 0 ? behind : q / together);
   at.row0 = a.offsets[at.e];
   return at;
 }
@@ -310,7 +318,7 @@ __global__ __launch_bounds__(WN * WM * 64, 2 * PER_CU) void tile_kernel(TileArgs
       at.seg = segment_rows(a, at.e);
       at.row0 = a.offsets[at.e];
     } else {
-      at = find_tile(a, first, col_tiles, tile);
+      at = find_tile(a, first, BM, col_tiles, tile);
     }
   };
 
@@ -801,7 +809,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(TileArgs a) {
   const int k1 = (int)((int64_t)steps * (wave + 1) / kFewWaves);
 
   for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const Place at = find_tile(a, first, col_tiles, tile);
+    const Place at = find_tile(a, first, kFewRows, col_tiles, tile);
     const int64_t xr = at.row0 + min(at.m * kFewRows + r16, at.seg - 1);
     const unsigned char* px = a.b + xr * depth * SIZE;
     int wr[2];

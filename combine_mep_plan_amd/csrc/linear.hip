@@ -11,15 +11,21 @@
 // reads give MFMA the values that lie along the summed index.
 //
 // A tile of 256 x 256 outputs (small problems: 128 x 128) takes 64 bf16 (128
-// E4M3) values of the summed index
-// a step: 32 KiB of each operand, moved from memory straight into LDS (no
-// registers), in two buffers of each, so that the next step's loads run while
-// this step's 64 MFMAs a wave do.  A step reads (256 + 256) x 128 bytes from
-// memory and 192 KiB from LDS for 8.4 MFLOP: LDS at 128 bytes a clock needs 75%
-// of the time the matrix cores need, which is why the tile is this large.
-// 16-byte units of an LDS row are exchanged by the row's low bits (by the
-// source address, as the loads fill LDS lane after lane) so that operand reads
-// touch every bank once.
+// E4M3) values of the summed index a step: 32 KiB of each operand, moved from
+// memory straight into LDS (no registers), in two buffers of each, so that the
+// next step's loads run while this step's 64 MFMAs a wave do.  A step reads
+// (256 + 256) x 128 bytes from memory and 192 KiB from LDS for 8.4 MFLOP: LDS at
+// 128 bytes a clock needs 75% of the time the matrix cores need, which is why
+// the tile is this large.  16-byte units of an LDS row are exchanged by the
+// row's low bits (by the source address, as the loads fill LDS lane after lane)
+// so that operand reads touch every bank once.
+//
+// Measured, 32 experts of 4096 x 7168, top 8: forward of 4096 tokens, gated, 1520
+// us (1.27 PFLOP/s; E4M3 1000 us, 1.92 PFLOP/s), gradients of 2048 tokens 800 us
+// (grad_x, 1.2 PFLOP/s) and 1150 us (grad_w, 0.84 PFLOP/s with 1.9 GB stored).
+// The bf16 products run at a clock that the card lowers for its power (matrix
+// cores 72% busy), grad_w waits for its stores between short products; 16
+// tokens over 64 experts read the weights at 5.9 TB/s (565 us).
 #include <algorithm>
 #include <type_traits>
 

@@ -300,6 +300,17 @@ def test_residual_in_place():
     assert np.array_equal(y.double().cpu().numpy()[c.used], ref[c.used])
 
 
+@pytest.mark.parametrize("counts,num_rows", [([1, 0, 2], 3), ([300, 0, 5], 10 ** 9)])
+@pytest.mark.parametrize("act", ["none", "silu_glu"])
+def test_residual_in_place_few_rows_and_large_tiles(counts, num_rows, act):
+    c = Case(counts, 192, 136, act)
+    ref, _ = c.forward(num_rows=num_rows)
+    y = c.res.cuda()
+    M.mep_expert_linear(c.cfg, c.dev(c.x), None, c.dev(c.counts), c.dev(c.off), c.cap, num_rows,
+                        c.dev(c.w), None, c.dev(c.bias), y, y, None)
+    assert np.array_equal(y.double().cpu().numpy()[c.used], ref[c.used])
+
+
 @pytest.mark.parametrize("act", list(ACT))
 @pytest.mark.parametrize("name", list(COUNTS))
 def test_backward(name, act):

@@ -1076,10 +1076,10 @@ void run_tiles(const TileArgs& a, int64_t rows, hipStream_t s) {
 
 // Tiles of 256 x 256, one block a CU, or of 128 x 128, two, which have twice the
 // traffic for a product but four times the tiles, and waste less on short
-// segments.  Measured (2048 -> 7168, one segment): 1000 rows, 116 large tiles,
-// 42.4 us large and 31.9 small; 1536 rows, 168 tiles, 45.0 and 64.8.  7168 ->
-// 2048 gated over 64 experts: 2 rows an expert 609 and 574 us, 32 rows 638 and
-// 620; over 256 experts 64 rows 1333 and 1326, 128 rows 1492 and 2102.
+// segments.  Measured, large / small (us): 2048 -> 7168, one segment, 1000 rows,
+// 116 large tiles, 47.3 / 33.0; 1536 rows, 168 tiles, 51.1 / 62.0.  7168 -> 2048
+// gated, 64 experts, 2 rows each 586 / 581, 32 rows 654 / 632; 256 experts, 64
+// rows 2617 / 2649, 128 rows 2854 / 4266.
 template <Mode MODE, bool FP8, int ACT>
 void run_sized(const TileArgs& a, int64_t rows, hipStream_t s) {
   using Large = Tile<MODE, FP8, ACT, 2, 4, 8, 4>;
@@ -1091,10 +1091,10 @@ void run_sized(const TileArgs& a, int64_t rows, hipStream_t s) {
 
 // Few rows: up to 16 an expert where small tiles are no more than the CUs.
 // Measured (us, tiles / few rows): one token over 8 experts of 4096 x 7168, 256
-// tiles, 103 and 94 (E4M3 38.5 and 40.3), 2 experts of 1024 x 7168 36.5 and 19.2
-// (28.1 and 12.2), one of 7168 x 2048 13.7 and 8.8 (11.2 and 5.8); 16 tokens over
-// 64 experts of 4096 x 7168, 2048 tiles, 566 and 637; 33 rows of one expert 15.9
-// and 20.7.
+// tiles, 97 and 94 (E4M3 36.9 and 41.1), 2 experts of 1024 x 7168 35.5 and 19.4
+// (27.0 and 12.2), one of 7168 x 2048 13.3 and 8.4 (11.0 and 5.7); 16 tokens over
+// 64 experts of 4096 x 7168, 2048 tiles, 584 and 658; 33 rows of one expert 15.5
+// and 15.6.
 template <bool FP8, int ACT>
 void run_forward(const TileArgs& a, int64_t rows, hipStream_t s) {
   using Small = Tile<kForward, FP8, ACT, 2, 4, 4, 2>;

@@ -241,6 +241,9 @@ __device__ __forceinline__ bool scores_apart(float hi, float lo) {
 //   Biased scores: the same in place of "equal" with neighbours too close for
 // fp32 to order sigmoid(x) + b (about 1 token in 150), and the second time in
 // fp64 over those that may be among the first k.
+//   Measured, 256 experts, top 8: one token 5.6 us, hardly more than a launch;
+// 16384 tokens, biased sigmoid scores of bf16 logits, 15.2 us (9.4 MB, which alone
+// would take 2): instructions bound it.
 template <class TL, int LPT, int EPL, bool BIAS>
 __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
   constexpr int SLOTS = (kMaxTopk + LPT - 1) / LPT;  // results a lane may hold
@@ -534,7 +537,8 @@ __device__ __forceinline__ void probabilities(float (&x)[EPL], int score, float 
 // adds the rows up in order, so the result does not depend on timing.  What
 // bounds it at 4096 x 256 is latency: a pass of loads, the rows' way to memory
 // and back (a second launch would cost more), and the last block's loads, which
-// 512 threads keep in flight 16 rows each.
+// 512 threads keep in flight 16 rows each.  16.0 us there, 8.3 for one token, 41
+// for 65536 (67 MB, 1.6 TB/s).
 constexpr int kBalanceThreads = 512;
 constexpr int kRowsAhead = 16;  // partial rows a thread of the last block has in flight
 
@@ -734,7 +738,9 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
 //   softmax:  dx = p (u - sum u p),   sigmoid:  dx = s (1 - s) / S (u - sum u p).
 // The weights: only selected experts receive a gradient of their own; lane j
 // works out position j's and adds it through the group's row in LDS, a
-// repeated expert's positions added up in order first.
+// repeated expert's positions added up in order first.  Bound by the launch and
+// one trip to memory: 6.9 us at 4096 tokens of 256 fp32 logits (8.7 MB), 8.3 at
+// 30011 of 60 bf16 logits, whose rows do not start on 16 bytes.
 constexpr int kGradThreads = 256;
 
 template <class TL, int LPT, int EPL>

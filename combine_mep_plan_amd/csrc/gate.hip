@@ -53,6 +53,11 @@ __device__ __forceinline__ uint32_t group_min(uint32_t v) {
   return group_reduce<LPT>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
 }
 
+template <int LPT>
+__device__ __forceinline__ uint32_t group_add(uint32_t v) {
+  return group_reduce<LPT>(v, [](uint32_t a, uint32_t b) { return a + b; });
+}
+
 // Every lane adds the same pairs (a + b and b + a round alike), so all agree.
 template <int LPT>
 __device__ __forceinline__ float group_sum(float v) {
@@ -273,7 +278,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
   for (int s = 0; s < SLOTS; ++s) { got_key[s] = 1u; got[s] = 0; }
   [[maybe_unused]] uint32_t first = 0;  // the largest value's key
   bool again = false;  // the short keys did not decide
-  [[maybe_unused]] uint32_t border = 0;  // biased: below this key nobody is among the first k
+  [[maybe_unused]] uint32_t kth = 0;  // biased: the short key that the k-th round found
   if constexpr (PACKED) {
     uint32_t last = 0xffffffffu;
 #pragma unroll
@@ -326,12 +331,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
           }
         }
         last = now;
-        if (BIAS && j == k - 1) {
-          const float lo = key_value(now & ~LOW);
-          border = lo > -__builtin_inff()
-                       ? order_key(lo - 1.9073486328125e-06f * (1.0f + fabsf(lo)))
-                       : 0u;
-        }
+        if (BIAS && j == k - 1) kth = now;
         if (s < SLOTS && j < k && l == jj)
           got[s < SLOTS ? s : 0] =
               expert_of<TL, LPT>(LOW - (int)(now & LOW), __builtin_ctzll(vote));
@@ -346,6 +346,20 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
     constexpr int CAP = 64, HAVE = CAP / LPT;
     __shared__ uint16_t lists[kGateThreads / LPT][CAP];
     if (again) {
+      // Below the border nobody is among the first k.  Equal short keys leave the
+      // rounds together, so all of them may have left before the k-th round, which
+      // then found the largest again: fewer than k reach what it found.  The border
+      // is 0 in that case, and where the k-th is -inf or NaN.
+      constexpr uint32_t LOW = EPL - 1;
+      uint32_t reach = 0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) reach += ((key[i] & ~LOW) | (LOW - i)) >= kth;
+      reach = group_add<LPT>(reach);
+      const float lo = key_value(kth & ~LOW);
+      const uint32_t border =
+          reach >= (uint32_t)k && lo > -__builtin_inff()
+              ? order_key(lo - 1.9073486328125e-06f * (1.0f + fabsf(lo)))
+              : 0u;
       uint16_t* list = lists[threadIdx.x / LPT];
       int n = 0;
 #pragma unroll

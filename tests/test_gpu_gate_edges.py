@@ -1,0 +1,59 @@
+"""The router where its number formats end: ties that outnumber a lane's
+registers, logits far below zero, the largest batch.
+
+Half-steps of fp32 (2^-24, relative) of a result below: an exponential 4 (the
+hardware's within one unit of the last place, two products and a sum), of a
+difference to the largest logit one for each unit of that difference; 1 + e, its
+reciprocal (2) and a product 4, so a score is within 8 + spread of its value; a
+sum of n of them n more; a quotient 2."""
+
+import numpy as np
+import pytest
+import torch
+
+import combine_mep_plan_amd as M
+
+import _experts_ref as R
+from test_gpu_gate import cfg, close, run_balance, run_gate
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = {"fp32": torch.float32, "bf16": torch.bfloat16}
+
+
+# (experts, k): k below, at and above the number of values that a lane holds
+TIES = [(64, 9), (64, 10), (64, 32), (60, 12), (8, 8), (33, 32), (128, 8), (128, 10), (128, 32),
+        (100, 11), (256, 17), (256, 32), (130, 20), (300, 32), (1024, 17), (1024, 32), (513, 25),
+        (4096, 32)]
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("E,k", TIES)
+def test_biased_ties(E, k, dtype):
+    rng = np.random.default_rng(E + k)
+    x = np.zeros((40, E), np.float32)
+    x[1, 5] = 1.0                                    # one above an equal row
+    x[2, [0, E // 2, E - 1]] = 1.0, 2.0, 0.5         # a few, all different
+    x[3, : E // 2] = 1.0                             # two values
+    x[4] = -np.inf
+    x[5, 1:] = -np.inf
+    x[6, ::3] = -np.inf
+    x[7, 2] = -1.0                                   # one below
+    for t in range(8, 24):                           # few values, many equals
+        x[t] = rng.choice(np.float32([0.0, 0.5, -2.0]), size=E, p=[0.9, 0.05, 0.05])
+    for t in range(24, 40):                          # a handful above, the rest equal
+        at = rng.choice(E, size=min(E, 1 + t % 7), replace=False)
+        x[t, at] = 1.0 + np.arange(len(at), dtype=np.float32)
+    bias = np.zeros(E, np.float32)
+    for name in ("zero", "two values", "one"):
+        b = bias.copy()
+        if name == "two values":
+            b[::4] = 0.25
+        elif name == "one":
+            b[E // 3] = 0.125
+        idx, w = run_gate(cfg(E, k, "sigmoid", dtype), torch.from_numpy(x).to(DTYPES[dtype]).cuda(),
+                          torch.from_numpy(b).cuda(), len(x))
+        assert all(len(set(r)) == k for r in idx.tolist()), (name, "an expert twice")
+        ridx, rw = R.gate(x, b, k, "sigmoid", 1, 1.0)
+        assert np.array_equal(idx, ridx), (name, np.argwhere((idx != ridx).any(1))[:4])
+        close(w, rw, np.abs(rw), R.prob_steps())

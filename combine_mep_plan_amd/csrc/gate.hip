@@ -113,22 +113,47 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
+constexpr float kLog2E = 1.44269504088896341f;
+
 // exp(x) in two instructions: the hardware's power of two of the rounded x log2 e,
-// so within 1 + 1.5 |x| half-steps of fp32 (relative).  Arguments here are
-// differences to a maximum, where large |x| means a negligible term.
+// so within 2 + 1.5 |x| half-steps of fp32 (relative).  For the selection's keys,
+// whose absolute error counts, and for probabilities of all experts, of which those
+// far below the largest add next to nothing to anything (exp_f32 there cost the
+// balance loss of 4096 x 256 16.0 -> 17.0 us, the gradient 6.6 -> 6.9).
 __device__ __forceinline__ float fast_exp(float x) {
-  return __builtin_amdgcn_exp2f(x * 1.44269504088896341f);
+  return __builtin_amdgcn_exp2f(x * kLog2E);
 }
 
-__device__ __forceinline__ float sigmoid(float x) {
-  return __builtin_amdgcn_rcpf(1.0f + fast_exp(-x));
+// For the weights, which may all be small: exp(x) of x <= 0 within 4 half-steps.
+// exp(x) = 2^t exp(x - t ln 2), where t is the rounded x log2 e; the rest, below
+// 2^-17, is worked out with ln 2 in two parts and enters to first order.  Where t is
+// -inf the rest is NaN (its parts are infinities of both signs), which the maximum
+// turns into a number that the power, 0, makes nothing of; NaN stays NaN by the
+// power.
+__device__ __forceinline__ float exp_f32(float x) {
+  constexpr float kLn2 = 0.693147180559945309f;
+  constexpr float kLn2Low = (float)(0.693147180559945309 - (double)kLn2);
+  const float t = x * kLog2E, y = __builtin_amdgcn_exp2f(t);
+  const float rest = fmaxf(fmaf(-t, kLn2Low, fmaf(-t, kLn2, x)), -1.0f);
+  return fmaf(y, rest, y);
 }
 
-// The sigmoid and its slope s (1 - s), neither with a cancellation.
+template <bool EXACT>
+__device__ __forceinline__ float exp_of(float x) {
+  return EXACT ? exp_f32(x) : fast_exp(x);
+}
+
+// The sigmoid and its slope s (1 - s), neither with a cancellation; EXACT: by
+// exp_f32, so within 8 half-steps.
+template <bool EXACT>
 __device__ __forceinline__ float sigmoid(float x, float& slope) {
-  const float e = fast_exp(-fabsf(x)), r = __builtin_amdgcn_rcpf(1.0f + e);
+  const float e = exp_of<EXACT>(-fabsf(x)), r = __builtin_amdgcn_rcpf(1.0f + e);
   slope = e * r * r;
   return x < 0.0f ? e * r : r;
+}
+
+__device__ __forceinline__ float fast_sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + fast_exp(-x));
 }
 
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
@@ -224,7 +249,7 @@ constexpr int kGateThreads = 256;
 
 // How far apart two fp32 scores sigmoid(x) + b must be for their order to be
 // the order of the exact scores.  The sigmoid's error: s (1 - s) <= 1/4 of the
-// exponential's relative one, which is at most 1 + 1.5 |x| half-steps, in all
+// exponential's relative one, which is at most 2 + 1.5 |x| half-steps, in all
 // below a half-step and a half, 2 for the reciprocal; the sum rounds once more.
 // So each score is within 2^-22 (1 + |score|), and two within twice that.
 __device__ __forceinline__ bool scores_apart(float hi, float lo) {
@@ -267,7 +292,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
   for (int i = 0; i < EPL; ++i) {
     const int e = expert_of<TL, LPT>(i, l);
     float s = x[i];
-    if constexpr (BIAS) s = sigmoid(s) + bias[i];
+    if constexpr (BIAS) s = fast_sigmoid(s) + bias[i];
     key[i] = e < E ? order_key(s) : 0u;
     if (PACKED && e < E) key[i] = (key[i] & 0xffff0000u) | (uint32_t)(0xffff - e);
   }
@@ -478,9 +503,10 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
       float v;
       if constexpr (PACKED) v = key_value(got_key[s]);
       else v = load_logit(row + got[s]);  // a cache hit
-      w[s] = a.score == MEP_SCORE_SIGMOID ? sigmoid(v)
+      [[maybe_unused]] float slope;
+      w[s] = a.score == MEP_SCORE_SIGMOID ? sigmoid<true>(v, slope)
              : m == -__builtin_inff()     ? 0.0f
-                                          : fast_exp(v - m);
+                                          : exp_f32(v - m);
     }
     sum += w[s];
   }
@@ -534,7 +560,7 @@ __device__ __forceinline__ void probabilities(float (&x)[EPL], int score, float 
   } else {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      p[i] = SLOPE ? sigmoid(x[i], x[i]) : sigmoid(x[i]);
+      p[i] = SLOPE ? sigmoid<false>(x[i], x[i]) : fast_sigmoid(x[i]);
       sum += p[i];
     }
   }
@@ -812,9 +838,9 @@ __global__ __launch_bounds__(kGradThreads) void gate_backward_kernel(GateBackwar
           gw[s] = a.scale * a.grad_weights[tt * k + j];
           const float xe = load_logit(row + e);
           if (softmax) {
-            v[s] = m == -__builtin_inff() ? 0.0f : fast_exp(xe - m);
+            v[s] = m == -__builtin_inff() ? 0.0f : exp_f32(xe - m);
           } else {
-            v[s] = sigmoid(xe, d[s]);
+            v[s] = sigmoid<true>(xe, d[s]);
           }
         }
       }

@@ -57,3 +57,39 @@ def test_biased_ties(E, k, dtype):
         ridx, rw = R.gate(x, b, k, "sigmoid", 1, 1.0)
         assert np.array_equal(idx, ridx), (name, np.argwhere((idx != ridx).any(1))[:4])
         close(w, rw, np.abs(rw), R.prob_steps())
+
+
+def scores_far_from_zero(T, E, seed, lo=20.0, hi=80.0):
+    """Logits of both signs with magnitudes in [lo, hi], eighths (so exact in
+    bf16's and fp32's products with small numbers of them)."""
+    rng = np.random.default_rng(seed)
+    x = rng.integers(int(8 * lo), int(8 * hi), size=(T, E)) / 8.0
+    return (x * rng.choice([-1.0, 1.0], size=(T, E))).astype(np.float32)
+
+
+@pytest.mark.parametrize("E,k", [(16, 16), (100, 32), (256, 32), (1030, 32)])
+def test_sigmoid_weights_far_below_zero(E, k):
+    # every selected logit is far below zero: the error of its exponential must
+    # not grow with its size
+    x = -np.abs(scores_far_from_zero(50, E, E))
+    idx, w = run_gate(cfg(E, k, "sigmoid", "fp32", 0, 2.5), torch.from_numpy(x).cuda(), None, 50)
+    ridx, rw = R.gate(x, None, k, "sigmoid", 0, 2.5)
+    assert np.array_equal(idx, ridx)
+    close(w, rw, rw, 8 + 2)          # the score, times the scale (itself exact)
+    g = np.random.default_rng(1).standard_normal((50, k)).astype(np.float32)
+    out = torch.empty((50, E), device="cuda")
+    M.mep_gate_backward(cfg(E, k, "sigmoid", "fp32", 0, 2.5), torch.from_numpy(x).cuda(),
+                        torch.from_numpy(ridx).cuda(), None, 50, torch.from_numpy(g).cuda(), None,
+                        None, out)
+    ref, mag = R.gate_grad(x, ridx, None, "sigmoid", 0, 2.5, 0.0, g, None, 0.0)
+    close(out.cpu().numpy(), ref, mag, 4 + 2 * 4 + 4)  # e / (1 + e)^2 times grad times scale
+
+
+def test_softmax_weights_far_below_the_largest():
+    # eighths: the difference to the largest logit is exact
+    x = scores_far_from_zero(50, 8, 3, 0.0, 40.0)
+    idx, w = run_gate(cfg(8, 8, "softmax", "fp32", 0, 2.5), torch.from_numpy(x).cuda(), None, 50)
+    ridx, rw = R.gate(x, None, 8, "softmax", 0, 2.5)
+    assert np.array_equal(idx, ridx)
+    # numerator 4, 8 exponentials of 4 and their sum 8, quotient and scale 2
+    close(w, rw, rw, 4 + 4 + 8 + 2)

@@ -156,6 +156,21 @@ __device__ __forceinline__ float fast_sigmoid(float x) {
   return __builtin_amdgcn_rcpf(1.0f + fast_exp(-x));
 }
 
+// Quotients of scores are taken of exponentials relative to the largest logit among
+// those that count: always for softmax, and for sigmoids where that logit is below
+// -20, where 1 + e^x rounds to 1 and the sigmoid is e^x (further down fp32 has no
+// number for it, while the quotients are ordinary ones).
+__device__ __forceinline__ bool relative(int score, float largest) {
+  return score == MEP_SCORE_SOFTMAX || largest < -20.0f;
+}
+
+// What to take off the logits then.  Where no score is left the exponentials of the
+// logits as they are, all 0: every logit -inf, or for sigmoids below -708, where
+// they leave the range of 64 bits too (masks of the type's lowest value).
+__device__ __forceinline__ float shift_of(int score, float largest) {
+  return largest > (score == MEP_SCORE_SOFTMAX ? -__builtin_inff() : -708.0f) ? largest : 0.0f;
+}
+
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
 __device__ __forceinline__ float load_logit(const uint16_t* p) {
   return __uint_as_float((uint32_t)*p << 16);
@@ -301,7 +316,6 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
   int got[SLOTS];
 #pragma unroll
   for (int s = 0; s < SLOTS; ++s) { got_key[s] = 1u; got[s] = 0; }
-  [[maybe_unused]] uint32_t first = 0;  // the largest value's key
   bool again = false;  // the short keys did not decide
   [[maybe_unused]] uint32_t kth = 0;  // biased: the short key that the k-th round found
   if constexpr (PACKED) {
@@ -315,7 +329,6 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) d = min(d, last - 1u - key[i]);
         last = last - 1u - group_min<LPT>(d);
-        if (j == 0) first = last | 0xffffu;
         if (l == jj) {
           got_key[s] = last;
           got[s] = 0xffff - (int)(last & 0xffffu);
@@ -326,7 +339,6 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
     // zero and all zeros from there on; NaN's key is 1 with the expert over it
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) got_key[s] = unpack_key(got_key[s]);
-    first = unpack_key(first);
   } else {
     constexpr uint32_t LOW = EPL - 1;
     static_assert((EPL & (EPL - 1)) == 0, "");
@@ -489,39 +501,44 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
   }
 
   // weights: lane l holds positions l, l + LPT, ...
+  const bool softmax = a.score == MEP_SCORE_SOFTMAX;
   float w[SLOTS];
-  // the largest logit (softmax only): the first position's
-  float m;
-  if constexpr (PACKED) m = key_value(first);
-  else m = load_logit(row + __shfl(got[0], 0, LPT));
+#pragma unroll
+  for (int s = 0; s < SLOTS; ++s) {
+    w[s] = -__builtin_inff();
+    if (s * LPT + l < k) {
+      if constexpr (PACKED) w[s] = key_value(got_key[s]);
+      else w[s] = load_logit(row + got[s]);  // a cache hit
+    }
+  }
+  // the largest logit that counts: the first position's, unless a bias chose it
+  float m = w[0];
+  if constexpr (BIAS) {
+#pragma unroll
+    for (int s = 1; s < SLOTS; ++s) m = fmaxf(m, w[s]);
+    if (a.normalize) m = group_fmax<LPT>(m);
+  } else {
+    m = __shfl(m, 0, LPT);
+  }
+  const bool rel = softmax || (a.normalize && relative(a.score, m));
+  const float shift = shift_of(a.score, m);
   float sum = 0.0f;
 #pragma unroll
   for (int s = 0; s < SLOTS; ++s) {
-    const int j = s * LPT + l;
-    w[s] = 0.0f;
-    if (j < k) {
-      float v;
-      if constexpr (PACKED) v = key_value(got_key[s]);
-      else v = load_logit(row + got[s]);  // a cache hit
-      [[maybe_unused]] float slope;
-      w[s] = a.score == MEP_SCORE_SIGMOID ? sigmoid<true>(v, slope)
-             : m == -__builtin_inff()     ? 0.0f
-                                          : exp_f32(v - m);
-    }
+    [[maybe_unused]] float slope;
+    w[s] = s * LPT + l >= k ? 0.0f : rel ? exp_f32(w[s] - shift) : sigmoid<true>(w[s], slope);
     sum += w[s];
   }
-  float scale = a.scale;
-  if (a.normalize || a.score == MEP_SCORE_SOFTMAX) {
+  const float scale = a.scale;
+  if (a.normalize || softmax) {
     if (!a.normalize) {  // softmax over all experts
       sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
-        if (expert_of<TL, LPT>(i, l) < E) sum += fast_exp(x[i] - m);
+        if (expert_of<TL, LPT>(i, l) < E) sum += fast_exp(x[i] - shift);
     }
     sum = group_sum<LPT>(sum);
-    // nothing selectable (every logit -inf): all weights are 0
-    if (a.score == MEP_SCORE_SOFTMAX && m == -__builtin_inff()) sum = 1.0f;
-    if (sum == 0.0f) sum = 1.0f;
+    if (sum == 0.0f) sum = 1.0f;  // no score left: all weights are 0
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) w[s] = w[s] / sum;
   }
@@ -540,22 +557,22 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
 
 // A token's probabilities over the experts in registers: softmax(x), or the
 // sigmoids over their sum: p[i] * inv.  A row of -inf has probability 0
-// everywhere.  SLOPE: sigmoid scores leave their slopes in x.
+// everywhere.  SLOPE: sigmoid scores leave their slopes, on the scale of p, in x.
 template <int LPT, int EPL, bool SLOPE>
 __device__ __forceinline__ void probabilities(float (&x)[EPL], int score, float (&p)[EPL], float& m,
                                               float& inv) {
   float sum = 0.0f;
-  m = 0.0f;
-  if (score == MEP_SCORE_SOFTMAX) {
-    m = -__builtin_inff();
+  m = -__builtin_inff();
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) m = fmaxf(m, x[i]);
-    m = group_fmax<LPT>(m);
-    const float shift = m == -__builtin_inff() ? 0.0f : m;
+  for (int i = 0; i < EPL; ++i) m = fmaxf(m, x[i]);
+  m = group_fmax<LPT>(m);
+  if (relative(score, m)) {
+    const float shift = shift_of(score, m);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {  // registers past E hold -inf: exp gives 0
       p[i] = fast_exp(x[i] - shift);
       sum += p[i];
+      if (SLOPE && score == MEP_SCORE_SIGMOID) x[i] = p[i];  // s (1 - s) is s down there
     }
   } else {
 #pragma unroll
@@ -825,25 +842,32 @@ __global__ __launch_bounds__(kGradThreads) void gate_backward_kernel(GateBackwar
     for (int e = l; e < E; e += LPT) extra[e] = 0.0f;
     int id[SLOTS];
     float v[SLOTS], d[SLOTS], gw[SLOTS];
-    float total = 0.0f, gsum = 0.0f;
+    float total = 0.0f, gsum = 0.0f, top = -__builtin_inff();
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
       const int j = s * LPT + l;
       id[s] = -1;
-      v[s] = d[s] = gw[s] = 0.0f;
+      v[s] = -__builtin_inff();
+      gw[s] = 0.0f;
       if (j < k) {
         const int e = a.indices[tt * k + j];
         if (e >= 0 && e < E) {
           id[s] = e;
           gw[s] = a.scale * a.grad_weights[tt * k + j];
-          const float xe = load_logit(row + e);
-          if (softmax) {
-            v[s] = m == -__builtin_inff() ? 0.0f : exp_f32(xe - m);
-          } else {
-            v[s] = sigmoid<true>(xe, d[s]);
-          }
+          v[s] = load_logit(row + e);
         }
       }
+      top = fmaxf(top, v[s]);
+    }
+    // the named experts may lie far below the largest logit (an earlier routing's)
+    if (a.normalize) top = group_fmax<LPT>(top); else top = m;
+    const bool rel = softmax || (a.normalize && relative(a.score, top));
+    const float from = shift_of(a.score, top);
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s) {
+      if (id[s] < 0) v[s] = d[s] = 0.0f;
+      else if (rel) v[s] = d[s] = exp_f32(v[s] - from);  // of a sigmoid the slope too
+      else v[s] = sigmoid<true>(v[s], d[s]);
       total += v[s];
       gsum += gw[s] * v[s];
     }

@@ -387,7 +387,9 @@ typedef struct mep_gate_config {
  * to the lower expert, and sigmoid scores that fp32 cannot order are compared
  * in 64 bits.  All k experts of a token are different, whatever its logits: NaN
  * ranks last, and a selected NaN gives NaN weights, as does a logit of +inf
- * under softmax; where every v_j is 0 (logits of -inf) the weights are 0.
+ * under softmax; where every v_j is 0 (logits of -inf, and sigmoids of logits
+ * below -708) the weights are 0.  Quotients are those of exact scores, also where
+ * a sigmoid is too small for fp32; this holds for p and the gradients below too.
  * 0 <= T <= 2^26.  MEP_ERR_CONFIG for a bias with softmax scores.
  */
 int mep_gate(const mep_gate_config *cfg, const void *logits, const float *bias, int32_t T,

@@ -93,3 +93,81 @@ def test_softmax_weights_far_below_the_largest():
     assert np.array_equal(idx, ridx)
     # numerator 4, 8 exponentials of 4 and their sum 8, quotient and scale 2
     close(w, rw, rw, 4 + 4 + 8 + 2)
+
+
+# Where all that count are so far below zero that fp32 has no sigmoid for them
+# (under -87.3), what is normalized is still well defined.
+LOW = [(-100.0, -90.0), (-700.0, -690.0), (-110.0, -60.0), (-30.0, -12.0),
+       (-3000.0, -2990.0)]  # the last vanish in 64 bits too: all weights are 0
+
+
+@pytest.mark.parametrize("lo,hi", LOW)
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("E,k", [(16, 4), (256, 8), (1030, 32)])
+def test_normalized_sigmoid_weights_of_very_low_logits(E, k, bias, lo, hi):
+    T, rng = 30, np.random.default_rng(E)
+    x = rng.uniform(lo, hi, size=(T, E)).astype(np.float32)
+    x[3, 1:] = -np.inf
+    x[4] = -np.inf
+    # experts that a bias selects, wherever their logits lie
+    b = None if not bias else (rng.permutation(E) / 64.0).astype(np.float32)
+    c = cfg(E, k, "sigmoid", "fp32", 1, 1.5)
+    idx, w = run_gate(c, torch.from_numpy(x).cuda(), None if b is None else torch.from_numpy(b).cuda(), T)
+    ridx, rw = R.gate(x, b, k, "sigmoid", 1, 1.5)
+    assert np.array_equal(idx, ridx)
+    # twice a score (8, and a step for each unit of difference), the sum, two more
+    close(w, rw, rw, 2 * (8 + hi - lo) + k + 2)
+    assert np.allclose(w[:3].sum(1), 1.5 if lo > -708 else 0.0) and (w[4] == 0).all()
+
+
+@pytest.mark.parametrize("lo,hi", LOW)
+@pytest.mark.parametrize("normalize", [0, 1])
+@pytest.mark.parametrize("E,k", [(16, 4), (256, 8), (1030, 32)])
+def test_loss_and_gradients_of_very_low_sigmoid_logits(E, k, normalize, lo, hi):
+    T, rng = 30, np.random.default_rng(E)
+    x = rng.uniform(lo, hi, size=(T, E)).astype(np.float32)
+    x[3, 1:] = -np.inf
+    x[4] = -np.inf
+    x[5, 1:] = 2.0                   # one row as usual
+    idx = R.top(x, k)
+    c = cfg(E, k, "sigmoid", "fp32", normalize, 1.5)
+    xt, it = torch.from_numpy(x).cuda(), torch.from_numpy(idx).cuda()
+    counts, mean, loss = run_balance(c, xt, it, None, T)
+    ref = R.balance(x, idx, None, "sigmoid", 0.02)
+    assert np.array_equal(counts, ref[0])
+    # scores 8, a step for each unit of difference, a lane's sum and the lanes', the tokens'
+    steps = 2 * (8 + hi - lo) + 70 + T + 4
+    close(mean, ref[1], ref[1], steps)
+    close(np.float64(loss), np.float64(ref[2]), np.float64(ref[2]), steps + 2)
+    gw = rng.standard_normal((T, k)).astype(np.float32)
+    out = torch.empty((T, E), device="cuda")
+    M.mep_gate_backward(c, xt, it, None, T, torch.from_numpy(gw).cuda(),
+                        torch.from_numpy(counts).cuda(), torch.full((1,), 30.0, device="cuda"), out)
+    g, mag = R.gate_grad(x, idx, None, "sigmoid", normalize, 1.5, 0.02, gw, counts, 30.0)
+    close(out.cpu().numpy(), g, mag, 3 * steps)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("far", [40.0, 95.0, 150.0])
+@pytest.mark.parametrize("E,k", [(16, 4), (256, 8), (1030, 32)])
+def test_gradient_of_normalized_weights_for_experts_far_from_the_largest(E, k, far, score):
+    # indices of an earlier routing, replayed on logits whose largest lies elsewhere
+    T, rng = 20, np.random.default_rng(E)
+    x = rng.uniform(-5, 0, size=(T, E)).astype(np.float32)
+    idx = np.stack([rng.choice(np.arange(1, E), size=k, replace=False) for _ in range(T)])
+    idx = idx.astype(np.int32)
+    np.put_along_axis(x, idx.astype(np.int64), rng.uniform(-far - 4, -far, size=(T, k)).astype(np.float32), 1)
+    x[:, 0] = 3.0
+    idx[1, 0] = -1                   # a dropped position
+    idx[2, 0] = idx[2, 1]            # an expert twice
+    idx[3] = -1                      # no position left
+    gw = rng.standard_normal((T, k)).astype(np.float32)
+    out = torch.empty((T, E), device="cuda")
+    M.mep_gate_backward(cfg(E, k, score, "fp32", 1, 1.5), torch.from_numpy(x).cuda(),
+                        torch.from_numpy(idx).cuda(), None, T, torch.from_numpy(gw).cuda(), None,
+                        None, out)
+    ref, mag = R.gate_grad(x, idx, None, score, 1, 1.5, 0.0, gw, None, 0.0)
+    assert np.abs(ref[4:]).max() > 0.01
+    # three quotients of scores (8, and a step for each unit of their difference) and
+    # sums of k, and the differences that the magnitudes cover
+    close(out.cpu().numpy(), ref, mag, 3 * (8 + 5 + k + 4))

@@ -7,7 +7,7 @@
 
 namespace {
 
-constexpr int32_t kMaxTokens = 1 << 26;  // 64 lanes a token: at most 2^32 threads
+constexpr int32_t kMaxTokens = 1 << 26;
 constexpr size_t kCounterBytes = 256;    // balance workspace: the blocks' counter
 
 bool aligned(const void* p) { return ((uintptr_t)p & 15u) == 0; }

@@ -973,13 +973,35 @@ void gate_typed(const GateArgs& a, hipStream_t s) {
 
 static bool is_wide(int E, int dtype) { return E % (dtype == MEP_BF16 ? 8 : 4) == 0; }
 
+// A launch has fewer than 2^32 threads, and a token up to 64 of them: larger
+// batches go in parts.
+constexpr int32_t kTokensALaunch = 1 << 25;
+
+// Calls f(first token, tokens) for each part.
+template <class F>
+static hipError_t in_parts(int32_t T, F f) {
+  for (int64_t t = 0; t < T; t += kTokensALaunch) {
+    f(t, (int32_t)std::min<int64_t>(kTokensALaunch, T - t));
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+static const void* logits_at(const void* logits, int64_t values, int dtype) {
+  return (const unsigned char*)logits + values * (dtype == MEP_BF16 ? 2 : 4);
+}
+
 hipError_t launch_gate(const GateArgs& a0, hipStream_t s) {
-  if (a0.T == 0) return hipSuccess;
-  GateArgs a = a0;
-  a.wide = is_wide(a.E, a.dtype);
-  if (a.dtype == MEP_BF16) gate_typed<uint16_t>(a, s);
-  else gate_typed<float>(a, s);
-  return hipGetLastError();
+  return in_parts(a0.T, [&](int64_t t, int32_t n) {
+    GateArgs a = a0;
+    a.T = n;
+    a.logits = logits_at(a0.logits, t * a.E, a.dtype);
+    a.indices += t * a.k;
+    a.weights += t * a.k;
+    a.wide = is_wide(a.E, a.dtype);
+    if (a.dtype == MEP_BF16) gate_typed<uint16_t>(a, s);
+    else gate_typed<float>(a, s);
+  });
 }
 
 // Blocks: a pass over one token a group takes about 0.6 us, and each block's
@@ -1016,19 +1038,25 @@ hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_gate_backward(const GateBackwardArgs& a0, hipStream_t s) {
-  if (a0.T == 0) return hipSuccess;
-  GateBackwardArgs a = a0;
-  a.wide = is_wide(a.E, a.dtype);
-  by_experts(a.E, [&](auto lpt, auto epl) {
-    const int groups = kGradThreads / lpt();
-    const unsigned blocks = (unsigned)((a.T + groups - 1) / groups);
-    const size_t lds = a.grad_weights ? (size_t)groups * a.E * 4 : 0;
-    if (a.dtype == MEP_BF16)
-      gate_backward_kernel<uint16_t, lpt(), epl()><<<blocks, kGradThreads, lds, s>>>(a);
-    else
-      gate_backward_kernel<float, lpt(), epl()><<<blocks, kGradThreads, lds, s>>>(a);
+  return in_parts(a0.T, [&](int64_t t, int32_t n) {
+    GateBackwardArgs a = a0;
+    a.T = n;
+    a.logits = logits_at(a0.logits, t * a.E, a.dtype);
+    a.grad_logits = const_cast<void*>(logits_at(a0.grad_logits, t * a.E, a.dtype));
+    a.indices += t * a.k;
+    if (a.mask) a.mask += t;
+    if (a.grad_weights) a.grad_weights += t * a.k;
+    a.wide = is_wide(a.E, a.dtype);
+    by_experts(a.E, [&](auto lpt, auto epl) {
+      const int groups = kGradThreads / lpt();
+      const unsigned blocks = (unsigned)((a.T + groups - 1) / groups);
+      const size_t lds = a.grad_weights ? (size_t)groups * a.E * 4 : 0;
+      if (a.dtype == MEP_BF16)
+        gate_backward_kernel<uint16_t, lpt(), epl()><<<blocks, kGradThreads, lds, s>>>(a);
+      else
+        gate_backward_kernel<float, lpt(), epl()><<<blocks, kGradThreads, lds, s>>>(a);
+    });
   });
-  return hipGetLastError();
 }
 
 }  // namespace mep

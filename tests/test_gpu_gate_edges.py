@@ -171,3 +171,37 @@ def test_gradient_of_normalized_weights_for_experts_far_from_the_largest(E, k, f
     # three quotients of scores (8, and a step for each unit of their difference) and
     # sums of k, and the differences that the magnitudes cover
     close(out.cpu().numpy(), ref, mag, 3 * (8 + 5 + k + 4))
+
+
+def test_largest_batch():
+    # 2^26 tokens with 64 lanes each are 2^32 threads, one more than a launch takes
+    T, E, k = 1 << 26, 513, 2
+    torch.cuda.empty_cache()
+    logits = torch.zeros((T, E), dtype=torch.bfloat16, device="cuda")
+    at = torch.tensor([0, 1, (1 << 25) - 1, 1 << 25, (1 << 25) + 1, T - 2, T - 1])
+    x = np.random.default_rng(0).standard_normal((len(at), E)).astype(np.float32)
+    x = torch.from_numpy(x).bfloat16()
+    logits[at.cuda()] = x.cuda()
+    c = cfg(E, k, "softmax", "bf16", 1, 1.0)
+    idx = torch.full((T, k), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T, k), -7.0, device="cuda")
+    M.mep_gate(c, logits, None, T, idx, w)
+    ridx, rw = R.gate(x.double().numpy(), None, k, "softmax", 1, 1.0)
+    assert np.array_equal(idx[at.cuda()].cpu().numpy(), ridx)
+    close(w[at.cuda()].cpu().numpy(), rw, rw, R.prob_steps())
+    others = torch.ones(T, dtype=torch.bool, device="cuda")
+    others[at.cuda()] = False
+    assert bool(((idx == torch.arange(k, device="cuda", dtype=torch.int32)).all(1) | ~others).all())
+    assert bool(((w == 0.5).all(1) | ~others).all())
+    gw = torch.zeros((T, k), device="cuda")
+    gw[at.cuda()] = torch.tensor([1.0, -2.0], device="cuda")
+    out = torch.full((T, E), 3.0, dtype=torch.bfloat16, device="cuda")
+    M.mep_gate_backward(c, logits, idx, None, T, gw, None, None, out)
+    g, mag = R.gate_grad(x.double().numpy(), ridx, None, "softmax", 1, 1.0, 0.0,
+                         gw[at.cuda()].cpu().numpy(), None, 0.0)
+    close(out[at.cuda()].float().cpu().numpy(), g, mag, 3 * R.prob_steps(), "bf16")
+    step = 1 << 22
+    for t in range(0, T, step):
+        assert not bool((out[t:t + step].any(1) & others[t:t + step]).any())
+    del logits, out
+    torch.cuda.empty_cache()

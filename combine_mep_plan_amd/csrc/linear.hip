@@ -946,15 +946,25 @@ __global__ __launch_bounds__(kGradZWaves * 64) void grad_z_kernel(LinearBackward
   const int rows = grad_z_rows(a.grad_bias), share = rows / kGradZWaves;
   for (int64_t blk = blockIdx.x; blk * rows < a.cap; blk += gridDim.x) {
     const int64_t r0 = blk * rows;
-    int lo = 0;  // the last segment that starts at or before r0
-    for (int e0 = 0; e0 < a.E; e0 += kWave) {
-      const bool before = e0 + lane < a.E && a.offsets[min(e0 + lane, a.E - 1)] <= r0;
-      const int n = __popcll(__ballot(before));
-      if (n > 0) lo = e0 + n - 1;
-      if (n < kWave) break;
+    // the end of the segment that r0 lies in (segments may be in any order): 256
+    // experts at a time, so that few loads follow one another (whole backward, 64
+    // tokens over 1024 experts of 128 x 128: 43 us, 64 at a time 50)
+    constexpr int GROUPS = 4;
+    int64_t end = r0;
+    for (int e0 = 0; e0 < a.E && end == r0; e0 += GROUPS * kWave) {
+      int64_t from[GROUPS], to[GROUPS];
+#pragma unroll
+      for (int u = 0; u < GROUPS; ++u) {
+        const int e = min(e0 + u * kWave + lane, a.E - 1);
+        from[u] = a.offsets[e];
+        to[u] = from[u] + max(a.counts[e], 0);
+      }
+#pragma unroll
+      for (int u = 0; u < GROUPS; ++u) {
+        const uint64_t in = ballot(from[u] >= 0 && from[u] <= r0 && r0 < to[u]);
+        if (in != 0) end = r0 + lane_value((int)(min(to[u], a.cap) - r0), __builtin_ctzll(in));
+      }
     }
-    int64_t end = min((int64_t)a.offsets[lo] + max(a.counts[lo], 0), a.cap);
-    if (a.offsets[lo] > r0) end = 0;
     const int col = (blockIdx.y * 64 + lane) * 8;
     float s0[8], s1[8];
 #pragma unroll

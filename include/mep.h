@@ -465,8 +465,9 @@ typedef struct mep_linear_config {
  * bf16.  Rows outside the segments' counts (padding,
  * rows behind the last segment) are neither used nor written, and rows past
  * cap_em are left out.  em_offsets[e] must be multiples of 128, em_counts[e] >=
- * 0 and segments must not overlap, as the calls above write them.  One segment
- * over a whole batch (E = 1) is an ordinary dense layer.  num_rows is the number
+ * 0 and segments must not overlap, as the calls above write them; their order is
+ * free, and em_offsets[E] is not read.  One segment over a whole batch (E = 1) is
+ * an ordinary dense layer.  num_rows is the number
  * of rows to expect in all segments together (T*k): it selects among kernels and
  * sizes the launch; results are complete for any value.  0 <= cap_em <=
  * INT32_MAX.  y and z overlap no input, but y may be residual itself.

@@ -424,3 +424,25 @@ def test_offsets_past_32_bits():
     got = gw[1].double().cpu().numpy()
     assert np.all(np.abs(got - sx) <= 5 * R.U32 * np.abs(x3).sum(0) + 1.01 * R.UBF16 * np.abs(sx))
     assert not bool(gw[0].any())
+
+
+@pytest.mark.parametrize("act", list(ACT))
+def test_segments_in_any_order(act):
+    # the experts' segments do not ascend, and empty experts name any start
+    c = Case([130, 0, 40, 7, 0, 300, 1, 0], 72, 40, act, extra=2)
+    order = [5, 2, 7, 0, 3, 6, 1, 4]
+    c.counts, starts = c.counts[order], c.off[:-1][order]
+    starts[np.flatnonzero(c.counts == 0)] = [0, 384, 128]
+    c.off = np.append(starts, c.off[-1]).astype(np.int32)
+    c.check_forward(want_z=True)
+    c.check_backward()
+
+
+def test_segments_in_any_order_many_experts():
+    counts = np.zeros(200, int)
+    counts[[3, 64, 130, 199]] = 5, 200, 33, 129
+    c = Case(counts, 24, 16, "silu_glu")
+    order = np.random.default_rng(1).permutation(200)
+    c.counts, c.off = c.counts[order], np.append(c.off[:-1][order], c.off[-1]).astype(np.int32)
+    c.check_forward(num_rows=367)
+    c.check_backward(num_rows=367)

@@ -543,9 +543,13 @@ def _call(fn, args, build, stream) -> None:
         dev = d
         ptrs.append(t.data_ptr())
     import torch
+    # the device query is what torch.cuda.current_device is made of, without its 0.3 us
     if dev < 0 or dev == torch._C._cuda_getDevice():
         if stream is None and dev >= 0:
-            stream = torch._C._cuda_getCurrentRawStream(dev)
+            try:
+                stream = torch._C._cuda_getCurrentRawStream(dev)
+            except AttributeError:  # a torch without the bare stream query
+                stream = torch.cuda.current_stream(dev).cuda_stream
         else:
             stream = _stream(stream)
         rc = build(getattr(_lib or lib(), fn), ptrs, stream)

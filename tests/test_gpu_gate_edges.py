@@ -205,3 +205,12 @@ def test_largest_batch():
         assert not bool((out[t:t + step].any(1) & others[t:t + step]).any())
     del logits, out
     torch.cuda.empty_cache()
+
+
+def test_a_torch_without_the_bare_stream_query(monkeypatch):
+    # the private handle that the binding prefers may go away
+    if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream")
+    x = np.random.default_rng(0).standard_normal((5, 64)).astype(np.float32)
+    idx, _ = run_gate(cfg(64, 4, "softmax", "fp32"), torch.from_numpy(x).cuda(), None, 5)
+    assert np.array_equal(idx, R.gate(x, None, 4, "softmax", 1, 1.0)[0])

@@ -214,3 +214,22 @@ def test_a_torch_without_the_bare_stream_query(monkeypatch):
     x = np.random.default_rng(0).standard_normal((5, 64)).astype(np.float32)
     idx, _ = run_gate(cfg(64, 4, "softmax", "fp32"), torch.from_numpy(x).cuda(), None, 5)
     assert np.array_equal(idx, R.gate(x, None, 4, "softmax", 1, 1.0)[0])
+
+
+@pytest.mark.parametrize("E,k", [(16, 6), (64, 12), (256, 8), (1030, 20)])
+def test_experts_masked_by_their_bias(E, k):
+    # -inf or the lowest value keeps an expert out while others are left, +inf
+    # puts it first, NaN last; k of them all are named all the same
+    T, rng = 20, np.random.default_rng(E)
+    x = rng.standard_normal((T, E)).astype(np.float32)
+    low = np.finfo(np.float32).min
+    for value, left in ((-np.inf, E - 3), (-np.inf, k), (-np.inf, k - 2), (low, k - 2), (np.nan, k - 2),
+                        (np.inf, 2), (np.inf, E - k - 1), (low, 1), (np.nan, 0), (-np.inf, 0)):
+        b = rng.uniform(-0.5, 0.5, size=E).astype(np.float32)
+        b[rng.choice(E, size=E - left, replace=False)] = value
+        idx, w = run_gate(cfg(E, k, "sigmoid", "fp32", 0), torch.from_numpy(x).cuda(),
+                          torch.from_numpy(b).cuda(), T)
+        ridx, rw = R.gate(x, b, k, "sigmoid", 0, 1.0)
+        assert all(len(set(r)) == k for r in idx.tolist()), (value, left)
+        assert np.array_equal(idx, ridx), (value, left)
+        close(w, rw, rw, 8 + 2)

@@ -286,9 +286,11 @@ __device__ __forceinline__ bool scores_apart(float hi, float lo) {
 //   Biased scores: the same in place of "equal" with neighbours too close for
 // fp32 to order sigmoid(x) + b (about 1 token in 150), and the second time in
 // fp64 over those that may be among the first k.
-//   Measured, 256 experts, top 8: one token 5.6 us, hardly more than a launch;
-// 16384 tokens, biased sigmoid scores of bf16 logits, 15.2 us (9.4 MB, which alone
-// would take 2): instructions bound it.
+//   Measured, 256 experts, top 8: one token 5.2 to 5.9 us, hardly more than a
+// launch; 16384 tokens, biased sigmoid scores of bf16 logits, 15.4 us (9.4 MB, which
+// alone would take 2), 1156 vector instructions a wave with four waves a SIMD, 8 us
+// of issue.  All scores equal, so that every token goes the 64-bit way: 29.2 us.
+// Without a bias 5.9 us, of fp32 logits 9.5.
 template <class TL, int LPT, int EPL, bool BIAS>
 __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
   constexpr int SLOTS = (kMaxTopk + LPT - 1) / LPT;  // results a lane may hold
@@ -796,8 +798,9 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(BalanceArgs a)
 // The weights: only selected experts receive a gradient of their own; lane j
 // works out position j's and adds it through the group's row in LDS, a
 // repeated expert's positions added up in order first.  Bound by the launch and
-// one trip to memory: 6.9 us at 4096 tokens of 256 fp32 logits (8.7 MB), 8.3 at
-// 30011 of 60 bf16 logits, whose rows do not start on 16 bytes.
+// one trip to memory: 6.6 to 7.0 us at 4096 tokens of 256 fp32 logits (8.7 MB), 8.6
+// at 30011 of 60 bf16 logits, whose rows do not start on 16 bytes and are loaded and
+// stored value by value.
 constexpr int kGradThreads = 256;
 
 template <class TL, int LPT, int EPL>

@@ -20,12 +20,13 @@
 // row's low bits (by the source address, as the loads fill LDS lane after lane)
 // so that operand reads touch every bank once.
 //
-// Measured, 32 experts of 4096 x 7168, top 8: forward of 4096 tokens, gated, 1520
-// us (1.27 PFLOP/s; E4M3 1000 us, 1.92 PFLOP/s), gradients of 2048 tokens 800 us
-// (grad_x, 1.2 PFLOP/s) and 1150 us (grad_w, 0.84 PFLOP/s with 1.9 GB stored).
-// The bf16 products run at a clock that the card lowers for its power (matrix
-// cores 72% busy), grad_w waits for its stores between short products; 16
-// tokens over 64 experts read the weights at 5.9 TB/s (565 us).
+// Measured on several cards, 32 experts of 4096 x 7168, top 8: forward of 4096 tokens,
+// gated, 1500 to 1635 us (1.18 to 1.28 PFLOP/s; E4M3 960 to 1040 us, 1.85 to 2.0
+// PFLOP/s), gradients of 2048 tokens 780 to 820 us (grad_x, 1.2 PFLOP/s) and 1120 to
+// 1180 us (grad_w, 0.84 PFLOP/s with 1.9 GB stored).  In the forward the matrix cores
+// are busy 70 to 72% of the cycles, at a clock that settles at 1.7 to 1.8 GHz of 2.4;
+// E4M3 45% at 2.0 to 2.2 GHz.  grad_w (42%) waits for its stores between short
+// products; 16 tokens over 64 experts read the weights at 5.9 TB/s (558 to 571 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -160,8 +161,8 @@ struct Tile {
 // rows.  Direct: the two units of a step's halves (E4M3: the two halves of a
 // lane's 32 values; which values those are is free as long as both operands
 // agree, and lanes read together then meet no bank twice: with two neighbouring
-// units a lane, conflicts took a sixth of the cycles, 1028 against 1023 us), the
-// fragments 2 KiB apart.  Turned: a place for each fragment.
+// units a lane, conflicts took a sixth of the cycles, though no time beyond the
+// spread of runs), the fragments 2 KiB apart.  Turned: a place for each fragment.
 template <int ROWS, bool TURNED, bool FP8, int COUNT>
 struct Reader {
   static constexpr int N = TURNED ? COUNT : 2;
@@ -929,10 +930,12 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(TileArgs a) {
 
 // A block takes rows of a segment and 512 columns of grad_y (8 a lane) at a time:
 // grad_z in bf16, and, where the bias wants it, the column sums of the unrounded
-// grad_z over those rows, 128 then.  Without, 32 rows: smaller blocks fill the
-// CUs more evenly (16384 rows of 2 x 2048 gated columns, 335 MB: 97 us; 64 rows
-// 107, 128 rows 112).  Few rows are bound by the loads that follow one another,
-// so 8 waves share them (602 rows of 520 columns 7.8 us; 4 waves 12.3).
+// grad_z over those rows, 128 then.  bf16 is the type of the products grad_z goes
+// into: their error grows from 0.0017 of the norm, the results' own rounding, to
+// 0.0023, and fp32 operands would take twice the products.  Without a bias, 32 rows:
+// smaller blocks fill the CUs more evenly (16384 rows of 2 x 2048 gated columns, 335
+// MB: 97 us; 64 rows 107, 128 rows 112).  Few rows are bound by the loads that follow
+// one another, so 8 waves share them (602 rows of 520 columns 7.8 us; 4 waves 12.3).
 constexpr int kGradZWaves = 8;
 
 // Rows a block takes.
@@ -1089,7 +1092,7 @@ void run_tiles(const TileArgs& a, int64_t rows, hipStream_t s) {
 // segments.  Measured, large / small (us): 2048 -> 7168, one segment, 1000 rows,
 // 116 large tiles, 47.3 / 33.0; 1536 rows, 168 tiles, 51.1 / 62.0.  7168 -> 2048
 // gated, 64 experts, 2 rows each 586 / 581, 32 rows 654 / 632; 256 experts, 64
-// rows 2617 / 2649, 128 rows 2854 / 4266.
+// rows 2617 / 2649 (small by the rule, 1% the slower), 128 rows 2854 / 4266.
 template <Mode MODE, bool FP8, int ACT>
 void run_sized(const TileArgs& a, int64_t rows, hipStream_t s) {
   using Large = Tile<MODE, FP8, ACT, 2, 4, 8, 4>;
@@ -1101,7 +1104,8 @@ void run_sized(const TileArgs& a, int64_t rows, hipStream_t s) {
 
 // Few rows: up to 16 an expert where small tiles are no more than the CUs.
 // Measured (us, tiles / few rows): one token over 8 experts of 4096 x 7168, 256
-// tiles, 97 and 94 (E4M3 36.9 and 41.1), 2 experts of 1024 x 7168 35.5 and 19.4
+// tiles, 97 and 94 (E4M3 36.9 and 41.1, where the rule, made for both types, takes
+// the slower), 2 experts of 1024 x 7168 35.5 and 19.4
 // (27.0 and 12.2), one of 7168 x 2048 13.3 and 8.4 (11.0 and 5.7); 16 tokens over
 // 64 experts of 4096 x 7168, 2048 tiles, 584 and 658; 33 rows of one expert 15.5
 // and 15.6.

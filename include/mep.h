@@ -380,12 +380,13 @@ typedef struct mep_gate_config {
  * dispatch and combine take them.  logits is [T,E]; per token,
  *   softmax: the k largest logits; v_j = exp(x_j - max) / sum over all experts
  *            of the same (p_j);
- *   sigmoid: the k largest s_e + bias[e] (bias fp32 [E], NULL for none); v_j =
- *            s_j, without the bias;
+ *   sigmoid: the k largest s_e + bias[e] (bias fp32 [E]), in the order of their
+ *            64-bit values, of which those of logits above about 37 are equal;
+ *            without a bias (NULL) the k largest logits, which tell apart what
+ *            64 bits do not; v_j = s_j, without the bias;
  *   weights[t, j] = scale * v_j, or scale * v_j / sum_j v_j when normalizing.
  * indices (int32) and weights (fp32) are [T,k], largest first; equal values go
- * to the lower expert, and sigmoid scores that fp32 cannot order are compared
- * in 64 bits.  All k experts of a token are different, whatever its logits: NaN
+ * to the lower expert.  All k experts of a token are different, whatever its logits: NaN
  * ranks last, and a selected NaN gives NaN weights, as does a logit of +inf
  * under softmax; where every v_j is 0 (logits of -inf, and sigmoids of logits
  * below -708) the weights are 0.  Quotients are those of exact scores, also where

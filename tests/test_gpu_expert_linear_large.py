@@ -115,6 +115,44 @@ def test_backward(act):
           extra=5).check_large_backward()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_most_experts_in_large_tiles(fp8):
+    # 4096 experts' row tiles beside the operands in LDS
+    E, n, K, N = 4096, 65, 128, 128
+    rows, cap = E * n, E * 128
+    assert takes_large_tiles(N, 256, rows, E) and takes_large_tiles(K, 256, rows, E)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    normal = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    t = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    x, w = normal(E, 128, K).to(t), normal(E, N, K).to(t)
+    ct = torch.full((E,), n, dtype=torch.int32, device="cuda")
+    ot = torch.arange(0, cap + 1, 128, dtype=torch.int32, device="cuda")
+    one = lambda *s: torch.ones(s, device="cuda") if fp8 else None  # noqa: E731
+    cfg = M.MepLinearConfig(E, K, N, M.MEP_ACT_NONE, M.MEP_QUANT_FP8_E4M3_BLOCK128 if fp8
+                            else M.MEP_QUANT_NONE)
+    y = torch.full((E, 128, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    M.mep_expert_linear(cfg, x, one(cap, 1), ct, ot, cap, rows, w, one(E, 1, 1), None, None, y,
+                        None)
+    x64, wt = x[:, :n].double(), w.double().transpose(1, 2).contiguous()
+    ref, mag = torch.matmul(x64, wt), torch.matmul(x64.abs(), wt.abs())
+    # E4M3: 7 * 2^-13 of the largest product in each group of 8, so of the magnitudes
+    err = (K + 2) * R.U32 * mag + (7 * 2.0 ** -13 * mag if fp8 else 0.0)
+    assert bool(((y[:, :n].double() - ref).abs() <= err + R.UBF16 * (ref.abs() + err)).all())
+    assert bool((y[:, n:] == 7.0).all())
+    if fp8:
+        return
+    gx = torch.full((E, 128, K), 7.0, dtype=torch.bfloat16, device="cuda")
+    gy = normal(E, 128, N).bfloat16()
+    ws = torch.empty(M.mep_linear_workspace_bytes(cfg, cap), dtype=torch.uint8, device="cuda")
+    M.mep_expert_linear_backward(cfg, gy, None, x, w, ct, ot, cap, rows, gx, None, None, ws)
+    g64, w64 = gy[:, :n].double(), w.double()
+    ref = torch.matmul(g64, w64)
+    err = (N + 2) * R.U32 * torch.matmul(g64.abs(), w64.abs())
+    assert bool(((gx[:, :n].double() - ref).abs() <= err + R.UBF16 * (ref.abs() + err)).all())
+    assert bool((gx[:, n:] == 7.0).all())
+
+
 def test_offsets_past_32_bits():
     # the second segment lies past 2^31 elements of x, y and their gradients
     K, N, rows = 9160, 9104, 640

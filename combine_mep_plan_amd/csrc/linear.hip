@@ -1105,10 +1105,9 @@ void run_sized(const TileArgs& a, int64_t rows, hipStream_t s) {
 // Few rows: up to 16 an expert where small tiles are no more than the CUs.
 // Measured (us, tiles / few rows): one token over 8 experts of 4096 x 7168, 256
 // tiles, 97 and 94 (E4M3 36.9 and 41.1, where the rule, made for both types, takes
-// the slower), 2 experts of 1024 x 7168 35.5 and 19.4
-// (27.0 and 12.2), one of 7168 x 2048 13.3 and 8.4 (11.0 and 5.7); 16 tokens over
-// 64 experts of 4096 x 7168, 2048 tiles, 584 and 658; 33 rows of one expert 15.5
-// and 15.6.
+// the slower), 2 experts of 1024 x 7168 35.5 and 19.4 (27.0 and 12.2), one of 7168 x
+// 2048 13.3 and 8.4 (11.0 and 5.7); 16 tokens over 64 experts of 4096 x 7168, 2048
+// tiles, 584 and 658; 33 rows of one expert 15.5 and 15.6.
 template <bool FP8, int ACT>
 void run_forward(const TileArgs& a, int64_t rows, hipStream_t s) {
   using Small = Tile<kForward, FP8, ACT, 2, 4, 4, 2>;

@@ -386,12 +386,12 @@ typedef struct mep_gate_config {
  *            64 bits do not; v_j = s_j, without the bias;
  *   weights[t, j] = scale * v_j, or scale * v_j / sum_j v_j when normalizing.
  * indices (int32) and weights (fp32) are [T,k], largest first; equal values go
- * to the lower expert.  All k experts of a token are different, whatever its logits: NaN
- * ranks last, and a selected NaN gives NaN weights, as does a logit of +inf
- * under softmax; where every v_j is 0 (logits of -inf, and sigmoids of logits
- * below -708) the weights are 0.  Quotients are those of exact scores, also where
- * a sigmoid is too small for fp32; this holds for p and the gradients below too.
- * 0 <= T <= 2^26.  MEP_ERR_CONFIG for a bias with softmax scores.
+ * to the lower expert.  All k experts of a token are different, whatever its
+ * logits: NaN ranks last, and a selected NaN gives NaN weights, as does a logit of
+ * +inf under softmax; where every v_j is 0 (logits of -inf, and sigmoids of logits
+ * below -708) the weights are 0.  A sum of v_j too small for fp32 is divided by
+ * all the same, here and in p and the gradients below.  0 <= T <= 2^26.
+ * MEP_ERR_CONFIG for a bias with softmax scores.
  */
 int mep_gate(const mep_gate_config *cfg, const void *logits, const float *bias, int32_t T,
              int32_t *indices, float *weights, void *stream);
@@ -460,18 +460,18 @@ typedef struct mep_linear_config {
  * em_x is [cap_em,K], w [E,Nz,K], bias fp32 [E,Nz] or NULL, residual bf16
  * [cap_em,N] or NULL, y bf16 [cap_em,N]; z, bf16 [cap_em,Nz], receives the
  * product before the activation for mep_expert_linear_backward, or is NULL.
- * E4M3: em_scales fp32 [cap_em,K/128], w_scales fp32 [E,Nz/128,K/128]; a value is
- * code * scale (the matrix instruction adds 8 neighbouring E4M3 products to
+ * E4M3: em_scales fp32 [cap_em,K/128], w_scales fp32 [E,Nz/128,K/128]; a value
+ * is code * scale (the matrix instruction adds 8 neighbouring E4M3 products to
  * within 7 * 2^-13 of the largest of them, and all else in fp32); both NULL for
- * bf16.  Rows outside the segments' counts (padding,
- * rows behind the last segment) are neither used nor written, and rows past
- * cap_em are left out.  em_offsets[e] must be multiples of 128, em_counts[e] >=
- * 0 and segments must not overlap, as the calls above write them; their order is
- * free, and em_offsets[E] is not read.  One segment over a whole batch (E = 1) is
- * an ordinary dense layer.  num_rows is the number
- * of rows to expect in all segments together (T*k): it selects among kernels and
- * sizes the launch; results are complete for any value.  0 <= cap_em <=
- * INT32_MAX.  y and z overlap no input, but y may be residual itself.
+ * bf16. Rows outside the segments' counts (padding, rows behind the last
+ * segment) are neither used nor written, and rows past cap_em are left out.
+ * em_offsets[e] must be multiples of 128, em_counts[e] >= 0 and segments must
+ * not overlap, as the calls above write them; their order is free, and
+ * em_offsets[E] is not read. One segment over a whole batch (E = 1) is an
+ * ordinary dense layer. num_rows is the number of rows to expect in all segments
+ * together (T*k): it selects among kernels and sizes the launch; results are
+ * complete for any value. 0 <= cap_em <= INT32_MAX. y and z overlap no input,
+ * but y may be residual itself.
  */
 int mep_expert_linear(const mep_linear_config *cfg, const void *em_x, const float *em_scales,
                       const int32_t *em_counts, const int32_t *em_offsets, int64_t cap_em,

@@ -39,10 +39,18 @@ MEP_FP32 = 0
 MEP_BF16 = 1
 MEP_SCORE_SOFTMAX = 0
 MEP_SCORE_SIGMOID = 1
+MEP_GROUP_MAX = 0
+MEP_GROUP_TOP2 = 1
 MEP_ACT_NONE = 0
 MEP_ACT_GELU = 1
 MEP_ACT_SILU = 2
 MEP_ACT_SILU_GLU = 3
+MEP_NORM_NONE = 0
+MEP_NORM_RMS = 1
+MEP_NORM_LAYER = 2
+MEP_BLOCK_GATE_NONE = 0
+MEP_BLOCK_GATE_TOKEN = 1
+MEP_BLOCK_GATE_ELEMENT = 2
 
 
 class MepConfig(C.Structure):
@@ -80,6 +88,31 @@ class MepLinearConfig(C.Structure):
     ]
 
 
+class MepNormConfig(C.Structure):
+    _fields_ = [
+        ("hidden_dim", C.c_int32),
+        ("dtype", C.c_int32),
+        ("post", C.c_int32),
+        ("pre", C.c_int32),
+        ("gate", C.c_int32),
+        ("gate_sigmoid", C.c_int32),
+        ("eps", C.c_float),
+        ("weight_offset", C.c_float),
+        ("residual_scale", C.c_float),
+        ("block_scale", C.c_float),
+    ]
+
+
+class MepGrad(C.Structure):
+    _fields_ = [
+        ("data", C.c_void_p),
+        ("out", C.c_void_p),
+        ("numel", C.c_int64),
+        ("dtype", C.c_int32),
+        ("reserved", C.c_int32),
+    ]
+
+
 class MepError(RuntimeError):
     def __init__(self, fn: str, code: int):
         self.code = code
@@ -99,6 +132,7 @@ def lib() -> C.CDLL:
         p, i32, i64, sz = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
         cfgp = C.POINTER(MepConfig)
         gatep, linp = C.POINTER(MepGateConfig), C.POINTER(MepLinearConfig)
+        normp = C.POINTER(MepNormConfig)
         sig = {
             "mep_error_string": ([C.c_int], C.c_char_p),
             "mep_workspace_bytes": ([cfgp], sz),
@@ -127,6 +161,13 @@ def lib() -> C.CDLL:
             "mep_linear_workspace_bytes": ([linp, i64], sz),
             "mep_expert_linear_backward": ([linp, p, p, p, p, p, p, i64, i64, p, p, p, p, sz, p],
                                            C.c_int),
+            "mep_gate_grouped": ([gatep, i32, i32, i32, p, p, i32, p, p, p], C.c_int),
+            "mep_block_norm": ([normp] + [p] * 7 + [i32] + [p] * 5, C.c_int),
+            "mep_block_norm_workspace_bytes": ([normp, i32], sz),
+            "mep_block_norm_backward": ([normp] + [p] * 8 + [i32] + [p] * 8 + [sz, p], C.c_int),
+            "mep_grad_workspace_bytes": ([p, i32], sz),
+            "mep_grad_norm": ([p, i32, p, p, sz, p], C.c_int),
+            "mep_grad_clip": ([p, i32, p, C.c_float, p], C.c_int),
             "mep_probe_e4m3": ([p, p, i64, p], C.c_int),
             "mep_probe_bf16": ([p, p, i64, p], C.c_int),
             "mep_probe_mxfp4": ([p, p, p, i64, p], C.c_int),
@@ -645,6 +686,126 @@ def mep_expert_linear_backward(cfg, grad_y, z, em_x, w, em_counts, em_offsets, c
            ("grad_bias", grad_bias, 4 * E * Nz, "f32"), ("workspace", workspace, 0, "any")),
           lambda f, p, s: f(C.byref(cfg), p[0], p[1], p[2], p[3], p[4], p[5], cap_em, num_rows,
                             p[6], p[7], p[8], p[9], have, s), stream)
+
+
+def mep_gate_grouped(cfg, num_groups, top_groups, group_score, logits, bias, T, indices, weights,
+                     stream=None) -> None:
+    kind, size = _logits_kind(cfg)
+    E, k = cfg.num_experts, cfg.top_k
+    _call("mep_gate_grouped",
+          (("logits", logits, T * E * size, kind), ("bias", bias, 4 * E, "f32"),
+           ("indices", indices, 4 * T * k, "i32"), ("weights", weights, 4 * T * k, "f32")),
+          lambda f, p, s: f(C.byref(cfg), num_groups, top_groups, group_score, p[0], p[1], T, p[2],
+                            p[3], s), stream)
+
+
+def _block_gate(c, T, rows, kind):
+    return (4 * T, "f32") if c.gate == MEP_BLOCK_GATE_TOKEN else (rows, kind)
+
+
+def mep_block_norm(cfg, x, y, gate, post_weight, post_bias, pre_weight, pre_bias, T, s, n, n_codes,
+                   n_scales, stream=None) -> None:
+    H = cfg.hidden_dim
+    kind, size = _logits_kind(cfg)
+    rows, vec = T * H * size, 4 * H
+    gate_bytes, gate_kind = _block_gate(cfg, T, rows, kind)
+    _call("mep_block_norm",
+          (("x", x, rows, kind), ("y", y, rows, kind), ("gate", gate, gate_bytes, gate_kind),
+           ("post_weight", post_weight, vec, "f32"), ("post_bias", post_bias, vec, "f32"),
+           ("pre_weight", pre_weight, vec, "f32"), ("pre_bias", pre_bias, vec, "f32"),
+           ("s", s, rows, kind), ("n", n, rows, kind), ("n_codes", n_codes, T * H, "e4m3"),
+           ("n_scales", n_scales, 4 * T * (H // 128), "f32")),
+          lambda f, p, st: f(C.byref(cfg), p[0], p[1], p[2], p[3], p[4], p[5], p[6], T, p[7], p[8],
+                             p[9], p[10], st), stream)
+
+
+def mep_block_norm_workspace_bytes(cfg, T) -> int:
+    return lib().mep_block_norm_workspace_bytes(C.byref(cfg), T)
+
+
+def mep_block_norm_backward(cfg, grad_s, grad_n, s, y, gate, post_weight, post_bias, pre_weight, T,
+                            grad_x, grad_y, grad_gate, grad_post_weight, grad_post_bias,
+                            grad_pre_weight, grad_pre_bias, workspace, stream=None) -> None:
+    """The workspace is a tensor of mep_block_norm_workspace_bytes(cfg, T) bytes
+    (its size is passed on)."""
+    H = cfg.hidden_dim
+    kind, size = _logits_kind(cfg)
+    rows, vec = T * H * size, 4 * H
+    gate_bytes, gate_kind = _block_gate(cfg, T, rows, kind)
+    have = workspace.nbytes if workspace is not None else 0
+    _call("mep_block_norm_backward",
+          (("grad_s", grad_s, rows, kind), ("grad_n", grad_n, rows, kind), ("s", s, rows, kind),
+           ("y", y, rows, kind), ("gate", gate, gate_bytes, gate_kind),
+           ("post_weight", post_weight, vec, "f32"), ("post_bias", post_bias, vec, "f32"),
+           ("pre_weight", pre_weight, vec, "f32"), ("grad_x", grad_x, rows, kind),
+           ("grad_y", grad_y, rows, kind), ("grad_gate", grad_gate, gate_bytes, gate_kind),
+           ("grad_post_weight", grad_post_weight, vec, "f32"),
+           ("grad_post_bias", grad_post_bias, vec, "f32"),
+           ("grad_pre_weight", grad_pre_weight, vec, "f32"),
+           ("grad_pre_bias", grad_pre_bias, vec, "f32"), ("workspace", workspace, 0, "any")),
+          lambda f, p, st: f(C.byref(cfg), p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], T, p[8],
+                             p[9], p[10], p[11], p[12], p[13], p[14], p[15], have, st), stream)
+
+
+class MepGrads:
+    """The gradients of one model as mep_grad_norm and mep_grad_clip take them: a
+    mep_grad for each tensor (fp32 or bf16, dense, on one GPU).  ``outs`` are the
+    tensors that clipping writes, of the same types and sizes; None: the gradients
+    themselves.  The tensors are kept alive and their memory is used as it was when
+    this was made, so it serves as long as the gradients stay where they are."""
+
+    def __init__(self, grads, outs=None):
+        import torch
+        kinds = {torch.float32: MEP_FP32, torch.bfloat16: MEP_BF16}
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        if len(self.outs) != len(self.grads):
+            raise ValueError(f"MepGrads: {len(self.outs)} outs for {len(self.grads)} gradients")
+        self.device = -1
+        self.array = (MepGrad * max(1, len(self.grads)))()
+        for i, (g, o) in enumerate(zip(self.grads, self.outs)):
+            if g.dtype not in kinds or o.dtype != g.dtype:
+                raise ValueError(f"MepGrads: tensor {i} must be fp32 or bf16 and its out of the "
+                                 f"same type, not {g.dtype} and {o.dtype}")
+            if g.numel() != o.numel():
+                raise ValueError(f"MepGrads: tensor {i} has {g.numel()} values, its out "
+                                 f"{o.numel()}")
+            data, out = _ptr(g), _ptr(o)
+            if self.device < 0:
+                self.device = g.get_device()
+            if g.get_device() != self.device or o.get_device() != self.device:
+                raise ValueError(f"MepGrads: tensor {i} is not on GPU {self.device}")
+            self.array[i] = MepGrad(data, out, g.numel(), kinds[g.dtype], 0)
+
+    def __len__(self):
+        return len(self.grads)
+
+
+def _grads_device(fn, grads, *tensors) -> None:
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and grads.device >= 0 and \
+                t.get_device() != grads.device:
+            raise ValueError(f"{fn}: a tensor is on {t.device}, the gradients are on GPU "
+                             f"{grads.device}")
+
+
+def mep_grad_workspace_bytes(grads) -> int:
+    return lib().mep_grad_workspace_bytes(grads.array, len(grads))
+
+
+def mep_grad_norm(grads, norm, workspace, stream=None) -> None:
+    """``grads`` is a MepGrads; the workspace a tensor of
+    mep_grad_workspace_bytes(grads) zeroed bytes (its size is passed on)."""
+    _grads_device("mep_grad_norm", grads, norm, workspace)
+    have = workspace.nbytes if workspace is not None else 0
+    _call("mep_grad_norm", (("norm", norm, 4, "f32"), ("workspace", workspace, 0, "any")),
+          lambda f, p, s: f(grads.array, len(grads), p[0], p[1], have, s), stream)
+
+
+def mep_grad_clip(grads, norm, max_norm, stream=None) -> None:
+    _grads_device("mep_grad_clip", grads, norm)
+    _call("mep_grad_clip", (("norm", norm, 4, "f32"),),
+          lambda f, p, s: f(grads.array, len(grads), p[0], max_norm, s), stream)
 
 
 def mep_probe_e4m3(inp, out, n, stream=None) -> None:

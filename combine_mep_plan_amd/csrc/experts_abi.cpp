@@ -35,6 +35,35 @@ int check_gate(const mep_gate_config* c, int32_t T) {
   return MEP_OK;
 }
 
+int check_groups(const mep_gate_config& c, int32_t groups, int32_t top, int32_t by) {
+  if (groups < 1 || groups > mep::kMaxGroups || c.num_experts % groups != 0)
+    return MEP_ERR_CONFIG;
+  const int32_t size = c.num_experts / groups;
+  if (top < 1 || top > groups || c.top_k > top * size) return MEP_ERR_CONFIG;
+  if (by != MEP_GROUP_MAX && by != MEP_GROUP_TOP2) return MEP_ERR_CONFIG;
+  return by == MEP_GROUP_TOP2 && size < 2 ? MEP_ERR_CONFIG : MEP_OK;
+}
+
+// What mep_gate and mep_gate_grouped share; cfg and T are checked.
+int gate_args(const mep_gate_config& c, const void* logits, const float* bias, int32_t T,
+              int32_t* indices, float* weights, mep::GateArgs& a) {
+  if (bias && c.score != MEP_SCORE_SIGMOID) return MEP_ERR_CONFIG;
+  if (T > 0 && any_null({logits, indices, weights})) return MEP_ERR_NULL;
+  if (!all_aligned({logits, bias, indices, weights})) return MEP_ERR_ALIGN;
+  a.logits = logits;
+  a.bias = bias;
+  a.indices = indices;
+  a.weights = weights;
+  a.T = T;
+  a.E = c.num_experts;
+  a.k = c.top_k;
+  a.score = c.score;
+  a.dtype = c.dtype;
+  a.normalize = c.normalize != 0;
+  a.scale = c.scale;
+  return MEP_OK;
+}
+
 bool counts_fit(const mep_gate_config& c, int32_t T) {
   return (int64_t)T * c.top_k <= INT32_MAX;
 }
@@ -72,23 +101,23 @@ extern "C" {
 
 int mep_gate(const mep_gate_config* cfg, const void* logits, const float* bias, int32_t T,
              int32_t* indices, float* weights, void* stream) {
-  int rc = check_gate(cfg, T);
-  if (rc != MEP_OK) return rc;
-  if (bias && cfg->score != MEP_SCORE_SIGMOID) return MEP_ERR_CONFIG;
-  if (T > 0 && any_null({logits, indices, weights})) return MEP_ERR_NULL;
-  if (!all_aligned({logits, bias, indices, weights})) return MEP_ERR_ALIGN;
   mep::GateArgs a{};
-  a.logits = logits;
-  a.bias = bias;
-  a.indices = indices;
-  a.weights = weights;
-  a.T = T;
-  a.E = cfg->num_experts;
-  a.k = cfg->top_k;
-  a.score = cfg->score;
-  a.dtype = cfg->dtype;
-  a.normalize = cfg->normalize != 0;
-  a.scale = cfg->scale;
+  int rc = check_gate(cfg, T);
+  if (rc == MEP_OK) rc = gate_args(*cfg, logits, bias, T, indices, weights, a);
+  return rc != MEP_OK ? rc : hip_rc(mep::launch_gate(a, (hipStream_t)stream));
+}
+
+int mep_gate_grouped(const mep_gate_config* cfg, int32_t num_groups, int32_t top_groups,
+                     int32_t group_score, const void* logits, const float* bias, int32_t T,
+                     int32_t* indices, float* weights, void* stream) {
+  mep::GateArgs a{};
+  int rc = check_gate(cfg, T);
+  if (rc == MEP_OK) rc = check_groups(*cfg, num_groups, top_groups, group_score);
+  if (rc == MEP_OK) rc = gate_args(*cfg, logits, bias, T, indices, weights, a);
+  if (rc != MEP_OK) return rc;
+  a.groups = num_groups;
+  a.top_groups = top_groups;
+  a.group_score = group_score;
   return hip_rc(mep::launch_gate(a, (hipStream_t)stream));
 }
 

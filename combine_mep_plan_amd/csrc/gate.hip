@@ -271,6 +271,123 @@ __device__ __forceinline__ bool scores_apart(float hi, float lo) {
   return hi - lo > 4.76837158203125e-07f * (1.0f + fabsf(hi));
 }
 
+// ---- groups of experts ----------------------------------------------------
+
+// What group selection needs of a row besides its registers.
+struct GroupScore {
+  int G, S, M, by, score;
+  float inv_size;    // 1 / S: (e + 1/2) / S cuts down to e's group for every e < 4096
+  const float* bias;
+  bool exact;        // scores are the logits themselves: their order needs no more bits
+};
+
+__device__ __forceinline__ int group_of(const GroupScore& q, int e) {
+  return (int)(((float)e + 0.5f) * q.inv_size);
+}
+
+// A group's score from its two largest; a NaN among the scores counted as -inf.
+template <class T>
+__device__ __forceinline__ T join_top(int by, T first, T second) {
+  return by == MEP_GROUP_TOP2 && first < (T)__builtin_inf() ? first + second : first;
+}
+
+// The M best of G groups as a set of bits, the lower among equals, from the scores of
+// groups l, l + LPT, .. in lane l.  Key: order_key's type.
+template <int LPT, int SLOTS, class Key>
+__device__ __forceinline__ uint64_t best_groups(Key (&key)[SLOTS], int l, int G, int M) {
+  uint64_t chosen = 0;
+  for (int j = 0; j < M; ++j) {
+    uint64_t best = 0;
+    int at = 0x7fff;
+#pragma unroll
+    for (int q = 0; q < SLOTS; ++q) {
+      const int g = q * LPT + l;
+      if (g < G && !((chosen >> g) & 1) && (key[q] > best || at == 0x7fff)) {
+        best = key[q];
+        at = g;
+      }
+    }
+    group_best<LPT>(best, at);
+    chosen |= 1ull << at;
+  }
+  return chosen;
+}
+
+// The groups a token's experts come from.  The scores go through LDS (`shared`, E values
+// of the token's own), from where lane l takes those of groups l, l + LPT, ..  Only
+// which groups are chosen counts, not their order: where the worst chosen and the best
+// left out are too close for fp32, their scores are worked out again in 64 bits.
+// Each score is within 2^-22 (1 + |score|) (see scores_apart; an exponential of a value
+// at most 0 is nearer still), so a sum of two within 2^-21 (2 + |a| + |b|) with its own
+// rounding.
+template <class TL, int LPT, int EPL>
+__device__ __forceinline__ uint64_t choose_groups(const GroupScore& q, const float (&score)[EPL],
+                                                  const TL* row, float shift, int E, int l,
+                                                  float* shared) {
+  constexpr int SLOTS = 64 / LPT;
+  constexpr float kNone = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = expert_of<TL, LPT>(i, l);
+    if (e < E) shared[e] = fmaxf(score[i], kNone);  // NaN: -inf
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  float val[SLOTS], err[SLOTS];
+  uint32_t key[SLOTS];
+#pragma unroll
+  for (int u = 0; u < SLOTS; ++u) {
+    const int g = u * LPT + l;
+    val[u] = err[u] = 0.0f;
+    key[u] = 0u;
+    if (g < q.G) {
+      float a = kNone, b = kNone;
+      for (int i = 0; i < q.S; ++i) {
+        const float v = shared[g * q.S + i];
+        b = fmaxf(b, fminf(a, v));
+        a = fmaxf(a, v);
+      }
+      val[u] = join_top(q.by, a, b);
+      err[u] = q.by == MEP_GROUP_TOP2 ? fabsf(a) + fabsf(b) : fabsf(a);
+      err[u] = 4.76837158203125e-07f * (2.0f + err[u]);
+      key[u] = order_key(val[u]);
+    }
+  }
+  uint64_t chosen = best_groups<LPT>(key, l, q.G, q.M);
+  if (q.exact) return chosen;
+  float low = __builtin_inff(), high = kNone;
+#pragma unroll
+  for (int u = 0; u < SLOTS; ++u) {
+    const int g = u * LPT + l;
+    if (g >= q.G) continue;
+    if ((chosen >> g) & 1) low = fminf(low, val[u] - err[u]);
+    else high = fmaxf(high, val[u] + err[u]);
+  }
+  low = -group_fmax<LPT>(-low);
+  high = group_fmax<LPT>(high);
+  if (low > high) return chosen;
+  uint64_t wide[SLOTS];
+#pragma unroll
+  for (int u = 0; u < SLOTS; ++u) {
+    const int g = u * LPT + l;
+    wide[u] = 0;
+    if (g < q.G) {
+      double a = kNone, b = kNone;
+      for (int i = 0; i < q.S; ++i) {
+        const int e = g * q.S + i;
+        const double x = (double)load_logit(row + e);
+        double v = q.score == MEP_SCORE_SOFTMAX ? exp(x - (double)shift) : 1.0 / (1.0 + exp(-x));
+        if (q.bias) v += (double)q.bias[e];
+        v = fmax(v, (double)kNone);
+        b = fmax(b, fmin(a, v));
+        a = fmax(a, v);
+      }
+      wide[u] = order_key(join_top(q.by, a, b));
+    }
+  }
+  return best_groups<LPT>(wide, l, q.G, q.M);
+}
+
 // k rounds of "largest first, the lowest expert among equals".  The rounds and
 // not the one pass over the logits bound the kernel for many experts, so they
 // are cut down to one subtraction and half a minimum a value: with all keys of
@@ -291,7 +408,7 @@ __device__ __forceinline__ bool scores_apart(float hi, float lo) {
 // alone would take 2), 1156 vector instructions a wave with four waves a SIMD, 8 us
 // of issue.  All scores equal, so that every token goes the 64-bit way: 29.2 us.
 // Without a bias 5.9 us, of fp32 logits 9.5.
-template <class TL, int LPT, int EPL, bool BIAS>
+template <class TL, int LPT, int EPL, bool BIAS, bool GROUPED>
 __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
   constexpr int SLOTS = (kMaxTopk + LPT - 1) / LPT;  // results a lane may hold
   constexpr bool PACKED = !BIAS && sizeof(TL) == 2;
@@ -304,7 +421,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
   float x[EPL], bias[BIAS ? EPL : 1];
   load_row<TL, LPT, EPL>(row, E, l, a.wide, -__builtin_inff(), x);
   if constexpr (BIAS) load_per_expert<TL, LPT, EPL>(a.bias, E, l, a.wide, bias);
-  uint32_t key[EPL];
+  uint32_t key[EPL];  // 0: no expert, or one of a group left out
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = expert_of<TL, LPT>(i, l);
@@ -312,6 +429,38 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
     if constexpr (BIAS) s = fast_sigmoid(s) + bias[i];
     key[i] = e < E ? order_key(s) : 0u;
     if (PACKED && e < E) key[i] = (key[i] & 0xffff0000u) | (uint32_t)(0xffff - e);
+  }
+  int have = E;  // experts to choose from
+  if constexpr (GROUPED) {
+    extern __shared__ float group_scores[];
+    const GroupScore q{a.groups, E / a.groups, a.top_groups, a.group_score, a.score,
+                       1.0f / (float)(E / a.groups), BIAS ? a.bias : nullptr,
+                       !BIAS && a.group_score == MEP_GROUP_MAX};
+    have = q.M * q.S;
+    if (q.M < q.G) {
+      float shift = 0.0f;
+      if (!q.exact && a.score == MEP_SCORE_SOFTMAX) {
+        shift = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) shift = fmaxf(shift, x[i]);
+        shift = group_fmax<LPT>(shift);
+        shift = fabsf(shift) < __builtin_inff() ? shift : 0.0f;
+      }
+      float score[EPL];
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        if constexpr (BIAS) score[i] = fast_sigmoid(x[i]) + bias[i];
+        else if (q.exact) score[i] = x[i];
+        else score[i] = a.score == MEP_SCORE_SOFTMAX ? fast_exp(x[i] - shift) : fast_sigmoid(x[i]);
+      }
+      const uint64_t chosen = choose_groups<TL, LPT, EPL>(
+          q, score, row, shift, E, l, group_scores + (size_t)(threadIdx.x / LPT) * E);
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = expert_of<TL, LPT>(i, l);
+        if (e < E && !((chosen >> group_of(q, e)) & 1)) key[i] = 0u;
+      }
+    }
   }
 
   uint32_t got_key[SLOTS];
@@ -350,7 +499,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
     for (int s = 0; s < SLOTS + 1; ++s) {
       for (int jj = 0; jj < LPT; ++jj) {
         const int j = s * LPT + jj;
-        if (j > k || j >= E) break;
+        if (j > k || j >= have) break;
         uint32_t d = 0xffffffffu;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
@@ -404,7 +553,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         const int e = expert_of<TL, LPT>(i, l);
-        const bool in = e < E && key[i] >= border;
+        const bool in = key[i] != 0u && key[i] >= border;
         uint64_t vote = ballot(in) >> (lane_id() & (64 - LPT));
         if (LPT < 64) vote &= (1ull << (LPT & 63)) - 1;
         const int at = n + __popcll(vote & ((1ull << l) - 1));
@@ -460,7 +609,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
               const int e = expert_of<TL, LPT>(i, l);
-              if (e < E && !((out >> i) & 1)) {
+              if (key[i] != 0u && !((out >> i) & 1)) {
                 const uint64_t q =
                     order_key(1.0 / (1.0 + exp(-(double)x[i])) + (double)bias[i]);
                 if (q > best) {  // registers hold ascending experts: the lowest wins
@@ -965,10 +1114,17 @@ void gate_typed(const GateArgs& a, hipStream_t s) {
   const int64_t threads = (int64_t)a.T * lanes_of(a.E);
   const unsigned blocks = (unsigned)((threads + kGateThreads - 1) / kGateThreads);
   by_experts(a.E, [&](auto lpt, auto epl) {
-    if (a.bias)
-      gate_kernel<TL, lpt(), epl(), true><<<blocks, kGateThreads, 0, s>>>(a);
-    else
-      gate_kernel<TL, lpt(), epl(), false><<<blocks, kGateThreads, 0, s>>>(a);
+    const size_t lds = a.groups ? (size_t)(kGateThreads / lpt()) * a.E * sizeof(float) : 0;
+    auto launch = [&](auto bias, auto grouped) {
+      gate_kernel<TL, lpt(), epl(), bias(), grouped()><<<blocks, kGateThreads, lds, s>>>(a);
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+    if (a.groups) {
+      if (a.bias) launch(Yes{}, Yes{}); else launch(No{}, Yes{});
+    } else {
+      if (a.bias) launch(Yes{}, No{}); else launch(No{}, No{});
+    }
   });
 }
 

@@ -215,6 +215,9 @@ struct GateArgs {              // router: top-k experts and weights
   int32_t* indices;             // [T,k]
   float* weights;               // [T,k]
   int32_t T, E, k, score, dtype, normalize;
+  int32_t groups;               // equal groups of experts, 0: none
+  int32_t top_groups;           // of which a token's experts come from
+  int32_t group_score;          // MEP_GROUP_*
   float scale;
   bool wide;                    // rows are whole 16-byte units, set at launch
 };
@@ -279,6 +282,64 @@ struct LinearBackwardArgs {
 
 constexpr int kSegRows = 128;   // expert segments start at multiples of this many rows
 constexpr int kMaxExperts = kMaxRanks * kMaxEpr;
+constexpr int kMaxGroups = kMaxRanks;  // bits of a 64-bit set
+
+// ---- norms around a block ---------------------------------------------------
+struct NormArgs {
+  const void* x;                // [T,H], or null
+  const void* y;                // [T,H] block's output, or null
+  const void* gate;             // [T] fp32 or [T,H], or null
+  const float* post_weight;     // [H] each, or null
+  const float* post_bias;
+  const float* pre_weight;
+  const float* pre_bias;
+  void* s;                      // [T,H], or null
+  void* n;                      // [T,H], or null
+  void* codes;                  // [T,H] E4M3, or null
+  float* scales;                // [T,H/128]
+  int32_t T, H, dtype, post, pre, gate_kind, sigmoid;
+  float eps, offset, residual_scale, block_scale;
+};
+
+struct NormBackwardArgs {
+  const void* grad_s;           // [T,H], or null
+  const void* grad_n;           // [T,H], or null
+  const void* s;                // [T,H]
+  const void* y;                // [T,H], or null
+  const void* gate;
+  const float* post_weight;
+  const float* post_bias;
+  const float* pre_weight;
+  void* grad_x;                 // [T,H], or null
+  void* grad_y;                 // [T,H], or null
+  void* grad_gate;              // as gate, or null
+  float* columns[4];            // [H] each, or null: post weight, post bias, pre weight, pre bias
+  float* part;                  // workspace [blocks][wanted columns][H]
+  int32_t T, H, dtype, post, pre, gate_kind, sigmoid;
+  float eps, offset, residual_scale, block_scale;
+};
+
+constexpr int32_t kMaxNormRow = 16384;
+
+// ---- gradients of many tensors ----------------------------------------------
+constexpr int kGradsALaunch = 128;  // tensors whose table fits a launch's arguments
+constexpr uint32_t kMaxChunks = 1u << 31;  // of a launch
+
+struct GradTable {
+  const void* data[kGradsALaunch];
+  void* out[kGradsALaunch];
+  int64_t numel_type[kGradsALaunch];  // 2 * values + (bf16: 1)
+  uint32_t first[kGradsALaunch + 1];  // first chunk of each tensor, and their number
+  int32_t n;
+};
+
+struct GradNormArgs {
+  float* norm;                  // [1]
+  double* part;                 // [blocks of all launches] sums of squares
+  uint32_t* done;               // blocks of the last launch that are done; 0 between calls
+  int32_t first_part;           // this launch's first
+  int32_t parts;                // of all launches; 0 in all but the last
+};
 
 // Host-side checks and argument packing shared by the entry points
 // (mep_abi.cpp); each check returns MEP_OK or a MEP_ERR_* code.
@@ -314,6 +375,13 @@ int balance_blocks(int E, int64_t T);  // rows of partial sums a balance call wr
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s);
 hipError_t launch_gate_backward(const GateBackwardArgs& a, hipStream_t s);
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
+hipError_t launch_block_norm(const NormArgs& a, hipStream_t s);
+int norm_backward_blocks(int32_t H, int32_t T);  // rows of partial column sums it writes
+hipError_t launch_block_norm_backward(const NormBackwardArgs& a, hipStream_t s);
+uint32_t grad_chunks(int64_t numel, bool bf16);  // of one tensor
+int32_t grad_norm_blocks(const GradTable& t);    // sums a launch leaves
+hipError_t launch_grad_norm(const GradTable& t, const GradNormArgs& a, hipStream_t s);
+hipError_t launch_grad_clip(const GradTable& t, const float* norm, float max_norm, hipStream_t s);
 hipError_t launch_linear_backward(const LinearBackwardArgs& a, hipStream_t s);
 hipError_t launch_copy_i32(const int32_t* src, int32_t* dst, int64_t n, hipStream_t s);
 hipError_t launch_probe_e4m3(const float* in, uint8_t* out, int64_t n, hipStream_t s);

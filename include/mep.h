@@ -364,6 +364,8 @@ int mep_get_route(mep_handle *h, int32_t *recv_row, int32_t *em_row, void *strea
 #define MEP_BF16 1               /* logits and their gradient: bf16               */
 #define MEP_SCORE_SOFTMAX 0      /* p = softmax of the logits                      */
 #define MEP_SCORE_SIGMOID 1      /* s = 1 / (1 + exp(-x)), p = s / sum of s        */
+#define MEP_GROUP_MAX 0          /* a group of experts counts by its best          */
+#define MEP_GROUP_TOP2 1         /* by the sum of its two best                     */
 
 typedef struct mep_gate_config {
   int32_t num_experts; /* E: 1..4096                                             */
@@ -395,6 +397,24 @@ typedef struct mep_gate_config {
  */
 int mep_gate(const mep_gate_config *cfg, const void *logits, const float *bias, int32_t T,
              int32_t *indices, float *weights, void *stream);
+
+/*
+ * Router over groups of experts: as mep_gate, with the k experts taken from the
+ * top_groups best of num_groups equal groups (group g: experts g*E/num_groups and
+ * on).  With one group per rank a token goes to at most top_groups ranks.  A group's
+ * score is, of the scores of its experts (softmax: p; sigmoid: s + bias),
+ *   MEP_GROUP_MAX    the largest;
+ *   MEP_GROUP_TOP2   the sum of the two largest (the largest where that is +inf).
+ * Groups are chosen in the order of these scores' 64-bit values (MEP_GROUP_MAX
+ * without a bias: in the logits' order), equal ones the lower first; a NaN among the
+ * scores counts as -inf there, and a logit of +inf puts its group first.  Within the chosen groups everything is as in
+ * mep_gate, and so is the gradient (mep_gate_backward).  num_groups: 1..64, divides
+ * E; top_groups: 1..num_groups; k at most the chosen groups' experts; for
+ * MEP_GROUP_TOP2 two experts a group at least (MEP_ERR_CONFIG otherwise).
+ */
+int mep_gate_grouped(const mep_gate_config *cfg, int32_t num_groups, int32_t top_groups,
+                     int32_t group_score, const void *logits, const float *bias, int32_t T,
+                     int32_t *indices, float *weights, void *stream);
 
 /*
  * Load-balance loss of a batch and what it is made of.  With n the tokens that
@@ -498,6 +518,108 @@ int mep_expert_linear_backward(const mep_linear_config *cfg, const void *grad_y,
                                const int32_t *em_offsets, int64_t cap_em, int64_t num_rows,
                                void *grad_x, void *grad_w, float *grad_bias, void *workspace,
                                size_t workspace_bytes, void *stream);
+
+/* ---- norms around a block ------------------------------------------------- */
+#define MEP_NORM_NONE 0          /* hat(u) = u                                     */
+#define MEP_NORM_RMS 1           /* hat(u) = u / sqrt(mean u^2 + eps)              */
+#define MEP_NORM_LAYER 2         /* hat(u) = (u - mean u) / sqrt(var u + eps)      */
+#define MEP_BLOCK_GATE_NONE 0
+#define MEP_BLOCK_GATE_TOKEN 1   /* fp32 [T]: one factor a row                     */
+#define MEP_BLOCK_GATE_ELEMENT 2 /* [T,H] in the rows' type                        */
+
+typedef struct mep_norm_config {
+  int32_t hidden_dim;   /* H: multiple of 8 up to 16384, of 128 where codes are made */
+  int32_t dtype;        /* MEP_FP32 or MEP_BF16: every [T,H] tensor                  */
+  int32_t post;         /* MEP_NORM_* of the block's output                          */
+  int32_t pre;          /* MEP_NORM_* of the new stream, the next block's input      */
+  int32_t gate;         /* MEP_BLOCK_GATE_*                                          */
+  int32_t gate_sigmoid; /* not 0: the gate's factor is 1 / (1 + exp(-gate))          */
+  float eps;            /* > 0                                                       */
+  float weight_offset;  /* o: a weight w stands for the factor o + w                 */
+  float residual_scale; /* a                                                         */
+  float block_scale;    /* c                                                         */
+} mep_norm_config;
+
+/*
+ * What stands between two blocks, in one pass over the rows.  With x [T,H] the stream
+ * before a block, y [T,H] the block's output (mep_combine's, say) and g the gate's
+ * factor of a row or element (1 without a gate), per row
+ *   v = hat_post(y) (o + post_weight) + post_bias
+ *   s = a x + c g v
+ *   n = hat_pre(s) (o + pre_weight) + pre_bias
+ * in fp32, s and n rounded once each to the rows' type (n is of s before its rounding).
+ * s is the new stream; n the next block's input, for its router and, as E4M3 codes with
+ * a scale per 128 columns, for a dispatch with MEP_QUANT_FP8_CARRY:
+ *   n_scales[t, b] = amax_b / 448 (fp32 [T,H/128]),  n_codes = E4M3_rne(n / scale)
+ * of n before its rounding (zeros where amax_b is 0; a block with an infinity or a NaN in
+ * it is NaN throughout).  s, n and n_codes are NULL where not wanted, not all
+ * three.  x NULL: no residual; y NULL: no block part (gate then NULL too), so that the
+ * call norms or only encodes rows; not both NULL.  Weights and biases are fp32 [H]; a
+ * NULL weight stands for the factor 1, a NULL bias for 0.  A row's mean square must fit
+ * fp32.  s may be x or y itself and n may be y itself; other outputs overlap nothing.
+ * 0 <= T <= 2^26.
+ */
+int mep_block_norm(const mep_norm_config *cfg, const void *x, const void *y, const void *gate,
+                   const float *post_weight, const float *post_bias, const float *pre_weight,
+                   const float *pre_bias, int32_t T, void *s, void *n, void *n_codes,
+                   float *n_scales, void *stream);
+
+/*
+ * Gradients of mep_block_norm from those of s and n (either may be NULL: none, not
+ * both; codes pass n's through).  s is the forward call's, needed with grad_n; y and
+ * gate as there.  With gs = grad_s + what hat_pre hands back of grad_n (o + pre_weight),
+ *   grad_x = a gs                                       ([T,H])
+ *   grad_y = what hat_post hands back of c g gs (o + post_weight)   ([T,H])
+ *   grad_gate = c gs v (summed over a row for a factor a row), times the sigmoid's
+ *               slope                                   (as gate)
+ *   grad_post_weight = sum_t c g gs hat_post(y),   grad_post_bias = sum_t c g gs,
+ *   grad_pre_weight = sum_t grad_n hat_pre(s),     grad_pre_bias = sum_t grad_n
+ * (fp32 [H]); each NULL when not wanted, not all seven, and the block's four only with
+ * y, the pre norm's two only with grad_n.  hat_pre is taken at s as it is given.
+ * Results do not depend on timing.  workspace: mep_block_norm_workspace_bytes(cfg, T)
+ * bytes (0 if cfg or T is invalid), of any content; it serves one call at a time.
+ * grad_x may be grad_s itself and grad_y may be y itself; other outputs overlap
+ * nothing.  0 <= T <= 2^26; the sums over no rows are 0.
+ */
+size_t mep_block_norm_workspace_bytes(const mep_norm_config *cfg, int32_t T);
+int mep_block_norm_backward(const mep_norm_config *cfg, const void *grad_s, const void *grad_n,
+                            const void *s, const void *y, const void *gate,
+                            const float *post_weight, const float *post_bias,
+                            const float *pre_weight, int32_t T, void *grad_x, void *grad_y,
+                            void *grad_gate, float *grad_post_weight, float *grad_post_bias,
+                            float *grad_pre_weight, float *grad_pre_bias, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+/* ---- gradients of many tensors --------------------------------------------- */
+typedef struct mep_grad {
+  const void *data; /* the gradient, dense                                           */
+  void *out;        /* where mep_grad_clip puts it: data itself or a buffer of its own */
+  int64_t numel;    /* >= 0; 0: pointers may be NULL                                 */
+  int32_t dtype;    /* MEP_FP32 or MEP_BF16, of both                                 */
+  int32_t reserved; /* 0                                                             */
+} mep_grad;
+
+/*
+ * The norm of n gradients together, norm[0] = sqrt(sum of all values squared) (fp32, on
+ * the device; summed in fp64, so it neither overflows nor vanishes before its rounding;
+ * inf and NaN come through).  grads is a host array, read during the call.  n >= 0, at
+ * most 65536.  workspace: mep_grad_workspace_bytes(grads, n) bytes (0 if grads or n is
+ * invalid), zero-filled before its first use; it serves one call at a time and is ready
+ * for the next when the call has run.  `out` is not used.  Does not depend on timing.
+ */
+size_t mep_grad_workspace_bytes(const mep_grad *grads, int32_t n);
+int mep_grad_norm(const mep_grad *grads, int32_t n, float *norm, void *workspace,
+                  size_t workspace_bytes, void *stream);
+
+/*
+ * Clipping: out = data * min(1, max_norm / (norm[0] + 1e-6)) for each of n gradients,
+ * rounded to its type; norm is mep_grad_norm's, or several ranks' put together.  Where
+ * the factor is 1, tensors that are their own `out` are not touched.  A NaN norm gives
+ * NaN, an infinite one 0 (NaN where the gradient is not finite).  max_norm > 0.
+ * Outputs overlap neither each other nor other inputs.
+ */
+int mep_grad_clip(const mep_grad *grads, int32_t n, const float *norm, float max_norm,
+                  void *stream);
 
 /*
  * Codec probes: run, over n values, exactly the device conversions the

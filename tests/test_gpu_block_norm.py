@@ -1,0 +1,334 @@
+"""The norms around a block and their gradients against 64-bit references, within bounds
+that count roundings (``_block_ref``), and against differences."""
+
+import numpy as np
+import pytest
+import torch
+
+import combine_mep_plan_amd as M
+
+import _block_ref as B
+
+pytestmark = pytest.mark.gpu
+
+KIND = {"none": M.MEP_NORM_NONE, "rms": M.MEP_NORM_RMS, "layer": M.MEP_NORM_LAYER}
+GATE = {"none": M.MEP_BLOCK_GATE_NONE, "token": M.MEP_BLOCK_GATE_TOKEN,
+        "element": M.MEP_BLOCK_GATE_ELEMENT}
+DTYPE = {"fp32": (M.MEP_FP32, torch.float32), "bf16": (M.MEP_BF16, torch.bfloat16)}
+FILL = -7.0
+
+
+class Case:
+    """Inputs of one call on the GPU, and in 64 bits on the host."""
+
+    def __init__(self, T, H, dtype, post="rms", pre="rms", gate="none", sigmoid=0, x=True, y=True,
+                 weights=True, biases=False, a=1.0, c=1.0, offset=0.0, eps=1e-5, seed=0, mean=0.0):
+        self.T, self.H, self.dtype, self.torch = T, H, dtype, DTYPE[dtype][1]
+        self.post, self.pre, self.gate_kind, self.sigmoid = post, pre, gate, sigmoid
+        self.cfg = M.MepNormConfig(H, DTYPE[dtype][0], KIND[post], KIND[pre], GATE[gate], sigmoid,
+                                   eps, offset, a, c)
+        f = lambda v: float(np.float32(v))  # noqa: E731  as the config holds it
+        self.ref = dict(post=post, pre=pre, sigmoid=sigmoid, eps=f(eps), offset=f(offset), a=f(a),
+                        c=f(c))
+        rng = np.random.default_rng(seed)
+        rows = lambda: mean + rng.standard_normal((T, H)) * (0.2 + 2 * rng.random((T, 1)))  # noqa: E731
+        self.x = self.put(rows()) if x else None
+        self.y = self.put(rows()) if y else None
+        self.gate = None
+        if gate == "token":
+            self.gate = self.put(rng.standard_normal(T), torch.float32)
+        elif gate == "element":
+            self.gate = self.put(rng.standard_normal((T, H)))
+        vec = lambda on, m: self.put(m + 0.3 * rng.standard_normal(H), torch.float32) if on else None  # noqa: E731
+        self.wp, self.wn = vec(weights, 1.0), vec(weights, 1.0)
+        self.bp, self.bn = vec(biases, 0.0), vec(biases, 0.0)
+        self.gs, self.gn = self.put(rng.standard_normal((T, H))), self.put(rng.standard_normal((T, H)))
+
+    def put(self, v, dtype=None):
+        return torch.from_numpy(np.asarray(v, np.float32)).to(dtype or self.torch).cuda()
+
+    def rows(self, dtype=None, cols=None):
+        """An output with a row behind the last, which the call must leave."""
+        return torch.full((self.T + 1, cols or self.H), FILL, device="cuda").to(dtype or self.torch)
+
+    def forward(self, s=True, n=True, codes=False, stream=None):
+        self.s, self.n = self.rows() if s else None, self.rows() if n else None
+        self.codes = self.rows(torch.float8_e4m3fn) if codes else None
+        self.scales = self.rows(torch.float32, self.H // 128) if codes else None
+        M.mep_block_norm(self.cfg, self.x, self.y, self.gate, self.wp, self.bp, self.wn, self.bn,
+                         self.T, self.s, self.n, self.codes, self.scales, stream)
+        torch.cuda.synchronize()
+        for t in (self.s, self.n, self.codes, self.scales):
+            assert t is None or bool((t[self.T:].float() == FILL).all())
+
+    def backward(self, stream_rows, want=None, stream=None):
+        want = want or ("x", "y", "gate", "post_weight", "post_bias", "pre_weight", "pre_bias")
+        z = lambda n, t: torch.full_like(t, FILL) if n in want and t is not None else None  # noqa: E731
+        col = lambda n, on: torch.full((self.H,), FILL, device="cuda") if n in want and on else None  # noqa: E731
+        g = {"x": z("x", stream_rows), "y": z("y", self.y), "gate": z("gate", self.gate),
+             "post_weight": col("post_weight", self.y is not None),
+             "post_bias": col("post_bias", self.y is not None),
+             "pre_weight": col("pre_weight", self.gn is not None),
+             "pre_bias": col("pre_bias", self.gn is not None)}
+        ws = torch.full((M.mep_block_norm_workspace_bytes(self.cfg, self.T),), 255,
+                        dtype=torch.uint8, device="cuda")  # of any content
+        M.mep_block_norm_backward(self.cfg, self.gs, self.gn, stream_rows, self.y, self.gate,
+                                  self.wp, self.bp, self.wn, self.T, *g.values(), ws, stream)
+        torch.cuda.synchronize()
+        return {k: v for k, v in g.items() if v is not None}
+
+
+def h64(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+def close(got, value, bound, what):
+    got = h64(got) if torch.is_tensor(got) else got
+    bad = ~(np.abs(got - value) <= bound)
+    assert not bad.any(), (what, int(bad.sum()), np.argwhere(bad)[:3], got[bad][:3], value[bad][:3],
+                           bound[bad][:3])
+
+
+def check_forward(k, s=True, n=True, codes=False):
+    k.forward(s, n, codes)
+    (rs, es), (rn, en) = B.block_norm(k.ref, h64(k.x), h64(k.y), h64(k.gate), h64(k.wp), h64(k.bp),
+                                      h64(k.wn), h64(k.bn))
+    if s:
+        close(k.s[:k.T], rs, B.rounded(rs, es, k.dtype), "s")
+    if n:
+        close(k.n[:k.T], rn, B.rounded(rn, en, k.dtype), "n")
+    if codes:
+        blocks = lambda v: v.reshape(k.T, -1, 128)  # noqa: E731
+        scale = h64(k.scales)[:k.T]
+        amax, most = np.abs(blocks(rn)).max(axis=2), blocks(en).max(axis=2)
+        close(scale, amax / 448, (most + 2 * B.U32 * amax) / 448 + 1e-45, "scales")
+        got = blocks(h64(k.codes)[:k.T]) * scale[:, :, None]
+        # half a step of E4M3: 2^-4 of the value, at least 2^-10 of the scale
+        close(got, blocks(rn), blocks(en) + np.maximum(2.0 ** -4 * np.abs(blocks(rn)), 2.0 ** -10
+                                                       * scale[:, :, None]) * (1 + 2.0 ** -18),
+              "codes")
+    return k
+
+
+SIZES = [(1, 8), (3, 64), (1, 7168), (257, 72), (70, 512), (33, 520), (40, 1024), (21, 1032),
+         (5, 2048), (300, 2056), (9, 4104), (1100, 128), (17, 7168), (6, 8192), (5, 8200), (3, 16384)]
+
+
+@pytest.mark.parametrize("T,H", SIZES)
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("post,pre", [("rms", "rms"), ("layer", "layer"), ("none", "rms"),
+                                      ("layer", "none")])
+def test_forward(T, H, dtype, post, pre):
+    gate = ("none", "token", "element")[(T + H // 8) % 3]
+    check_forward(Case(T, H, dtype, post, pre, gate, sigmoid=T % 2, biases=post == "layer", a=0.5,
+                       c=1.5, offset=1.0 if pre == "rms" else 0.0, seed=T + H))
+
+
+@pytest.mark.parametrize("gate", ["none", "token", "element"])
+@pytest.mark.parametrize("sigmoid", [0, 1])
+@pytest.mark.parametrize("H", [1024, 1536])
+def test_forward_gates(gate, sigmoid, H):
+    check_forward(Case(37, H, "bf16", "rms", "rms", gate, sigmoid, seed=H))
+    check_forward(Case(37, H, "fp32", "none", "rms", gate, sigmoid, weights=False, seed=H))
+
+
+@pytest.mark.parametrize("T,H", [(1, 128), (30, 1024), (7, 1152), (129, 7168), (3, 16384)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_codes(T, H, dtype):
+    k = check_forward(Case(T, H, dtype, "rms", "rms", "token", 1, seed=H), codes=True)
+    if dtype == "fp32":  # the codes of exactly the rows that n holds
+        n, scale = k.n[:T].cpu(), k.scales[:T].cpu()
+        want = (n.reshape(T, -1, 128) / scale[:, :, None]).reshape(T, H).to(torch.float8_e4m3fn)
+        assert torch.equal(want.view(torch.uint8), k.codes[:T].cpu().view(torch.uint8))
+    check_forward(Case(T, H, dtype, "none", "rms", y=False, seed=H), s=False, n=False, codes=True)
+    # without a norm the call only encodes rows
+    check_forward(Case(T, H, dtype, "none", "none", y=False, weights=False, seed=H), s=False, n=False,
+                  codes=True)
+
+
+def test_codes_of_zero_tiny_and_non_finite_blocks():
+    k = Case(6, 384, "fp32", "none", "none", y=False, weights=False)
+    x = torch.randn((6, 384), generator=torch.Generator().manual_seed(2))
+    x[0, :128] = 0.0
+    x[1, 128:256] *= 1e-38 / 4     # scales below fp32's normal numbers
+    x[2, 300] = float("inf")
+    x[3, 7] = float("nan")
+    x[4] *= 1e37
+    k.x = x.cuda()
+    k.forward(True, True, True)
+    codes, scale = k.codes[:6].cpu(), k.scales[:6].cpu()
+    assert bool((codes[0, :128].float() == 0).all()) and float(scale[0, 0]) == 0
+    value = codes.float().reshape(6, 3, 128) * scale[:, :, None]
+    spoilt = torch.zeros((6, 3), dtype=torch.bool)
+    spoilt[2, 2] = spoilt[3, 0] = True
+    assert bool(torch.isnan(value[spoilt]).all()) and bool(torch.isfinite(value[~spoilt]).all())
+    off = (value - x.reshape(6, 3, 128)).abs()
+    lim = torch.maximum(x.reshape(6, 3, 128).abs() / 16, scale[:, :, None] / 1024) * 1.001
+    lim[1, 1] = scale[1, 1] * 32   # the scale itself has few bits there: its half-step times 448
+    assert bool((off <= lim)[~spoilt].all())
+
+
+@pytest.mark.parametrize("H", [256, 4096])
+@pytest.mark.parametrize("pre", ["rms", "layer"])
+def test_zero_constant_and_large_rows(pre, H):
+    k = Case(4, H, "fp32", "none", pre, y=False, seed=3)
+    k.x[0] = 0.0
+    k.x[1] = 3.0
+    k.x[2] *= 1e15
+    k.x[3] *= 1e-20
+    check_forward(k)
+
+
+def test_parts_that_are_not_there():
+    check_forward(Case(9, 640, "bf16", x=False, seed=1))           # no residual
+    check_forward(Case(9, 640, "bf16", y=False, seed=1))           # no block
+    check_forward(Case(9, 640, "bf16", seed=1), n=False)           # the stream alone
+    check_forward(Case(9, 640, "bf16", seed=1), s=False)
+    check_forward(Case(9, 640, "bf16", weights=False, biases=True, seed=1))
+    k = Case(0, 640, "bf16")
+    k.forward()                                                    # no rows
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("H", [640, 2056])
+def test_in_place(dtype, H):
+    k = Case(300, H, dtype, "rms", "layer", "token", 1, seed=4)
+    k.forward()
+    s, n = k.s[:300].clone(), k.n[:300].clone()
+    x, y = k.x.clone(), k.y.clone()
+    M.mep_block_norm(k.cfg, x, y, k.gate, k.wp, k.bp, k.wn, k.bn, 300, x, y, None, None)
+    torch.cuda.synchronize()
+    assert torch.equal(x, s) and torch.equal(y, n)
+    want = k.backward(k.x)
+    gs, y = k.gs.clone(), k.y.clone()
+    ws = torch.zeros(M.mep_block_norm_workspace_bytes(k.cfg, 300), dtype=torch.uint8, device="cuda")
+    M.mep_block_norm_backward(k.cfg, gs, k.gn, k.x, y, k.gate, k.wp, k.bp, k.wn, 300, gs, y, None,
+                              None, None, None, None, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(gs, want["x"]) and torch.equal(y, want["y"])
+
+
+# ---- gradients ---------------------------------------------------------------
+
+def reference_gradients(k, s):
+    return B.block_norm_backward(k.ref, h64(k.gs), h64(k.gn), h64(s), h64(k.y), h64(k.gate),
+                                 h64(k.wp), h64(k.bp), h64(k.wn), max(1, k.T))
+
+
+def check_backward(k, want=None):
+    s = k.x if k.x is not None else k.put(np.random.default_rng(8).standard_normal((k.T, k.H)))
+    got = k.backward(s, want)
+    ref = reference_gradients(k, s)
+    assert want is None or set(want) >= set(got)
+    for name, t in got.items():
+        value, err = ref[name]
+        vector = name.startswith(("p", "b")) or (name == "gate" and k.gate_kind == "token")
+        close(t, value, B.rounded(value, err, "fp32" if vector else k.dtype), name)
+    return got, ref, s
+
+
+@pytest.mark.parametrize("T,H", SIZES)
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("post,pre", [("rms", "rms"), ("layer", "layer"), ("none", "rms"),
+                                      ("layer", "none")])
+def test_backward(T, H, dtype, post, pre):
+    gate = ("token", "element", "none")[(T + H // 8) % 3]
+    check_backward(Case(T, H, dtype, post, pre, gate, sigmoid=T % 2, biases=post == "layer", a=0.5,
+                        c=1.5, offset=1.0 if pre == "rms" else 0.0, seed=T + H))
+
+
+@pytest.mark.parametrize("gate", ["none", "token", "element"])
+@pytest.mark.parametrize("sigmoid", [0, 1])
+@pytest.mark.parametrize("H", [1024, 1536])
+def test_backward_gates(gate, sigmoid, H):
+    check_backward(Case(600, H, "bf16", "rms", "rms", gate, sigmoid, seed=H))
+    check_backward(Case(37, H, "fp32", "none", "rms", gate, sigmoid, weights=False, biases=True, seed=H))
+
+
+def test_backward_of_what_is_asked():
+    full, _, _ = check_backward(Case(50, 640, "bf16", "rms", "layer", "token", 1, biases=True, seed=2))
+    for want in (("x",), ("y",), ("gate",), ("post_weight",), ("pre_bias",), ("post_bias", "pre_weight"),
+                 ("x", "pre_weight")):
+        k = Case(50, 640, "bf16", "rms", "layer", "token", 1, biases=True, seed=2)
+        got, _, _ = check_backward(k, want)
+        assert set(got) == set(want)
+        assert all(torch.equal(got[n], full[n]) for n in want)
+    k = Case(50, 640, "bf16", seed=2)
+    k.gs = None
+    check_backward(k)                            # of n alone
+    k = Case(50, 640, "bf16", "layer", seed=2)
+    k.gn = None
+    check_backward(k)                            # of s alone
+    k = Case(50, 640, "bf16", y=False, seed=2)
+    check_backward(k)                            # no block
+    k = Case(0, 640, "bf16", seed=2)
+    got = k.backward(k.x)
+    assert all(bool((got[n] == 0).all()) for n in ("post_weight", "post_bias", "pre_weight", "pre_bias"))
+
+
+@pytest.mark.parametrize("post,pre", [("rms", "layer"), ("layer", "rms"), ("none", "none")])
+@pytest.mark.parametrize("gate", ["token", "element"])
+def test_gradients_are_the_definitions(post, pre, gate):
+    """By differentiating the forward formula in 64 bits, and by its differences along a
+    random direction of all inputs at once."""
+    k = Case(24, 264, "fp32", post, pre, gate, 1, biases=True, a=0.7, c=1.3, offset=1.0, seed=11)
+    names = ("x", "y", "gate", "wp", "bp", "wn", "bn")
+    inputs = {n: getattr(k, n).cpu().double().requires_grad_(True) for n in names}
+    gs, gn = k.gs.cpu().double(), k.gn.cpu().double()
+
+    def hat(kind, u):
+        if kind == "layer":
+            u = u - u.mean(1, keepdim=True)
+        return u if kind == "none" else u / torch.sqrt((u * u).mean(1, keepdim=True) + k.ref["eps"])
+
+    def total(i):
+        g = torch.sigmoid(i["gate"])
+        v = hat(post, i["y"]) * (1 + i["wp"]) + i["bp"]
+        s = k.ref["a"] * i["x"] + k.ref["c"] * (g[:, None] if gate == "token" else g) * v
+        n = hat(pre, s) * (1 + i["wn"]) + i["bn"]
+        return (s * gs).sum() + (n * gn).sum(), s
+
+    loss, s = total(inputs)
+    want = dict(zip(names, torch.autograd.grad(loss, list(inputs.values()))))
+    stream = s.detach().float().cuda()
+    got = k.backward(stream)
+    ref = reference_gradients(k, stream)
+    called = dict(zip(names, ("x", "y", "gate", "post_weight", "post_bias", "pre_weight", "pre_bias")))
+    # the stream rounds to fp32 on its way: a half-step of every value, through a norm
+    # whose second derivative is below 8 r^2 |g| at these rows: far below 1e-5 of the norm
+    for n in names:
+        off = (got[called[n]].cpu().double() - want[n]).norm() / want[n].norm()
+        assert off <= 1e-5, (n, off)
+        value = torch.from_numpy(ref[called[n]][0])
+        assert (value - want[n]).norm() <= 1e-5 * want[n].norm(), n
+    rng = torch.Generator().manual_seed(1)
+    d = {n: torch.randn(t.shape, generator=rng, dtype=torch.float64) for n, t in inputs.items()}
+    h = 1e-6
+    with torch.no_grad():
+        up, _ = total({n: inputs[n] + h * d[n] for n in names})
+        down, _ = total({n: inputs[n] - h * d[n] for n in names})
+    slope = sum(float((got[called[n]].cpu().double() * d[n]).sum()) for n in names)
+    size = sum(float((want[n] * d[n]).norm()) for n in names)
+    # fp32 gradients 1e-5 of their norms at most, differences h^2 and 1e-16/h of the sums
+    assert abs(float(up - down) / (2 * h) - slope) <= 1e-5 * size + 1e-8 * float(gn.abs().sum())
+
+
+def test_results_repeat():
+    k = Case(2000, 1536, "bf16", "rms", "rms", "token", 1, seed=5)
+    a, b = k.backward(k.x), k.backward(k.x)
+    assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+def test_long_batch():
+    # rows past 2^31 elements
+    T, H = (1 << 31) // 16384 + 3, 16384
+    cfg = M.MepNormConfig(H, M.MEP_BF16, M.MEP_NORM_NONE, M.MEP_NORM_RMS, 0, 0, 1e-6, 0.0, 1.0, 1.0)
+    x = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn((3, H), generator=torch.Generator().manual_seed(3)).cuda()
+    n = torch.zeros_like(x)
+    M.mep_block_norm(cfg, x, None, None, None, None, None, None, T, None, n, None, None)
+    torch.cuda.synchronize()
+    small = torch.zeros((3, H), dtype=torch.bfloat16, device="cuda")
+    M.mep_block_norm(cfg, x[-3:].contiguous(), None, None, None, None, None, None, 3, None, small, None,
+                     None)
+    assert torch.equal(n[-3:], small) and bool(small.any()) and not bool(n[:-3].any())

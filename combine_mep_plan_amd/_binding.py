@@ -795,7 +795,7 @@ def mep_grad_workspace_bytes(grads) -> int:
 
 def mep_grad_norm(grads, norm, workspace, stream=None) -> None:
     """``grads`` is a MepGrads; the workspace a tensor of
-    mep_grad_workspace_bytes(grads) zeroed bytes (its size is passed on)."""
+    mep_grad_workspace_bytes(grads) bytes (its size is passed on)."""
     _grads_device("mep_grad_norm", grads, norm, workspace)
     have = workspace.nbytes if workspace is not None else 0
     _call("mep_grad_norm", (("norm", norm, 4, "f32"), ("workspace", workspace, 0, "any")),

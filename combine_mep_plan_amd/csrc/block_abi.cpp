@@ -10,7 +10,6 @@ namespace {
 
 constexpr int32_t kMaxTokens = 1 << 26;
 constexpr int32_t kMaxGrads = 65536;
-constexpr size_t kCounterBytes = 256;  // gradients' workspace: the blocks' counter
 
 bool aligned(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 bool all_aligned(std::initializer_list<const void*> ps) {  // null pointers pass
@@ -66,7 +65,7 @@ int by_tables(const mep_grad* g, int32_t n, F f) {
       ++i;
     }
     t.first[t.n] = (uint32_t)chunks;
-    if (const int rc = f(t, i >= n); rc != MEP_OK) return rc;
+    if (const int rc = f(t); rc != MEP_OK) return rc;
   } while (i < n);
   return MEP_OK;
 }
@@ -181,11 +180,11 @@ int mep_block_norm_backward(const mep_norm_config* cfg, const void* grad_s, cons
 size_t mep_grad_workspace_bytes(const mep_grad* grads, int32_t n) {
   if (check_grads(grads, n) != MEP_OK) return 0;
   size_t parts = 0;
-  by_tables(grads, n, [&](const mep::GradTable& t, bool) {
+  by_tables(grads, n, [&](const mep::GradTable& t) {
     parts += (size_t)mep::grad_norm_blocks(t);
     return MEP_OK;
   });
-  return kCounterBytes + parts * sizeof(double);
+  return parts * sizeof(double);
 }
 
 int mep_grad_norm(const mep_grad* grads, int32_t n, float* norm, void* workspace,
@@ -199,17 +198,15 @@ int mep_grad_norm(const mep_grad* grads, int32_t n, float* norm, void* workspace
   for (int32_t i = 0; i < n; ++i)
     if (!aligned(grads[i].data)) return MEP_ERR_ALIGN;
   if (workspace_bytes < mep_grad_workspace_bytes(grads, n)) return MEP_ERR_SHAPE;
-  mep::GradNormArgs a{};
-  a.norm = norm;
-  a.done = (uint32_t*)workspace;
-  a.part = (double*)((unsigned char*)workspace + kCounterBytes);
-  return by_tables(grads, n, [&](const mep::GradTable& t, bool last) {
-    const int32_t blocks = mep::grad_norm_blocks(t);
-    a.parts = last ? a.first_part + blocks : 0;
-    const hipError_t e = mep::launch_grad_norm(t, a, (hipStream_t)stream);
-    a.first_part += blocks;
+  double* part = (double*)workspace;
+  rc = by_tables(grads, n, [&](const mep::GradTable& t) {
+    const hipError_t e = mep::launch_grad_norm(t, part, (hipStream_t)stream);
+    part += mep::grad_norm_blocks(t);
     return hip_rc(e);
   });
+  if (rc != MEP_OK) return rc;
+  return hip_rc(mep::launch_grad_join((double*)workspace, (int32_t)(part - (double*)workspace), norm,
+                                      (hipStream_t)stream));
 }
 
 int mep_grad_clip(const mep_grad* grads, int32_t n, const float* norm, float max_norm,
@@ -223,7 +220,7 @@ int mep_grad_clip(const mep_grad* grads, int32_t n, const float* norm, float max
   if (!aligned(norm)) return MEP_ERR_ALIGN;
   for (int32_t i = 0; i < n; ++i)
     if (!all_aligned({grads[i].data, grads[i].out})) return MEP_ERR_ALIGN;
-  return by_tables(grads, n, [&](const mep::GradTable& t, bool) {
+  return by_tables(grads, n, [&](const mep::GradTable& t) {
     return hip_rc(mep::launch_grad_clip(t, norm, max_norm, (hipStream_t)stream));
   });
 }

@@ -333,13 +333,6 @@ struct GradTable {
   int32_t n;
 };
 
-struct GradNormArgs {
-  float* norm;                  // [1]
-  double* part;                 // [blocks of all launches] sums of squares
-  uint32_t* done;               // blocks of the last launch that are done; 0 between calls
-  int32_t first_part;           // this launch's first
-  int32_t parts;                // of all launches; 0 in all but the last
-};
 
 // Host-side checks and argument packing shared by the entry points
 // (mep_abi.cpp); each check returns MEP_OK or a MEP_ERR_* code.
@@ -380,7 +373,8 @@ int norm_backward_blocks(int32_t H, int32_t T);  // rows of partial column sums 
 hipError_t launch_block_norm_backward(const NormBackwardArgs& a, hipStream_t s);
 uint32_t grad_chunks(int64_t numel, bool bf16);  // of one tensor
 int32_t grad_norm_blocks(const GradTable& t);    // sums a launch leaves
-hipError_t launch_grad_norm(const GradTable& t, const GradNormArgs& a, hipStream_t s);
+hipError_t launch_grad_norm(const GradTable& t, double* part, hipStream_t s);
+hipError_t launch_grad_join(const double* part, int32_t n, float* norm, hipStream_t s);
 hipError_t launch_grad_clip(const GradTable& t, const float* norm, float max_norm, hipStream_t s);
 hipError_t launch_linear_backward(const LinearBackwardArgs& a, hipStream_t s);
 hipError_t launch_copy_i32(const int32_t* src, int32_t* dst, int64_t n, hipStream_t s);

@@ -604,8 +604,8 @@ typedef struct mep_grad {
  * the device; summed in fp64, so it neither overflows nor vanishes before its rounding;
  * inf and NaN come through).  grads is a host array, read during the call.  n >= 0, at
  * most 65536.  workspace: mep_grad_workspace_bytes(grads, n) bytes (0 if grads or n is
- * invalid), zero-filled before its first use; it serves one call at a time and is ready
- * for the next when the call has run.  `out` is not used.  Does not depend on timing.
+ * invalid), of any content; it serves one call at a time.  `out` is not used.  Does not
+ * depend on timing.
  */
 size_t mep_grad_workspace_bytes(const mep_grad *grads, int32_t n);
 int mep_grad_norm(const mep_grad *grads, int32_t n, float *norm, void *workspace,

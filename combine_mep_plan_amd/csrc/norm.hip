@@ -23,6 +23,7 @@ namespace {
 constexpr int kUnit = 8;           // values of a unit
 constexpr int kMaxWaves = 16;      // of a block
 constexpr int kCodeBlock = 128;    // columns that share an E4M3 scale
+constexpr int kShare = kCodeBlock / kUnit;  // units that do
 
 // ---- sums over a row --------------------------------------------------------
 
@@ -39,6 +40,19 @@ __device__ __forceinline__ float sum16(float v) {
   v = dpp_add<0x4E>(v);
   v = dpp_add<0x141>(v);
   return dpp_add<0x140>(v);
+}
+
+// The largest of 16 lanes, in every lane; values >= 0.
+__device__ __forceinline__ float max16(float v) {
+  auto step = [&](auto ctrl) {
+    const int u = __float_as_int(v);
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(u, u, ctrl(), 0xf, 0xf, false)));
+  };
+  step(std::integral_constant<int, 0xB1>{});
+  step(std::integral_constant<int, 0x4E>{});
+  step(std::integral_constant<int, 0x141>{});
+  step(std::integral_constant<int, 0x140>{});
+  return v;
 }
 
 __device__ __forceinline__ float wave_sum(float v) {
@@ -83,50 +97,82 @@ struct RowSum {
 
 // ---- units ------------------------------------------------------------------
 
+// One row of a tensor as a buffer: what lies outside (the units past a row's end, and
+// everything where there is no such tensor or row) reads as 0 and is not written.
+struct RowBuffer {
+  __amdgpu_buffer_rsrc_t r;
+
+  __device__ __forceinline__ RowBuffer(const void* p, int64_t t, int64_t T, int bytes) {
+    constexpr int kRaw = 0x00027000;  // untyped, offsets in bytes
+    const bool on = p != nullptr && t < T;
+    r = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<unsigned char*>(reinterpret_cast<const unsigned char*>(p)) + t * bytes, 0,
+        on ? bytes : 0, kRaw);
+  }
+};
+
+constexpr int kPast = 2;  // cache policy of loads and stores: rows are passed once (nt)
+
 template <class TL>
 struct Raw;
 template <>
 struct Raw<uint16_t> {
   u32x4 q;
-  __device__ __forceinline__ void load(const void* p, int64_t unit) {
-    q = reinterpret_cast<const u32x4*>(p)[unit];
+  __device__ __forceinline__ void load(const RowBuffer& b, int unit) {
+    q = __builtin_amdgcn_raw_buffer_load_b128(b.r, unit * 16, 0, kPast);
   }
   __device__ __forceinline__ float at(int i) const { return i & 1 ? bf16_hi(q[i / 2]) : bf16_lo(q[i / 2]); }
+  // The compiler forgets what it has made of the values so far, and widens them again
+  // where they are needed next instead of keeping them in twice the registers.
+  __device__ __forceinline__ void hold() { asm volatile("" : "+v"(q)); }
 };
 template <>
 struct Raw<float> {
   u32x4 q[2];
-  __device__ __forceinline__ void load(const void* p, int64_t unit) {
-    q[0] = reinterpret_cast<const u32x4*>(p)[2 * unit];
-    q[1] = reinterpret_cast<const u32x4*>(p)[2 * unit + 1];
+  __device__ __forceinline__ void load(const RowBuffer& b, int unit) {
+    q[0] = __builtin_amdgcn_raw_buffer_load_b128(b.r, unit * 32, 0, kPast);
+    q[1] = __builtin_amdgcn_raw_buffer_load_b128(b.r, unit * 32 + 16, 0, kPast);
   }
   __device__ __forceinline__ float at(int i) const { return __uint_as_float(q[i / 4][i % 4]); }
+  __device__ __forceinline__ void hold() { asm volatile("" : "+v"(q[0]), "+v"(q[1])); }
 };
 
-__device__ __forceinline__ void store_unit(uint16_t*, void* p, int64_t unit, const float (&v)[kUnit]) {
+__device__ __forceinline__ void store_unit(uint16_t*, const RowBuffer& b, int unit,
+                                           const float (&v)[kUnit]) {
   u32x4 q;
 #pragma unroll
   for (int i = 0; i < 4; ++i) q[i] = pack_bf16_rne(v[2 * i], v[2 * i + 1]);
-  reinterpret_cast<u32x4*>(p)[unit] = q;
+  __builtin_amdgcn_raw_buffer_store_b128(q, b.r, unit * 16, 0, kPast);
 }
-__device__ __forceinline__ void store_unit(float*, void* p, int64_t unit, const float (&v)[kUnit]) {
-  float4* to = reinterpret_cast<float4*>(p) + 2 * unit;
-  to[0] = make_float4(v[0], v[1], v[2], v[3]);
-  to[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void store_unit(float*, const RowBuffer& b, int unit,
+                                           const float (&v)[kUnit]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const u32x4 q = {__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]),
+                     __float_as_uint(v[4 * h + 2]), __float_as_uint(v[4 * h + 3])};
+    __builtin_amdgcn_raw_buffer_store_b128(q, b.r, unit * 32 + 16 * h, 0, kPast);
+  }
 }
 
-// A vector's values at a unit; `none` where there is no vector, else plus `offset`.
-__device__ __forceinline__ void load_vector(const float* p, int unit, float none, float offset,
-                                            float (&v)[kUnit]) {
-  if (p) {
-    const float4* q = reinterpret_cast<const float4*>(p) + 2 * unit;
-    const float4 a = q[0], b = q[1];
-    v[0] = offset + a.x; v[1] = offset + a.y; v[2] = offset + a.z; v[3] = offset + a.w;
-    v[4] = offset + b.x; v[5] = offset + b.y; v[6] = offset + b.z; v[7] = offset + b.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < kUnit; ++i) v[i] = none;
+// A vector's values at a unit, read through the caches: every row needs them.
+struct RawVector {
+  u32x4 q[2];
+  __device__ __forceinline__ void load(const float* p, int H, int unit) {
+    const RowBuffer b(p, 0, 1, H * 4);
+    q[0] = __builtin_amdgcn_raw_buffer_load_b128(b.r, unit * 32, 0, 0);
+    q[1] = __builtin_amdgcn_raw_buffer_load_b128(b.r, unit * 32 + 16, 0, 0);
   }
+  // Plus `base`: a vector that is not there reads as 0.
+  __device__ __forceinline__ void widen(float base, float (&v)[kUnit]) const {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) v[i] = base + __uint_as_float(q[i / 4][i % 4]);
+  }
+};
+
+// One value of a tensor for the whole row, the same in every lane.
+__device__ __forceinline__ float load_token(const void* p, int64_t t, int64_t T) {
+  const RowBuffer b(p, t, T, 4);
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b.r, 0, 0, 0));
 }
 
 // The gate's factor and its slope.
@@ -140,347 +186,479 @@ __device__ __forceinline__ float open_gate(float g, int sigmoid, float& slope) {
   return g < 0.0f ? e * r : r;
 }
 
-// A row's values as the norm of `kind` leaves them, in place, and the factor that does
-// it.  Units that are not `on` hold 0 and stay so.
-template <int UPT, bool WAVE>
-__device__ __forceinline__ void norm_row(int kind, float (&v)[UPT][kUnit], const bool (&on)[UPT],
-                                         float inv_h, float eps, RowSum<WAVE>& sum) {
-  if (kind == MEP_NORM_NONE) return;
-  float t[1] = {0.0f};
-  if (kind == MEP_NORM_LAYER) {
-#pragma unroll
-    for (int u = 0; u < UPT; ++u)
-#pragma unroll
-      for (int i = 0; i < kUnit; ++i) t[0] += v[u][i];
-    sum(t);
-    const float mean = t[0] * inv_h;
-#pragma unroll
-    for (int u = 0; u < UPT; ++u)
-#pragma unroll
-      for (int i = 0; i < kUnit; ++i) v[u][i] = on[u] ? v[u][i] - mean : 0.0f;
-    t[0] = 0.0f;
-  }
-#pragma unroll
-  for (int u = 0; u < UPT; ++u)
-#pragma unroll
-    for (int i = 0; i < kUnit; ++i) t[0] = fmaf(v[u][i], v[u][i], t[0]);
-  sum(t);
-  const float r = 1.0f / sqrtf(fmaf(t[0], inv_h, eps));
-#pragma unroll
-  for (int u = 0; u < UPT; ++u)
-#pragma unroll
-    for (int i = 0; i < kUnit; ++i) v[u][i] *= r;
+// Within 2 half-steps of fp32, as the root's error and the quotient's together would be.
+__device__ __forceinline__ float inv_root(float mean_square, float eps) {
+  return rsqrtf(mean_square + eps);
 }
+
+// Which of a row's units a thread holds, and how rows go over blocks.
+template <int UPT, bool WAVE>
+struct Place {
+  int at[UPT];    // units, past the row's end for threads that hold none
+  int units, lane;  // of a row; among the row's lanes
+  int64_t first, step;
+
+  __device__ __forceinline__ explicit Place(int H) {
+    const int lanes = WAVE ? kWave : blockDim.x;
+    lane = WAVE ? lane_id() : threadIdx.x;
+    units = H / kUnit;
+#pragma unroll
+    for (int u = 0; u < UPT; ++u) at[u] = u * lanes + lane;
+    const int rows = WAVE ? blockDim.x / kWave : 1;
+    first = (int64_t)blockIdx.x * rows + (WAVE ? first_lane(threadIdx.x / kWave) : 0);
+    step = (int64_t)gridDim.x * rows;
+  }
+  __device__ __forceinline__ bool on(int u) const { return at[u] < units; }
+};
+
+// Threads of a block: four rows of a wave each, or one row.
+constexpr int most_threads(bool wave) { return wave ? 4 * kWave : kMaxWaves * kWave; }
 
 // ---- forward ----------------------------------------------------------------
 
 // E4M3 codes of a block of 128 columns, which 16 lanes hold: scale = amax / 448, codes of
-// the correctly rounded quotients.  The maximum is taken on the bits, where NaN is above
-// everything, so a block with a NaN or an infinity in it is NaN throughout.
+// the values times 1 / scale (one rounding; a quotient's five instructions a value were a
+// fifth of the kernel's).  A NaN is left out of the maximum and stays a NaN; an infinity
+// makes the scale infinite and its whole block NaN.
 __device__ __forceinline__ u32x2 encode_unit(const float (&v)[kUnit], float& scale) {
-  uint32_t m = 0;
+  float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kUnit; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-  auto step = [&](auto ctrl) {
-    m = max(m, (uint32_t)__builtin_amdgcn_update_dpp((int)m, (int)m, ctrl(), 0xf, 0xf, false));
-  };
-  step(std::integral_constant<int, 0xB1>{});
-  step(std::integral_constant<int, 0x4E>{});
-  step(std::integral_constant<int, 0x141>{});
-  step(std::integral_constant<int, 0x140>{});
-  scale = __uint_as_float(m) / 448.0f;
+  for (int i = 0; i < kUnit; ++i) m = fmaxf(m, fabsf(v[i]));
+  m = max16(m);
+  scale = m / 448.0f;
   float q[kUnit];
+  if (scale >= 0x1p-125f || scale == 0.0f) {
+    const float inv = scale == 0.0f ? 0.0f : 1.0f / scale;
 #pragma unroll
-  for (int i = 0; i < kUnit; ++i) q[i] = scale == 0.0f ? 0.0f : v[i] / scale;
+    for (int i = 0; i < kUnit; ++i) q[i] = v[i] * inv;
+  } else {  // 1 / scale may leave fp32
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) q[i] = v[i] / scale;
+  }
   return u32x2{pack_e4m3x4(q[0], q[1], q[2], q[3]), pack_e4m3x4(q[4], q[5], q[6], q[7])};
 }
 
-template <class TL, int UPT, bool WAVE>
-__global__ __launch_bounds__(kMaxWaves * kWave) void norm_kernel(NormArgs a) {
+// FULL: with biases, layer norms or a gate for every element, which take registers and
+// instructions of their own; 8 waves a SIMD without, so that two blocks of 7168 columns
+// fit a CU (4096 rows in bf16: 58 us, with one block 64 to 70).
+template <class TL, int UPT, bool WAVE, bool FULL>
+__global__ __launch_bounds__(most_threads(WAVE), !WAVE && !FULL && sizeof(TL) * UPT == 2 ? 8 : 1)
+void norm_kernel(NormArgs a) {
   __shared__ float4 lds[2][kMaxWaves];
-  const int lanes = WAVE ? kWave : blockDim.x, l = WAVE ? lane_id() : threadIdx.x;
-  const int rows_here = WAVE ? blockDim.x / kWave : 1;
-  const int units = a.H / kUnit;
+  const Place<UPT, WAVE> p(a.H);
   const float inv_h = 1.0f / (float)a.H;
   RowSum<WAVE> sum{lds, 0, (int)blockDim.x / kWave};
-  bool on[UPT];
-  int at[UPT];
-  float wp[UPT][kUnit], bp[UPT][kUnit], wn[UPT][kUnit], bn[UPT][kUnit];
+  const bool by_element = FULL && a.gate_kind == MEP_BLOCK_GATE_ELEMENT;
+  const bool by_token = a.gate_kind == MEP_BLOCK_GATE_TOKEN;
+  const bool post_layer = FULL && a.post == MEP_NORM_LAYER, pre_layer = FULL && a.pre == MEP_NORM_LAYER;
+  // A row as it lies in memory; the next one's loads run while this one is worked on.
+  struct Row {
+    Raw<TL> x[UPT], y[UPT], gate[FULL ? UPT : 1];
+    float g;
+  };
+  const int bytes = a.H * (int)sizeof(TL);
+  auto load = [&](int64_t t, Row& r) __attribute__((always_inline)) {
+    const RowBuffer x(a.x, t, a.T, bytes), y(a.y, t, a.T, bytes), gate(a.gate, t, a.T, bytes);
+    if (a.y) {
 #pragma unroll
-  for (int u = 0; u < UPT; ++u) {
-    on[u] = u * lanes + l < units;
-    at[u] = min(u * lanes + l, units - 1);
-    load_vector(a.post_weight, at[u], 1.0f, a.offset, wp[u]);
-    load_vector(a.post_bias, at[u], 0.0f, 0.0f, bp[u]);
-    load_vector(a.pre_weight, at[u], 1.0f, a.offset, wn[u]);
-    load_vector(a.pre_bias, at[u], 0.0f, 0.0f, bn[u]);
-  }
-  const int64_t step = (int64_t)gridDim.x * rows_here;
-  for (int64_t t = (int64_t)blockIdx.x * rows_here + (WAVE ? threadIdx.x / kWave : 0); t < a.T;
-       t += step) {
-    const int64_t row = t * units;
-    float v[UPT][kUnit];
-#pragma unroll
-    for (int u = 0; u < UPT; ++u)
-#pragma unroll
-      for (int i = 0; i < kUnit; ++i) v[u][i] = 0.0f;
-    Raw<TL> x[UPT];
+      for (int u = 0; u < UPT; ++u) r.y[u].load(y, p.at[u]);
+    }
     if (a.x) {
 #pragma unroll
-      for (int u = 0; u < UPT; ++u) x[u].load(a.x, row + at[u]);
+      for (int u = 0; u < UPT; ++u) r.x[u].load(x, p.at[u]);
     }
+    if constexpr (FULL)
+      if (by_element) {
+#pragma unroll
+        for (int u = 0; u < UPT; ++u) r.gate[u].load(gate, p.at[u]);
+      }
+    r.g = 0.0f;
+    if (by_token) r.g = reinterpret_cast<const float*>(a.gate)[t];
+  };
+  Row now;
+  int64_t t = p.first;
+  if (t >= a.T) return;
+  load(t, now);
+  float wp[UPT][kUnit], wn[UPT][kUnit];
+  float bp[FULL ? UPT : 1][kUnit], bn[FULL ? UPT : 1][kUnit];
+  {
+    RawVector post_w[UPT], pre_w[UPT], post_b[FULL ? UPT : 1], pre_b[FULL ? UPT : 1];
+#pragma unroll
+    for (int u = 0; u < UPT; ++u) {
+      post_w[u].load(a.post_weight, a.H, p.at[u]);
+      pre_w[u].load(a.pre_weight, a.H, p.at[u]);
+      if constexpr (FULL) {
+        post_b[u].load(a.post_bias, a.H, p.at[u]);
+        pre_b[u].load(a.pre_bias, a.H, p.at[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < UPT; ++u) {
+      post_w[u].widen(a.post_weight ? a.offset : 1.0f, wp[u]);
+      pre_w[u].widen(a.pre_weight ? a.offset : 1.0f, wn[u]);
+      if constexpr (FULL) {
+        post_b[u].widen(0.0f, bp[u]);
+        pre_b[u].widen(0.0f, bn[u]);
+      }
+    }
+  }
+  for (; t < a.T; t += p.step) {
+    Row next;
+    if (t + p.step < a.T) load(t + p.step, next);
+    float v[UPT][kUnit];
     if (a.y) {
-      Raw<TL> g[UPT];
+      float mean = 0.0f, r = 1.0f, slope;
+      if (post_layer) {
+        float q[1] = {0.0f};
 #pragma unroll
-      for (int u = 0; u < UPT; ++u) {
-        Raw<TL> y;
-        y.load(a.y, row + at[u]);
+        for (int u = 0; u < UPT; ++u)
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) v[u][i] = on[u] ? y.at(i) : 0.0f;
+          for (int i = 0; i < kUnit; ++i) q[0] += now.y[u].at(i);  // 0 past the row's end
+        sum(q);
+        mean = q[0] * inv_h;
       }
-      float g_row = 1.0f, slope;
-      if (a.gate_kind == MEP_BLOCK_GATE_TOKEN)
-        g_row = open_gate(reinterpret_cast<const float*>(a.gate)[t], a.sigmoid, slope);
-      if (a.gate_kind == MEP_BLOCK_GATE_ELEMENT) {
+      if (a.post != MEP_NORM_NONE) {
+        float q[1] = {0.0f};
 #pragma unroll
-        for (int u = 0; u < UPT; ++u) g[u].load(a.gate, row + at[u]);
+        for (int u = 0; u < UPT; ++u)
+          if (!FULL || p.on(u))
+#pragma unroll
+            for (int i = 0; i < kUnit; ++i) {
+              const float d = FULL ? now.y[u].at(i) - mean : now.y[u].at(i);
+              q[0] = fmaf(d, d, q[0]);
+            }
+        sum(q);
+        r = inv_root(q[0] * inv_h, a.eps);
       }
-      norm_row<UPT, WAVE>(a.post, v, on, inv_h, a.eps, sum);
+      float c = a.block_scale;
+      if (by_token) c *= open_gate(now.g, a.sigmoid, slope);
 #pragma unroll
       for (int u = 0; u < UPT; ++u)
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) {
-          float f = fmaf(v[u][i], wp[u][i], bp[u][i]) * g_row;
-          if (a.gate_kind == MEP_BLOCK_GATE_ELEMENT) f *= open_gate(g[u].at(i), a.sigmoid, slope);
-          v[u][i] = f * a.block_scale;
+          if constexpr (FULL) {
+            float f = fmaf((now.y[u].at(i) - mean) * r, wp[u][i], bp[u][i]);
+            if (by_element) f *= open_gate(now.gate[u].at(i), a.sigmoid, slope);
+            v[u][i] = f * c;
+          } else {
+            v[u][i] = now.y[u].at(i) * (r * c) * wp[u][i];
+          }
         }
+    } else {
+#pragma unroll
+      for (int u = 0; u < UPT; ++u)
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) v[u][i] = 0.0f;
     }
+    if (a.x) {
 #pragma unroll
-    for (int u = 0; u < UPT; ++u) {
+      for (int u = 0; u < UPT; ++u)
 #pragma unroll
-      for (int i = 0; i < kUnit; ++i) {
-        if (a.x) v[u][i] = fmaf(a.residual_scale, x[u].at(i), v[u][i]);
-        if (!on[u]) v[u][i] = 0.0f;
+        for (int i = 0; i < kUnit; ++i) v[u][i] = fmaf(a.residual_scale, now.x[u].at(i), v[u][i]);
+    }
+    if (a.s) {
+      const RowBuffer s(a.s, t, a.T, bytes);
+#pragma unroll
+      for (int u = 0; u < UPT; ++u) store_unit((TL*)nullptr, s, p.at[u], v[u]);
+    }
+    if (a.n || a.codes) {
+      float mean = 0.0f, r = 1.0f;
+      if (pre_layer) {
+        float q[1] = {0.0f};
+#pragma unroll
+        for (int u = 0; u < UPT; ++u)
+          if (p.on(u))
+#pragma unroll
+            for (int i = 0; i < kUnit; ++i) q[0] += v[u][i];
+        sum(q);
+        mean = q[0] * inv_h;
       }
-      if (a.s && on[u]) store_unit((TL*)nullptr, a.s, row + at[u], v[u]);
-    }
-    if (!a.n && !a.codes) continue;
-    norm_row<UPT, WAVE>(a.pre, v, on, inv_h, a.eps, sum);
+      if (a.pre != MEP_NORM_NONE) {
+        float q[1] = {0.0f};
 #pragma unroll
-    for (int u = 0; u < UPT; ++u) {
+        for (int u = 0; u < UPT; ++u)
+          if (!FULL || p.on(u))
 #pragma unroll
-      for (int i = 0; i < kUnit; ++i) v[u][i] = fmaf(v[u][i], wn[u][i], bn[u][i]);
-      if (a.n && on[u]) store_unit((TL*)nullptr, a.n, row + at[u], v[u]);
+            for (int i = 0; i < kUnit; ++i) {
+              const float d = FULL ? v[u][i] - mean : v[u][i];
+              q[0] = fmaf(d, d, q[0]);
+            }
+        sum(q);
+        r = inv_root(q[0] * inv_h, a.eps);
+      }
+#pragma unroll
+      for (int u = 0; u < UPT; ++u)
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) {
+          if constexpr (FULL) v[u][i] = fmaf((v[u][i] - mean) * r, wn[u][i], bn[u][i]);
+          else v[u][i] = v[u][i] * r * wn[u][i];
+        }
+      if (a.n) {
+        const RowBuffer n(a.n, t, a.T, bytes);
+#pragma unroll
+        for (int u = 0; u < UPT; ++u) store_unit((TL*)nullptr, n, p.at[u], v[u]);
+      }
       if (a.codes) {
-        float scale;
-        const u32x2 c = encode_unit(v[u], scale);
-        if (on[u]) {
-          reinterpret_cast<u32x2*>(a.codes)[row + at[u]] = c;
-          if (at[u] % (kCodeBlock / kUnit) == 0) a.scales[(row + at[u]) / (kCodeBlock / kUnit)] = scale;
+        const RowBuffer codes(a.codes, t, a.T, a.H), scales(a.scales, t, a.T, a.H / kCodeBlock * 4);
+#pragma unroll
+        for (int u = 0; u < UPT; ++u) {
+          float scale;
+          const u32x2 c = encode_unit(v[u], scale);
+          __builtin_amdgcn_raw_buffer_store_b64(c, codes.r, p.at[u] * kUnit, 0, kPast);
+          // one lane of 16 has a block's scale; the others' offsets lie past the row
+          const int block = p.at[u] % kShare == 0 ? p.at[u] / kShare : p.units;
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(scale), scales.r, block * 4, 0, 0);
         }
       }
     }
+    now = next;
   }
 }
 
 // ---- gradients --------------------------------------------------------------
 
-// Adds to `grad` what a norm hands back of `g`, the gradient of its result times the
-// weight, and leaves the normed row in v.  With h = hat(u) and r the factor,
+// With h = hat(u), r its factor and g the gradient of the normed row times the weight,
 //   d/du = r (g - mean(g) [layer norms] - h mean(g h)).
-template <int UPT, bool WAVE>
-__device__ __forceinline__ void norm_row_backward(int kind, float (&v)[UPT][kUnit],
-                                                  const float (&g)[UPT][kUnit],
-                                                  const bool (&on)[UPT], float inv_h, float eps,
-                                                  RowSum<WAVE>& sum, float (&grad)[UPT][kUnit]) {
-  if (kind == MEP_NORM_NONE) {
-#pragma unroll
-    for (int u = 0; u < UPT; ++u)
-#pragma unroll
-      for (int i = 0; i < kUnit; ++i) grad[u][i] += g[u][i];
-    return;
-  }
-  float mean_g = 0.0f;
-  if (kind == MEP_NORM_LAYER) {
-    float t[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int u = 0; u < UPT; ++u)
-#pragma unroll
-      for (int i = 0; i < kUnit; ++i) {
-        t[0] += v[u][i];
-        t[1] += g[u][i];
-      }
-    sum(t);
-    const float mean = t[0] * inv_h;
-    mean_g = t[1] * inv_h;
-#pragma unroll
-    for (int u = 0; u < UPT; ++u)
-#pragma unroll
-      for (int i = 0; i < kUnit; ++i) v[u][i] = on[u] ? v[u][i] - mean : 0.0f;
-  }
-  float t[2] = {0.0f, 0.0f};
-#pragma unroll
-  for (int u = 0; u < UPT; ++u)
-#pragma unroll
-    for (int i = 0; i < kUnit; ++i) {
-      t[0] = fmaf(v[u][i], v[u][i], t[0]);
-      t[1] = fmaf(v[u][i], g[u][i], t[1]);
-    }
-  sum(t);
-  const float r = 1.0f / sqrtf(fmaf(t[0], inv_h, eps));
-  const float along = t[1] * inv_h * r;
-#pragma unroll
-  for (int u = 0; u < UPT; ++u)
-#pragma unroll
-    for (int i = 0; i < kUnit; ++i) {
-      v[u][i] *= r;
-      grad[u][i] = fmaf(r, g[u][i] - mean_g - v[u][i] * along, grad[u][i]);
-    }
-}
-
-// Each block adds up its rows' share of the column sums in registers and leaves them in
+// A row stays as it lies in memory (raw) while its sums are taken, each value widened
+// where it is needed: sums of both norms that do not wait for each other share a round.
+//   Each block adds up its rows' share of the column sums in registers and leaves them in
 // a row of `part`; norm_columns_kernel adds those up, in order, so that a result does
-// not depend on timing.  BIAS: the biases' sums are wanted too.
-template <class TL, int UPT, bool WAVE, bool BIAS>
-__global__ __launch_bounds__(kMaxWaves * kWave) void norm_backward_kernel(NormBackwardArgs a) {
+// not depend on timing.
+template <class TL, int UPT, bool WAVE, bool FULL>
+__global__ __launch_bounds__(most_threads(WAVE)) void norm_backward_kernel(NormBackwardArgs a) {
   __shared__ float4 lds[2][kMaxWaves];
-  const int lanes = WAVE ? kWave : blockDim.x, l = WAVE ? lane_id() : threadIdx.x;
-  const int rows_here = WAVE ? blockDim.x / kWave : 1;
-  const int units = a.H / kUnit;
+  constexpr int COLS = FULL ? 4 : 2;  // post weight, pre weight, their biases
+  constexpr int AHEAD = sizeof(TL) == 2 && UPT == 1 ? 2 : 1;  // rows whose loads have registers
+  const Place<UPT, WAVE> p(a.H);
   const float inv_h = 1.0f / (float)a.H;
   RowSum<WAVE> sum{lds, 0, (int)blockDim.x / kWave};
-  bool on[UPT];
-  int at[UPT];
-  float wp[UPT][kUnit], bp[UPT][kUnit], wn[UPT][kUnit];
-  float acc[BIAS ? 4 : 2][UPT][kUnit];  // post weight, pre weight, their biases
+  float acc[COLS][UPT][kUnit];
 #pragma unroll
-  for (int u = 0; u < UPT; ++u) {
-    on[u] = u * lanes + l < units;
-    at[u] = min(u * lanes + l, units - 1);
-    load_vector(a.post_weight, at[u], 1.0f, a.offset, wp[u]);
-    load_vector(a.post_bias, at[u], 0.0f, 0.0f, bp[u]);
-    load_vector(a.pre_weight, at[u], 1.0f, a.offset, wn[u]);
-#pragma unroll
-    for (int c = 0; c < (BIAS ? 4 : 2); ++c)
-#pragma unroll
-      for (int i = 0; i < kUnit; ++i) acc[c][u][i] = 0.0f;
-  }
-  const int64_t first = (int64_t)blockIdx.x * rows_here + (WAVE ? threadIdx.x / kWave : 0);
-  const int64_t step = (int64_t)gridDim.x * rows_here;
-  for (int64_t t = first; t < a.T; t += step) {
-    const int64_t row = t * units;
-    float grad[UPT][kUnit];  // of the stream
-    float v[UPT][kUnit], g[UPT][kUnit];
+  for (int c = 0; c < COLS; ++c)
 #pragma unroll
     for (int u = 0; u < UPT; ++u)
 #pragma unroll
-      for (int i = 0; i < kUnit; ++i) grad[u][i] = 0.0f;
-    if (a.grad_s) {
+      for (int i = 0; i < kUnit; ++i) acc[c][u][i] = 0.0f;
+  const bool by_element = FULL && a.gate_kind == MEP_BLOCK_GATE_ELEMENT;
+  const bool by_token = a.gate_kind == MEP_BLOCK_GATE_TOKEN;
+  const int pre = a.grad_n ? a.pre : MEP_NORM_NONE, post = a.y ? a.post : MEP_NORM_NONE;
+  struct Row {
+    Raw<TL> gs[UPT], gn[UPT], s[UPT], y[UPT], gate[FULL ? UPT : 1];
+    float g;
+  };
+  const int bytes = a.H * (int)sizeof(TL);
+  auto load_stream = [&](int64_t t, Row& r) __attribute__((always_inline)) {
+    const RowBuffer s(a.grad_n ? a.s : nullptr, t, a.T, bytes), gn(a.grad_n, t, a.T, bytes);
+    const RowBuffer gs(a.grad_s, t, a.T, bytes);
 #pragma unroll
-      for (int u = 0; u < UPT; ++u) {
-        Raw<TL> q;
-        q.load(a.grad_s, row + at[u]);
-#pragma unroll
-        for (int i = 0; i < kUnit; ++i) grad[u][i] = on[u] ? q.at(i) : 0.0f;
-      }
+    for (int u = 0; u < UPT; ++u) {
+      r.s[u].load(s, p.at[u]);
+      r.gn[u].load(gn, p.at[u]);
+      r.gs[u].load(gs, p.at[u]);
     }
-    if (a.grad_n) {
-      Raw<TL> gn[UPT];
+  };
+  auto load_block = [&](int64_t t, Row& r) __attribute__((always_inline)) {
+    const RowBuffer y(a.y, t, a.T, bytes), gate(by_element ? a.gate : nullptr, t, a.T, bytes);
 #pragma unroll
-      for (int u = 0; u < UPT; ++u) {
-        Raw<TL> q;
-        q.load(a.s, row + at[u]);
-        gn[u].load(a.grad_n, row + at[u]);
+    for (int u = 0; u < UPT; ++u) {
+      r.y[u].load(y, p.at[u]);
+      if constexpr (FULL) r.gate[u].load(gate, p.at[u]);
+    }
+    r.g = load_token(by_token ? a.gate : nullptr, t, a.T);
+  };
+  Row rows[AHEAD];
+  int64_t t = p.first;
+  load_stream(t, rows[0]);
+  load_block(t, rows[0]);
+  float wp[UPT][kUnit], wn[UPT][kUnit], bp[FULL ? UPT : 1][kUnit];
+  {
+    RawVector post_w[UPT], pre_w[UPT], post_b[FULL ? UPT : 1];
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) {
-          v[u][i] = on[u] ? q.at(i) : 0.0f;
-          g[u][i] = on[u] ? gn[u].at(i) * wn[u][i] : 0.0f;
-        }
-      }
-      norm_row_backward<UPT, WAVE>(a.pre, v, g, on, inv_h, a.eps, sum, grad);
+    for (int u = 0; u < UPT; ++u) {
+      pre_w[u].load(a.pre_weight, a.H, p.at[u]);
+      post_w[u].load(a.post_weight, a.H, p.at[u]);
+      if constexpr (FULL) post_b[u].load(a.post_bias, a.H, p.at[u]);
+    }
+    if constexpr (AHEAD == 2) {
+      load_stream(t + p.step, rows[1]);
+      load_block(t + p.step, rows[1]);
+    }
+#pragma unroll
+    for (int u = 0; u < UPT; ++u) {
+      pre_w[u].widen(a.pre_weight ? a.offset : 1.0f, wn[u]);
+      post_w[u].widen(a.post_weight ? a.offset : 1.0f, wp[u]);
+      if constexpr (FULL) post_b[u].widen(0.0f, bp[u]);
+    }
+  }
+  auto hold = [&](Row& r) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < UPT; ++u) {
+      r.s[u].hold();
+      r.gn[u].hold();
+      r.y[u].hold();
+    }
+  };
+  // one row; its place takes the loads of the row AHEAD steps on as parts of it are done
+  auto work = [&](int64_t t, Row& now) __attribute__((always_inline)) {
+    const int64_t then = t + AHEAD * p.step;
+    // the means of both norms' rows, and of the next norm's gradient
+    float mean_s = 0.0f, r_s = 1.0f, mean_n = 0.0f, along_n = 0.0f, mean_y = 0.0f, r_y = 1.0f;
+    if (FULL && (pre == MEP_NORM_LAYER || post == MEP_NORM_LAYER)) {
+      float q[3] = {0.0f, 0.0f, 0.0f};  // what lies past the row's end is 0
 #pragma unroll
       for (int u = 0; u < UPT; ++u)
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) {
-          acc[1][u][i] = fmaf(gn[u].at(i), v[u][i], acc[1][u][i]);
-          if constexpr (BIAS) acc[3][u][i] += gn[u].at(i);
+          q[0] += now.s[u].at(i);
+          q[1] = fmaf(now.gn[u].at(i), wn[u][i], q[1]);
+          q[2] += now.y[u].at(i);
         }
-    }
-    if (a.grad_x) {
-#pragma unroll
-      for (int u = 0; u < UPT; ++u) {
-        float f[kUnit];
-#pragma unroll
-        for (int i = 0; i < kUnit; ++i) f[i] = a.residual_scale * grad[u][i];
-        if (on[u]) store_unit((TL*)nullptr, a.grad_x, row + at[u], f);
+      sum(q);
+      if (pre == MEP_NORM_LAYER) {
+        mean_s = q[0] * inv_h;
+        mean_n = q[1] * inv_h;
       }
+      if (post == MEP_NORM_LAYER) mean_y = q[2] * inv_h;
+      hold(now);
     }
-    if (!a.y) continue;
-    // the block's part: gv, the gradient of v, takes the stream's place step by step
-    Raw<TL> gate[UPT];
-    float g_row = 1.0f, slope_row = 1.0f;
-    if (a.gate_kind == MEP_BLOCK_GATE_TOKEN)
-      g_row = open_gate(reinterpret_cast<const float*>(a.gate)[t], a.sigmoid, slope_row);
-    if (a.gate_kind == MEP_BLOCK_GATE_ELEMENT) {
+    // their factors, and what of the gradient lies along the row
+    if (pre != MEP_NORM_NONE || post != MEP_NORM_NONE) {
+      float q[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int u = 0; u < UPT; ++u) gate[u].load(a.gate, row + at[u]);
+      for (int u = 0; u < UPT; ++u)
+        if (!FULL || p.on(u))
+#pragma unroll
+          for (int i = 0; i < kUnit; ++i) {
+            const float s = FULL ? now.s[u].at(i) - mean_s : now.s[u].at(i);
+            const float y = FULL ? now.y[u].at(i) - mean_y : now.y[u].at(i);
+            q[0] = fmaf(s, s, q[0]);
+            q[1] = fmaf(s, now.gn[u].at(i) * wn[u][i], q[1]);
+            q[2] = fmaf(y, y, q[2]);
+          }
+      sum(q);
+      if (pre != MEP_NORM_NONE) {
+        r_s = inv_root(q[0] * inv_h, a.eps);
+        along_n = q[1] * inv_h * r_s;
+      }
+      if (post != MEP_NORM_NONE) r_y = inv_root(q[2] * inv_h, a.eps);
+      hold(now);
     }
-    const float c_row = a.block_scale * g_row;
-    float gv[UPT][kUnit], back[UPT][kUnit];
+    // the stream's gradient
+    float grad[UPT][kUnit];
 #pragma unroll
     for (int u = 0; u < UPT; ++u) {
-      Raw<TL> q;
-      q.load(a.y, row + at[u]);
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) {
-        float slope, f = c_row;
-        if (a.gate_kind == MEP_BLOCK_GATE_ELEMENT) f *= open_gate(gate[u].at(i), a.sigmoid, slope);
-        v[u][i] = on[u] ? q.at(i) : 0.0f;
-        gv[u][i] = f * grad[u][i];
-        g[u][i] = on[u] ? gv[u][i] * wp[u][i] : 0.0f;
-        back[u][i] = 0.0f;
+        float g = now.gs[u].at(i);  // 0 without grad_s; without grad_n, s and gn are 0
+        const float gn = now.gn[u].at(i);
+        const float h = FULL ? (now.s[u].at(i) - mean_s) * r_s : now.s[u].at(i) * r_s;
+        const float off = FULL ? fmaf(h, along_n, mean_n) : h * along_n;
+        g = fmaf(r_s, fmaf(gn, wn[u][i], -off), g);
+        acc[1][u][i] = fmaf(gn, h, acc[1][u][i]);
+        if constexpr (FULL) acc[3][u][i] += gn;
+        grad[u][i] = g;
       }
     }
-    norm_row_backward<UPT, WAVE>(a.post, v, g, on, inv_h, a.eps, sum, back);
-    float of_gate[1] = {0.0f};
+    load_stream(then, now);
+    const RowBuffer grad_x(a.grad_x, t, a.T, bytes);
 #pragma unroll
     for (int u = 0; u < UPT; ++u) {
       float f[kUnit];
 #pragma unroll
-      for (int i = 0; i < kUnit; ++i) {
-        acc[0][u][i] = fmaf(gv[u][i], v[u][i], acc[0][u][i]);
-        if constexpr (BIAS) acc[2][u][i] += gv[u][i];
-        // the gradient of the gate's factor
-        f[i] = a.block_scale * grad[u][i] * fmaf(v[u][i], wp[u][i], bp[u][i]);
-        of_gate[0] += on[u] ? f[i] : 0.0f;
-      }
-      if (a.grad_y && on[u]) store_unit((TL*)nullptr, a.grad_y, row + at[u], back[u]);
-      if (a.grad_gate && a.gate_kind == MEP_BLOCK_GATE_ELEMENT) {
-#pragma unroll
-        for (int i = 0; i < kUnit; ++i) {
-          float slope;
-          open_gate(gate[u].at(i), a.sigmoid, slope);
-          f[i] *= slope;
-        }
-        if (on[u]) store_unit((TL*)nullptr, a.grad_gate, row + at[u], f);
-      }
+      for (int i = 0; i < kUnit; ++i) f[i] = a.residual_scale * grad[u][i];
+      store_unit((TL*)nullptr, grad_x, p.at[u], f);
     }
-    if (a.grad_gate && a.gate_kind == MEP_BLOCK_GATE_TOKEN) {
-      sum(of_gate);
-      if (l == 0) reinterpret_cast<float*>(a.grad_gate)[t] = of_gate[0] * slope_row;
+    // the block's part (without a block y is 0, and nothing of this is stored)
+    float slope_row = 1.0f, c = a.block_scale;
+    if (by_token) c *= open_gate(now.g, a.sigmoid, slope_row);
+    // the gate's factor without c
+    auto factor = [&](int u, int i, float& slope) __attribute__((always_inline)) {
+      slope = 1.0f;
+      return by_element ? open_gate(now.gate[FULL ? u : 0].at(i), a.sigmoid, slope) : 1.0f;
+    };
+    const bool token_grad = by_token && a.grad_gate;
+    float mean_v = 0.0f, along_y = 0.0f, of_row = 0.0f;
+    if (post != MEP_NORM_NONE || token_grad) {
+      float q[FULL ? 3 : 1] = {0.0f};
+#pragma unroll
+      for (int u = 0; u < UPT; ++u)
+        if (!FULL || p.on(u))
+#pragma unroll
+          for (int i = 0; i < kUnit; ++i) {
+            if constexpr (FULL) {
+              float slope;
+              const float h = (now.y[u].at(i) - mean_y) * r_y;
+              const float g = factor(u, i, slope) * grad[u][i] * wp[u][i];
+              q[0] = fmaf(g, h, q[0]);
+              q[1] += g;
+              q[2] = fmaf(grad[u][i], bp[u][i], q[2]);
+            } else {
+              q[0] = fmaf(grad[u][i] * wp[u][i], now.y[u].at(i), q[0]);
+            }
+          }
+      sum(q);
+      if constexpr (!FULL) q[0] *= r_y;
+      if (post != MEP_NORM_NONE) along_y = c * q[0] * inv_h;
+      if constexpr (FULL) {
+        if (post == MEP_NORM_LAYER) mean_v = c * q[1] * inv_h;
+        q[0] += q[2];
+      }
+      of_row = a.block_scale * q[0] * slope_row;  // a gate a row: sum of grad v
+#pragma unroll
+      for (int u = 0; u < UPT; ++u) now.y[u].hold();
+    }
+    const RowBuffer grad_y(a.grad_y, t, a.T, bytes);
+    const RowBuffer grad_gate(by_element ? a.grad_gate : nullptr, t, a.T, bytes);
+#pragma unroll
+    for (int u = 0; u < UPT; ++u) {
+      float back[kUnit], of_gate[kUnit];
+#pragma unroll
+      for (int i = 0; i < kUnit; ++i) {
+        if constexpr (FULL) {
+          float slope;
+          const float h = (now.y[u].at(i) - mean_y) * r_y;
+          const float gv = c * factor(u, i, slope) * grad[u][i];
+          acc[0][u][i] = fmaf(gv, h, acc[0][u][i]);
+          acc[2][u][i] += gv;
+          back[i] = r_y * fmaf(gv, wp[u][i], -fmaf(h, along_y, mean_v));
+          of_gate[i] = a.block_scale * slope * grad[u][i] * fmaf(h, wp[u][i], bp[u][i]);
+        } else {
+          const float h = now.y[u].at(i) * r_y, gv = c * grad[u][i];
+          acc[0][u][i] = fmaf(gv, h, acc[0][u][i]);
+          back[i] = r_y * fmaf(gv, wp[u][i], -(h * along_y));
+        }
+      }
+      store_unit((TL*)nullptr, grad_y, p.at[u], back);
+      if constexpr (FULL) store_unit((TL*)nullptr, grad_gate, p.at[u], of_gate);
+    }
+    const RowBuffer row_gate(token_grad ? a.grad_gate : nullptr, t, a.T, 4);
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(of_row), row_gate.r, p.lane * 4, 0, 0);
+    load_block(then, now);
+  };
+  if (t < a.T) {
+    while (true) {
+      work(t, rows[0]);
+      if ((t += p.step) >= a.T) break;
+      if constexpr (AHEAD == 2) {
+        work(t, rows[1]);
+        if ((t += p.step) >= a.T) break;
+      }
     }
   }
   // this block's (or wave's) partial sums: wanted columns one after the other
-  float* part = a.part + first * a.H;
-  const int64_t next = (int64_t)step * a.H;
+  float* part = a.part + p.first * a.H;
   constexpr int kOf[4] = {0, 2, 1, 3};  // columns[] in the order of acc
 #pragma unroll
-  for (int c = 0; c < (BIAS ? 4 : 2); ++c) {
+  for (int c = 0; c < COLS; ++c) {
     if (!a.columns[kOf[c]]) continue;
 #pragma unroll
     for (int u = 0; u < UPT; ++u)
-      if (on[u]) store_unit((float*)nullptr, part, at[u], acc[c][u]);
-    part += next;
+      if (p.on(u)) {  // read again at once: through the caches
+        float4* to = reinterpret_cast<float4*>(part) + 2 * p.at[u];
+        to[0] = make_float4(acc[c][u][0], acc[c][u][1], acc[c][u][2], acc[c][u][3]);
+        to[1] = make_float4(acc[c][u][4], acc[c][u][5], acc[c][u][6], acc[c][u][7]);
+      }
+    part += p.step * a.H;
   }
 }
 
@@ -539,6 +717,16 @@ void by_shape(const RowShape& r, F f) {
   }
 }
 
+// Calls f(a value of the rows' type, full).
+template <class F>
+void by_type(int dtype, bool full, F f) {
+  if (dtype == MEP_BF16) {
+    if (full) f(uint16_t{}, std::true_type{}); else f(uint16_t{}, std::false_type{});
+  } else {
+    if (full) f(float{}, std::true_type{}); else f(float{}, std::false_type{});
+  }
+}
+
 int blocks_for(const RowShape& r, int32_t T, int most) {
   return (int)std::min<int64_t>(((int64_t)T + r.rows - 1) / r.rows, most);
 }
@@ -548,12 +736,14 @@ int blocks_for(const RowShape& r, int32_t T, int most) {
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
   const RowShape r = row_shape(a.H);
-  const int blocks = blocks_for(r, a.T, 1024);
+  const int blocks = blocks_for(r, a.T, 512);
   by_shape(r, [&](auto upt, auto wave) {
-    if (a.dtype == MEP_BF16)
-      norm_kernel<uint16_t, upt(), wave()><<<blocks, r.threads, 0, s>>>(a);
-    else
-      norm_kernel<float, upt(), wave()><<<blocks, r.threads, 0, s>>>(a);
+    auto launch = [&](auto type, auto full) {
+      norm_kernel<decltype(type), upt(), wave(), full()><<<blocks, r.threads, 0, s>>>(a);
+    };
+    const bool full = a.post_bias || a.pre_bias || a.gate_kind == MEP_BLOCK_GATE_ELEMENT ||
+                      a.post == MEP_NORM_LAYER || a.pre == MEP_NORM_LAYER;
+    by_type(a.dtype, full, launch);
   });
   return hipGetLastError();
 }
@@ -568,15 +758,13 @@ hipError_t launch_block_norm_backward(const NormBackwardArgs& a, hipStream_t s) 
   const int blocks = blocks_for(r, a.T, 256);
   if (blocks > 0) {
     by_shape(r, [&](auto upt, auto wave) {
-      auto launch = [&](auto type, auto bias) {
-        norm_backward_kernel<decltype(type), upt(), wave(), bias()><<<blocks, r.threads, 0, s>>>(a);
+      auto launch = [&](auto type, auto full) {
+        norm_backward_kernel<decltype(type), upt(), wave(), full()><<<blocks, r.threads, 0, s>>>(a);
       };
-      const bool bias = a.columns[1] || a.columns[3];
-      if (a.dtype == MEP_BF16) {
-        if (bias) launch(uint16_t{}, std::true_type{}); else launch(uint16_t{}, std::false_type{});
-      } else {
-        if (bias) launch(float{}, std::true_type{}); else launch(float{}, std::false_type{});
-      }
+      const bool full = a.columns[1] || a.columns[3] || a.post_bias ||
+                        a.gate_kind == MEP_BLOCK_GATE_ELEMENT || a.post == MEP_NORM_LAYER ||
+                        a.pre == MEP_NORM_LAYER;
+      by_type(a.dtype, full, launch);
     });
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }

@@ -550,9 +550,10 @@ typedef struct mep_norm_config {
  * in fp32, s and n rounded once each to the rows' type (n is of s before its rounding).
  * s is the new stream; n the next block's input, for its router and, as E4M3 codes with
  * a scale per 128 columns, for a dispatch with MEP_QUANT_FP8_CARRY:
- *   n_scales[t, b] = amax_b / 448 (fp32 [T,H/128]),  n_codes = E4M3_rne(n / scale)
- * of n before its rounding (zeros where amax_b is 0; a block with an infinity or a NaN in
- * it is NaN throughout).  s, n and n_codes are NULL where not wanted, not all
+ *   n_scales[t, b] = amax_b / 448 (fp32 [T,H/128]),  n_codes = E4M3_rne(n * (1 / scale))
+ * of n before its rounding, the reciprocal and the product rounded to fp32 (zeros where
+ * amax_b is 0; a NaN counts for no maximum and stays one; a block with an infinity in it is
+ * NaN throughout).  s, n and n_codes are NULL where not wanted, not all
  * three.  x NULL: no residual; y NULL: no block part (gate then NULL too), so that the
  * call norms or only encodes rows; not both NULL.  Weights and biases are fp32 [H]; a
  * NULL weight stands for the factor 1, a NULL bias for 0.  A row's mean square must fit

@@ -138,7 +138,7 @@ def test_codes(T, H, dtype):
     k = check_forward(Case(T, H, dtype, "rms", "rms", "token", 1, seed=H), codes=True)
     if dtype == "fp32":  # the codes of exactly the rows that n holds
         n, scale = k.n[:T].cpu(), k.scales[:T].cpu()
-        want = (n.reshape(T, -1, 128) / scale[:, :, None]).reshape(T, H).to(torch.float8_e4m3fn)
+        want = (n.reshape(T, -1, 128) * (1 / scale[:, :, None])).reshape(T, H).to(torch.float8_e4m3fn)
         assert torch.equal(want.view(torch.uint8), k.codes[:T].cpu().view(torch.uint8))
     check_forward(Case(T, H, dtype, "none", "rms", y=False, seed=H), s=False, n=False, codes=True)
     # without a norm the call only encodes rows
@@ -154,14 +154,18 @@ def test_codes_of_zero_tiny_and_non_finite_blocks():
     x[2, 300] = float("inf")
     x[3, 7] = float("nan")
     x[4] *= 1e37
+    x[5, 128:256] = float("nan")
     k.x = x.cuda()
     k.forward(True, True, True)
     codes, scale = k.codes[:6].cpu(), k.scales[:6].cpu()
     assert bool((codes[0, :128].float() == 0).all()) and float(scale[0, 0]) == 0
     value = codes.float().reshape(6, 3, 128) * scale[:, :, None]
     spoilt = torch.zeros((6, 3), dtype=torch.bool)
-    spoilt[2, 2] = spoilt[3, 0] = True
-    assert bool(torch.isnan(value[spoilt]).all()) and bool(torch.isfinite(value[~spoilt]).all())
+    spoilt[2, 2] = True               # an infinity spoils its block, a NaN only itself
+    assert bool(torch.isnan(value[spoilt]).all())
+    assert bool(torch.isnan(value[3, 0, 7])) and bool(torch.isnan(value[5, 1]).all())
+    value[3, 0, 7], value[5, 1], x[3, 7], x[5, 128:256] = 0, 0, 0, 0
+    assert bool(torch.isfinite(value[~spoilt]).all())
     off = (value - x.reshape(6, 3, 128)).abs()
     lim = torch.maximum(x.reshape(6, 3, 128).abs() / 16, scale[:, :, None] / 1024) * 1.001
     lim[1, 1] = scale[1, 1] * 32   # the scale itself has few bits there: its half-step times 448

@@ -211,8 +211,10 @@ struct Place {
   __device__ __forceinline__ bool on(int u) const { return at[u] < units; }
 };
 
-// Threads of a block: four rows of a wave each, or one row.
-constexpr int most_threads(bool wave) { return wave ? 4 * kWave : kMaxWaves * kWave; }
+// Threads that kernels are built for: four rows of a wave each, or one row of up to 512
+// or 1024 threads (which leave a thread 256 or 128 registers).
+constexpr int kWaveRows = 0, kHalfBlock = 512, kBlock = 1024;
+constexpr int most_threads(int rows) { return rows == kWaveRows ? 4 * kWave : rows; }
 
 // ---- forward ----------------------------------------------------------------
 
@@ -241,9 +243,10 @@ __device__ __forceinline__ u32x2 encode_unit(const float (&v)[kUnit], float& sca
 // FULL: with biases, layer norms or a gate for every element, which take registers and
 // instructions of their own; 8 waves a SIMD without, so that two blocks of 7168 columns
 // fit a CU (4096 rows in bf16: 58 us, with one block 64 to 70).
-template <class TL, int UPT, bool WAVE, bool FULL>
-__global__ __launch_bounds__(most_threads(WAVE), !WAVE && !FULL && sizeof(TL) * UPT == 2 ? 8 : 1)
+template <class TL, int UPT, int ROWS, bool FULL>
+__global__ __launch_bounds__(most_threads(ROWS), ROWS == kBlock && !FULL && sizeof(TL) * UPT == 2 ? 8 : 1)
 void norm_kernel(NormArgs a) {
+  constexpr bool WAVE = ROWS == kWaveRows;
   __shared__ float4 lds[2][kMaxWaves];
   const Place<UPT, WAVE> p(a.H);
   const float inv_h = 1.0f / (float)a.H;
@@ -421,14 +424,37 @@ void norm_kernel(NormArgs a) {
 //   d/du = r (g - mean(g) [layer norms] - h mean(g h)).
 // A row stays as it lies in memory (raw) while its sums are taken, each value widened
 // where it is needed: sums of both norms that do not wait for each other share a round.
+// The weights have registers, or lie in LDS where those would not do: 1024 threads leave
+// 128 a thread, and what spills costs as much as the rows (4096 x 7168 with layer norms,
+// biases and a gate for every element 122 us, with all in registers 248; 4096 x 16384
+// without any of these 190 and 345).
 //   Each block adds up its rows' share of the column sums in registers and leaves them in
 // a row of `part`; norm_columns_kernel adds those up, in order, so that a result does
 // not depend on timing.
-template <class TL, int UPT, bool WAVE, bool FULL>
-__global__ __launch_bounds__(most_threads(WAVE)) void norm_backward_kernel(NormBackwardArgs a) {
+constexpr bool weights_in_lds(int rows, int upt, bool full, bool bf16) {
+  return rows == kBlock ? full || upt > 1 : rows == kHalfBlock && full && bf16;
+}
+// Half blocks kept to 128 registers, so that 4 waves a SIMD fit whatever the block's
+// waves: all but those of fp32 rows with all of it, which would spill (4096 x 2056 90 us,
+// in 128 registers 101).
+constexpr bool packed_halves(int rows, bool full, bool bf16) {
+  return rows == kHalfBlock && (!full || bf16);
+}
+constexpr int kLdsRow = 8192;  // values of a row of which three vectors fit LDS, else two
+__host__ __device__ constexpr int vectors_in_lds(bool full, int H) {
+  return full && H <= kLdsRow ? 3 : 2;
+}
+
+template <class TL, int UPT, int ROWS, bool FULL>
+__global__ __launch_bounds__(most_threads(ROWS), packed_halves(ROWS, FULL, sizeof(TL) == 2) ? 4 : 1)
+void norm_backward_kernel(NormBackwardArgs a) {
+  constexpr bool WAVE = ROWS == kWaveRows;
   __shared__ float4 lds[2][kMaxWaves];
   constexpr int COLS = FULL ? 4 : 2;  // post weight, pre weight, their biases
-  constexpr int AHEAD = sizeof(TL) == 2 && UPT == 1 ? 2 : 1;  // rows whose loads have registers
+  // Rows whose loads have registers, and whether the weights have (else they lie in LDS,
+  // as far as that holds them).
+  constexpr bool IN_LDS = weights_in_lds(ROWS, UPT, FULL, sizeof(TL) == 2);
+  constexpr int AHEAD = sizeof(TL) == 2 && !IN_LDS ? 2 : 1;
   const Place<UPT, WAVE> p(a.H);
   const float inv_h = 1.0f / (float)a.H;
   RowSum<WAVE> sum{lds, 0, (int)blockDim.x / kWave};
@@ -470,14 +496,30 @@ __global__ __launch_bounds__(most_threads(WAVE)) void norm_backward_kernel(NormB
   int64_t t = p.first;
   load_stream(t, rows[0]);
   load_block(t, rows[0]);
-  float wp[UPT][kUnit], wn[UPT][kUnit], bp[FULL ? UPT : 1][kUnit];
-  {
-    RawVector post_w[UPT], pre_w[UPT], post_b[FULL ? UPT : 1];
+  extern __shared__ float4 weights[];  // IN_LDS: pre weight, post weight, post bias
+  float kept[IN_LDS ? 1 : FULL ? 3 : 2][UPT][kUnit];
+  if constexpr (IN_LDS) {
+    for (int v = 0; v < vectors_in_lds(FULL, a.H); ++v) {
+      const float* from = v == 0 ? a.pre_weight : v == 1 ? a.post_weight : a.post_bias;
+#pragma unroll
+      for (int u = 0; u < UPT; ++u) {
+        RawVector raw;
+        raw.load(from, a.H, p.at[u]);
+        float w[kUnit];
+        raw.widen(v == 2 ? 0.0f : from ? a.offset : 1.0f, w);
+        if (!p.on(u)) continue;
+        float4* to = weights + (int64_t)(v * p.units + p.at[u]) * 2;
+        to[0] = make_float4(w[0], w[1], w[2], w[3]);
+        to[1] = make_float4(w[4], w[5], w[6], w[7]);
+      }
+    }  // read by the thread that wrote them
+  } else {
+    RawVector raw[FULL ? 3 : 2][UPT];
 #pragma unroll
     for (int u = 0; u < UPT; ++u) {
-      pre_w[u].load(a.pre_weight, a.H, p.at[u]);
-      post_w[u].load(a.post_weight, a.H, p.at[u]);
-      if constexpr (FULL) post_b[u].load(a.post_bias, a.H, p.at[u]);
+      raw[0][u].load(a.pre_weight, a.H, p.at[u]);
+      raw[1][u].load(a.post_weight, a.H, p.at[u]);
+      if constexpr (FULL) raw[2][u].load(a.post_bias, a.H, p.at[u]);
     }
     if constexpr (AHEAD == 2) {
       load_stream(t + p.step, rows[1]);
@@ -485,11 +527,27 @@ __global__ __launch_bounds__(most_threads(WAVE)) void norm_backward_kernel(NormB
     }
 #pragma unroll
     for (int u = 0; u < UPT; ++u) {
-      pre_w[u].widen(a.pre_weight ? a.offset : 1.0f, wn[u]);
-      post_w[u].widen(a.post_weight ? a.offset : 1.0f, wp[u]);
-      if constexpr (FULL) post_b[u].widen(0.0f, bp[u]);
+      raw[0][u].widen(a.pre_weight ? a.offset : 1.0f, kept[0][u]);
+      raw[1][u].widen(a.post_weight ? a.offset : 1.0f, kept[1][u]);
+      if constexpr (FULL) raw[2][u].widen(0.0f, kept[2][u]);
     }
   }
+  // a vector's values at a unit, in the order above
+  auto vector = [&](int v, int u, float(&w)[kUnit]) __attribute__((always_inline)) {
+    if constexpr (!IN_LDS) {
+#pragma unroll
+      for (int i = 0; i < kUnit; ++i) w[i] = kept[v][u][i];
+    } else if (v < vectors_in_lds(FULL, a.H)) {
+      const float4* from = weights + (int64_t)(v * p.units + min(p.at[u], p.units - 1)) * 2;
+      const float4 lo = from[0], hi = from[1];
+      w[0] = lo.x; w[1] = lo.y; w[2] = lo.z; w[3] = lo.w;
+      w[4] = hi.x; w[5] = hi.y; w[6] = hi.z; w[7] = hi.w;
+    } else {  // the bias of a long row
+      RawVector raw;
+      raw.load(a.post_bias, a.H, p.at[u]);
+      raw.widen(0.0f, w);
+    }
+  };
   auto hold = [&](Row& r) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < UPT; ++u) {
@@ -506,13 +564,16 @@ __global__ __launch_bounds__(most_threads(WAVE)) void norm_backward_kernel(NormB
     if (FULL && (pre == MEP_NORM_LAYER || post == MEP_NORM_LAYER)) {
       float q[3] = {0.0f, 0.0f, 0.0f};  // what lies past the row's end is 0
 #pragma unroll
-      for (int u = 0; u < UPT; ++u)
+      for (int u = 0; u < UPT; ++u) {
+        float wn[kUnit];
+        vector(0, u, wn);
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) {
           q[0] += now.s[u].at(i);
-          q[1] = fmaf(now.gn[u].at(i), wn[u][i], q[1]);
+          q[1] = fmaf(now.gn[u].at(i), wn[i], q[1]);
           q[2] += now.y[u].at(i);
         }
+      }
       sum(q);
       if (pre == MEP_NORM_LAYER) {
         mean_s = q[0] * inv_h;
@@ -525,16 +586,19 @@ __global__ __launch_bounds__(most_threads(WAVE)) void norm_backward_kernel(NormB
     if (pre != MEP_NORM_NONE || post != MEP_NORM_NONE) {
       float q[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int u = 0; u < UPT; ++u)
+      for (int u = 0; u < UPT; ++u) {
+        float wn[kUnit];
+        vector(0, u, wn);
         if (!FULL || p.on(u))
 #pragma unroll
           for (int i = 0; i < kUnit; ++i) {
             const float s = FULL ? now.s[u].at(i) - mean_s : now.s[u].at(i);
             const float y = FULL ? now.y[u].at(i) - mean_y : now.y[u].at(i);
             q[0] = fmaf(s, s, q[0]);
-            q[1] = fmaf(s, now.gn[u].at(i) * wn[u][i], q[1]);
+            q[1] = fmaf(s, now.gn[u].at(i) * wn[i], q[1]);
             q[2] = fmaf(y, y, q[2]);
           }
+      }
       sum(q);
       if (pre != MEP_NORM_NONE) {
         r_s = inv_root(q[0] * inv_h, a.eps);
@@ -547,13 +611,15 @@ __global__ __launch_bounds__(most_threads(WAVE)) void norm_backward_kernel(NormB
     float grad[UPT][kUnit];
 #pragma unroll
     for (int u = 0; u < UPT; ++u) {
+      float wn[kUnit];
+      vector(0, u, wn);
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) {
         float g = now.gs[u].at(i);  // 0 without grad_s; without grad_n, s and gn are 0
         const float gn = now.gn[u].at(i);
         const float h = FULL ? (now.s[u].at(i) - mean_s) * r_s : now.s[u].at(i) * r_s;
         const float off = FULL ? fmaf(h, along_n, mean_n) : h * along_n;
-        g = fmaf(r_s, fmaf(gn, wn[u][i], -off), g);
+        g = fmaf(r_s, fmaf(gn, wn[i], -off), g);
         acc[1][u][i] = fmaf(gn, h, acc[1][u][i]);
         if constexpr (FULL) acc[3][u][i] += gn;
         grad[u][i] = g;
@@ -581,21 +647,25 @@ __global__ __launch_bounds__(most_threads(WAVE)) void norm_backward_kernel(NormB
     if (post != MEP_NORM_NONE || token_grad) {
       float q[FULL ? 3 : 1] = {0.0f};
 #pragma unroll
-      for (int u = 0; u < UPT; ++u)
+      for (int u = 0; u < UPT; ++u) {
+        float wp[kUnit], bp[kUnit];
+        vector(1, u, wp);
+        if constexpr (FULL) vector(2, u, bp);
         if (!FULL || p.on(u))
 #pragma unroll
           for (int i = 0; i < kUnit; ++i) {
             if constexpr (FULL) {
               float slope;
               const float h = (now.y[u].at(i) - mean_y) * r_y;
-              const float g = factor(u, i, slope) * grad[u][i] * wp[u][i];
+              const float g = factor(u, i, slope) * grad[u][i] * wp[i];
               q[0] = fmaf(g, h, q[0]);
               q[1] += g;
-              q[2] = fmaf(grad[u][i], bp[u][i], q[2]);
+              q[2] = fmaf(grad[u][i], bp[i], q[2]);
             } else {
-              q[0] = fmaf(grad[u][i] * wp[u][i], now.y[u].at(i), q[0]);
+              q[0] = fmaf(grad[u][i] * wp[i], now.y[u].at(i), q[0]);
             }
           }
+      }
       sum(q);
       if constexpr (!FULL) q[0] *= r_y;
       if (post != MEP_NORM_NONE) along_y = c * q[0] * inv_h;
@@ -611,7 +681,9 @@ __global__ __launch_bounds__(most_threads(WAVE)) void norm_backward_kernel(NormB
     const RowBuffer grad_gate(by_element ? a.grad_gate : nullptr, t, a.T, bytes);
 #pragma unroll
     for (int u = 0; u < UPT; ++u) {
-      float back[kUnit], of_gate[kUnit];
+      float back[kUnit], of_gate[kUnit], wp[kUnit], bp[kUnit];
+      vector(1, u, wp);
+      if constexpr (FULL) vector(2, u, bp);
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) {
         if constexpr (FULL) {
@@ -620,12 +692,12 @@ __global__ __launch_bounds__(most_threads(WAVE)) void norm_backward_kernel(NormB
           const float gv = c * factor(u, i, slope) * grad[u][i];
           acc[0][u][i] = fmaf(gv, h, acc[0][u][i]);
           acc[2][u][i] += gv;
-          back[i] = r_y * fmaf(gv, wp[u][i], -fmaf(h, along_y, mean_v));
-          of_gate[i] = a.block_scale * slope * grad[u][i] * fmaf(h, wp[u][i], bp[u][i]);
+          back[i] = r_y * fmaf(gv, wp[i], -fmaf(h, along_y, mean_v));
+          of_gate[i] = a.block_scale * slope * grad[u][i] * fmaf(h, wp[i], bp[i]);
         } else {
           const float h = now.y[u].at(i) * r_y, gv = c * grad[u][i];
           acc[0][u][i] = fmaf(gv, h, acc[0][u][i]);
-          back[i] = r_y * fmaf(gv, wp[u][i], -(h * along_y));
+          back[i] = r_y * fmaf(gv, wp[i], -(h * along_y));
         }
       }
       store_unit((TL*)nullptr, grad_y, p.at[u], back);
@@ -645,20 +717,41 @@ __global__ __launch_bounds__(most_threads(WAVE)) void norm_backward_kernel(NormB
       }
     }
   }
-  // this block's (or wave's) partial sums: wanted columns one after the other
-  float* part = a.part + p.first * a.H;
+  // this block's partial sums: wanted columns one after the other
+  float* part = a.part + (int64_t)blockIdx.x * a.H;
   constexpr int kOf[4] = {0, 2, 1, 3};  // columns[] in the order of acc
 #pragma unroll
   for (int c = 0; c < COLS; ++c) {
     if (!a.columns[kOf[c]]) continue;
+    if constexpr (WAVE) {  // four waves' sums first
+      __shared__ float4 join[4][UPT * 2 * kWave];
 #pragma unroll
-    for (int u = 0; u < UPT; ++u)
-      if (p.on(u)) {  // read again at once: through the caches
-        float4* to = reinterpret_cast<float4*>(part) + 2 * p.at[u];
-        to[0] = make_float4(acc[c][u][0], acc[c][u][1], acc[c][u][2], acc[c][u][3]);
-        to[1] = make_float4(acc[c][u][4], acc[c][u][5], acc[c][u][6], acc[c][u][7]);
+      for (int u = 0; u < UPT; ++u)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          join[threadIdx.x / kWave][(u * 2 + h) * kWave + p.lane] =
+              make_float4(acc[c][u][4 * h], acc[c][u][4 * h + 1], acc[c][u][4 * h + 2], acc[c][u][4 * h + 3]);
+      __syncthreads();
+      for (int i = threadIdx.x; i < UPT * 2 * kWave; i += 4 * kWave) {
+        float4 v = join[0][i];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) {
+          v.x += join[w][i].x; v.y += join[w][i].y; v.z += join[w][i].z; v.w += join[w][i].w;
+        }
+        const int unit = i / (2 * kWave) * kWave + i % kWave, h = i / kWave % 2;
+        if (unit < p.units) reinterpret_cast<float4*>(part)[2 * unit + h] = v;
       }
-    part += p.step * a.H;
+      __syncthreads();
+    } else {
+#pragma unroll
+      for (int u = 0; u < UPT; ++u)
+        if (p.on(u)) {  // read again at once: through the caches
+          float4* to = reinterpret_cast<float4*>(part) + 2 * p.at[u];
+          to[0] = make_float4(acc[c][u][0], acc[c][u][1], acc[c][u][2], acc[c][u][3]);
+          to[1] = make_float4(acc[c][u][4], acc[c][u][5], acc[c][u][6], acc[c][u][7]);
+        }
+    }
+    part += (int64_t)gridDim.x * a.H;
   }
 }
 
@@ -692,28 +785,32 @@ __global__ __launch_bounds__(kColumns * kSlices) void norm_columns_kernel(const 
 
 // How a row of H values is held: by a wave or a block, with so many units a thread.
 struct RowShape {
-  bool wave;
+  int kind;                // kWaveRows, kHalfBlock or kBlock
   int upt, threads, rows;  // rows: a block works on at once
 };
 
 RowShape row_shape(int H) {
   const int units = H / kUnit;
-  if (units <= 2 * kWave) return {true, units <= kWave ? 1 : 2, 4 * kWave, 4};
-  const int upt = units <= kMaxWaves * kWave ? 1 : 2;
-  const int lanes = (units + upt - 1) / upt;
-  return {false, upt, (lanes + kWave - 1) / kWave * kWave, 1};
+  if (units <= 2 * kWave) return {kWaveRows, units <= kWave ? 1 : 2, 4 * kWave, 4};
+  const int upt = units <= kBlock ? 1 : 2;
+  const int lanes = ((units + upt - 1) / upt + kWave - 1) / kWave * kWave;
+  return {lanes <= kHalfBlock ? kHalfBlock : kBlock, upt, lanes, 1};
 }
 
-// Calls f(units a thread, whether a wave holds a row).
+// Calls f(units a thread, kind).
 template <class F>
 void by_shape(const RowShape& r, F f) {
   using std::integral_constant;
-  if (r.wave) {
-    if (r.upt == 1) f(integral_constant<int, 1>{}, std::true_type{});
-    else f(integral_constant<int, 2>{}, std::true_type{});
+  const integral_constant<int, 1> one;
+  const integral_constant<int, 2> two;
+  if (r.kind == kWaveRows) {
+    const integral_constant<int, kWaveRows> kind;
+    if (r.upt == 1) f(one, kind); else f(two, kind);
+  } else if (r.kind == kHalfBlock) {
+    f(one, integral_constant<int, kHalfBlock>{});
   } else {
-    if (r.upt == 1) f(integral_constant<int, 1>{}, std::false_type{});
-    else f(integral_constant<int, 2>{}, std::false_type{});
+    const integral_constant<int, kBlock> kind;
+    if (r.upt == 1) f(one, kind); else f(two, kind);
   }
 }
 
@@ -736,35 +833,50 @@ int blocks_for(const RowShape& r, int32_t T, int most) {
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
   const RowShape r = row_shape(a.H);
-  const int blocks = blocks_for(r, a.T, 512);
-  by_shape(r, [&](auto upt, auto wave) {
-    auto launch = [&](auto type, auto full) {
-      norm_kernel<decltype(type), upt(), wave(), full()><<<blocks, r.threads, 0, s>>>(a);
-    };
-    const bool full = a.post_bias || a.pre_bias || a.gate_kind == MEP_BLOCK_GATE_ELEMENT ||
-                      a.post == MEP_NORM_LAYER || a.pre == MEP_NORM_LAYER;
-    by_type(a.dtype, full, launch);
+  const bool full = a.post_bias || a.pre_bias || a.gate_kind == MEP_BLOCK_GATE_ELEMENT ||
+                    a.post == MEP_NORM_LAYER || a.pre == MEP_NORM_LAYER;
+  const bool bf16 = a.dtype == MEP_BF16;
+  // Blocks that the CUs hold at once and no more, as each loads the weights.  4096 rows
+  // with 256, 512, 1024 blocks (us): 7168 bf16 columns 44.4, 43.3, 48.7, with layer norms,
+  // biases and a gate for every element 60.5, 62.1, 67.1; 2056 columns 22.0, 17.5, 15.3, in
+  // fp32 with all of it 40.0, 38.0, 45.0; 512 by wave 5.3, 4.5, 4.5 (768: 4.2).
+  const int most = r.kind == kWaveRows ? 768
+                   : r.kind == kBlock && (full || !bf16 || r.upt > 1) ? 256
+                   : bf16 && r.threads <= 384 ? 1024 : 512;
+  const int blocks = blocks_for(r, a.T, most);
+  by_shape(r, [&](auto upt, auto kind) {
+    by_type(a.dtype, full, [&](auto type, auto f) {
+      norm_kernel<decltype(type), upt(), kind(), f()><<<blocks, r.threads, 0, s>>>(a);
+    });
   });
   return hipGetLastError();
 }
 
-int norm_backward_blocks(int32_t H, int32_t T) {
-  const RowShape r = row_shape(H);
-  return blocks_for(r, T, 256) * r.rows;
+// Blocks of the gradients' launch, each of which leaves a row of partial sums: one a CU,
+// two where they fit.  4096 rows with 256 and 512 blocks (us): 2056 bf16 columns 42 and
+// 34, all of it in fp32 90 and 95, 7168 bf16 columns 72 and 80, 512 columns by wave 19 and 24.
+static int backward_blocks(const RowShape& r, int32_t T, bool full, bool bf16) {
+  return blocks_for(r, T, packed_halves(r.kind, full, bf16) ? 512 : 256);
+}
+
+int norm_backward_blocks(int32_t H, int32_t T) {  // the most of all
+  return backward_blocks(row_shape(H), T, false, true);
 }
 
 hipError_t launch_block_norm_backward(const NormBackwardArgs& a, hipStream_t s) {
   const RowShape r = row_shape(a.H);
-  const int blocks = blocks_for(r, a.T, 256);
+  const bool full = a.columns[1] || a.columns[3] || a.post_bias ||
+                    a.gate_kind == MEP_BLOCK_GATE_ELEMENT || a.post == MEP_NORM_LAYER ||
+                    a.pre == MEP_NORM_LAYER;
+  const int blocks = backward_blocks(r, a.T, full, a.dtype == MEP_BF16);
   if (blocks > 0) {
-    by_shape(r, [&](auto upt, auto wave) {
-      auto launch = [&](auto type, auto full) {
-        norm_backward_kernel<decltype(type), upt(), wave(), full()><<<blocks, r.threads, 0, s>>>(a);
-      };
-      const bool full = a.columns[1] || a.columns[3] || a.post_bias ||
-                        a.gate_kind == MEP_BLOCK_GATE_ELEMENT || a.post == MEP_NORM_LAYER ||
-                        a.pre == MEP_NORM_LAYER;
-      by_type(a.dtype, full, launch);
+    const size_t lds = weights_in_lds(r.kind, r.upt, full, a.dtype == MEP_BF16)
+                           ? (size_t)vectors_in_lds(full, a.H) * a.H * sizeof(float)
+                           : 0;
+    by_shape(r, [&](auto upt, auto kind) {
+      by_type(a.dtype, full, [&](auto type, auto f) {
+        norm_backward_kernel<decltype(type), upt(), kind(), f()><<<blocks, r.threads, lds, s>>>(a);
+      });
     });
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
@@ -774,7 +886,7 @@ hipError_t launch_block_norm_backward(const NormBackwardArgs& a, hipStream_t s) 
     if (a.columns[c]) out[n++] = a.columns[c];
   if (n > 0)
     norm_columns_kernel<<<dim3((a.H + kColumns - 1) / kColumns, n), kColumns * kSlices, 0, s>>>(
-        a.part, blocks * r.rows, a.H, out[0], out[1], out[2], out[3]);
+        a.part, blocks, a.H, out[0], out[1], out[2], out[3]);
   return hipGetLastError();
 }
 

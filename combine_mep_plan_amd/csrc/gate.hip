@@ -313,64 +313,165 @@ __device__ __forceinline__ uint64_t best_groups(Key (&key)[SLOTS], int l, int G,
   return chosen;
 }
 
-// The groups a token's experts come from.  The scores go through LDS (`shared`, E values
-// of the token's own), from where lane l takes those of groups l, l + LPT, ..  Only
-// which groups are chosen counts, not their order: where the worst chosen and the best
-// left out are too close for fp32, their scores are worked out again in 64 bits.
-// Each score is within 2^-22 (1 + |score|) (see scores_apart; an exponential of a value
-// at most 0 is nearer still), so a sum of two within 2^-21 (2 + |a| + |b|) with its own
-// rounding.
+// The first and second of the values seen so far, one more seen (b is the median of
+// the old first, the old second and it).
+__device__ __forceinline__ void see(float v, float& a, float& b) {
+  b = __builtin_amdgcn_fmed3f(a, b, v);
+  a = fmaxf(a, v);
+}
+
+// A group's first and second from two parts of it.
+__device__ __forceinline__ void join_parts(float oa, float ob, float& a, float& b) {
+  b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+  a = fmaxf(a, oa);
+}
+
+template <int CTRL>
+__device__ __forceinline__ void join_lanes(float& a, float& b) {
+  const float oa = __uint_as_float(dpp<CTRL>(__float_as_uint(a)));
+  const float ob = __uint_as_float(dpp<CTRL>(__float_as_uint(b)));
+  join_parts(oa, ob, a, b);
+}
+
+// Adds to `before` the lanes TURN, TURN + 1, .. 15 places down the row of 16 whose key is
+// above lane l's, or equal in a lower lane, those of another token left out.
+template <int LPT, int TURN = 1>
+__device__ __forceinline__ void rank_in_row(uint32_t key, int l, int& before) {
+  const uint32_t o = dpp<0x120 + TURN>(key);  // row_ror: lane i gets lane i - TURN's
+  const int from = (lane_id() - TURN) & 15;
+  const bool mine = LPT >= 16 || ((from ^ lane_id()) & LPT) == 0;
+  before += mine && (o > key || (o == key && (from & (LPT - 1)) < l));
+  if constexpr (TURN < 15) rank_in_row<LPT, TURN + 1>(key, l, before);
+}
+
+// How many groups come before lane l's among the token's lanes, which hold a group each
+// (key 0: none).  All lanes must call it.
+template <int LPT>
+__device__ __forceinline__ int group_rank(uint32_t key, int l, int G) {
+  int before = 0;
+  if constexpr (LPT == 64) {
+    for (int g = 0; g < G; ++g) {
+      const uint32_t o = (uint32_t)lane_value((int)key, g);
+      before += o > key || (o == key && g < l);
+    }
+  } else {
+    rank_in_row<LPT>(key, l, before);
+  }
+  return before;
+}
+
+// The groups a token's experts come from, as a set of bits.  Only which groups are chosen
+// counts, not their order: where the worst chosen and the best left out are too close for
+// fp32, their scores are worked out again in 64 bits.  Each score is within 2^-22 (1 +
+// |score|) (see scores_apart; an exponential of a value at most 0 is nearer still), so a
+// sum of two within 2^-21 (2 + |a| + |b|) with its own rounding.
+//   Groups that are whole 16-byte units over a power of two of lanes are joined in
+// registers; the others' scores go through LDS (`shared`, E values of the token's own),
+// where a lane takes a whole group.  256 experts in 8 groups, the best 4 by their two
+// best: 16384 tokens 21.1 us, one token 7.3 (15.4 and 5.2 to 5.9 without groups); all
+// groups through LDS and chosen round by round 28.2 and 10.1.
 template <class TL, int LPT, int EPL>
 __device__ __forceinline__ uint64_t choose_groups(const GroupScore& q, const float (&score)[EPL],
-                                                  const TL* row, float shift, int E, int l,
+                                                  const TL* row, float shift, int E, int l, bool wide,
                                                   float* shared) {
-  constexpr int SLOTS = 64 / LPT;
+  constexpr int SLOTS = 64 / LPT, V = Vec<TL>::V;
   constexpr float kNone = -__builtin_inff();
+  const int span = q.S / V;  // lanes of a group
+  const bool in_registers =
+      wide && q.S % V == 0 && (span & (span - 1)) == 0 && span <= (LPT < 16 ? LPT : 16);
+  auto sync = [] {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
+  if (in_registers) {
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = expert_of<TL, LPT>(i, l);
-    if (e < E) shared[e] = fmaxf(score[i], kNone);  // NaN: -inf
-  }
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  float val[SLOTS], err[SLOTS];
-  uint32_t key[SLOTS];
-#pragma unroll
-  for (int u = 0; u < SLOTS; ++u) {
-    const int g = u * LPT + l;
-    val[u] = err[u] = 0.0f;
-    key[u] = 0u;
-    if (g < q.G) {
+    for (int c = 0; c < EPL; c += V) {
       float a = kNone, b = kNone;
-      for (int i = 0; i < q.S; ++i) {
-        const float v = shared[g * q.S + i];
-        b = fmaxf(b, fminf(a, v));
-        a = fmaxf(a, v);
-      }
-      val[u] = join_top(q.by, a, b);
-      err[u] = q.by == MEP_GROUP_TOP2 ? fabsf(a) + fabsf(b) : fabsf(a);
-      err[u] = 4.76837158203125e-07f * (2.0f + err[u]);
-      key[u] = order_key(val[u]);
+#pragma unroll
+      for (int i = 0; i < V; ++i) see(fmaxf(score[c + i], kNone), a, b);  // NaN: -inf
+      if (span >= 2) join_lanes<kXor1>(a, b);
+      if (span >= 4) join_lanes<kXor2>(a, b);
+      if (span >= 8) join_lanes<kHalfMirror>(a, b);
+      if (LPT >= 16 && span >= 16) join_lanes<kMirror>(a, b);
+      const int e = expert_of<TL, LPT>(c, l);
+      if (e < E && (l & (span - 1)) == 0)
+        reinterpret_cast<float2*>(shared)[group_of(q, e)] = make_float2(a, b);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = expert_of<TL, LPT>(i, l);
+      if (e < E) shared[e] = fmaxf(score[i], kNone);
     }
   }
-  uint64_t chosen = best_groups<LPT>(key, l, q.G, q.M);
-  if (q.exact) return chosen;
+  sync();
+  auto top = [&](int g, float& a, float& b) __attribute__((always_inline)) {
+    if (in_registers) {
+      const float2 v = reinterpret_cast<const float2*>(shared)[g];
+      a = v.x;
+      b = v.y;
+      return;
+    }
+    a = b = kNone;
+#pragma unroll 4
+    for (int i = 0; i < q.S; ++i) see(shared[g * q.S + i], a, b);
+  };
+  auto error_of = [&](float a, float b) {
+    const float of = q.by == MEP_GROUP_TOP2 ? fabsf(a) + fabsf(b) : fabsf(a);
+    return 4.76837158203125e-07f * (2.0f + of);
+  };
+  uint64_t chosen;
   float low = __builtin_inff(), high = kNone;
+  if (q.G <= LPT) {  // a lane a group
+    float val = 0.0f, err = 0.0f;
+    uint32_t key = 0u;
+    if (l < q.G) {
+      float a, b;
+      top(l, a, b);
+      val = join_top(q.by, a, b);
+      err = error_of(a, b);
+      key = order_key(val);
+    }
+    const int rank = group_rank<LPT>(key, l, q.G);
+    const bool in = l < q.G && rank < q.M;
+    chosen = ballot(in);
+    if (LPT < 64) chosen = chosen >> (lane_id() & (64 - LPT)) & ((1ull << (LPT & 63)) - 1);
+    if (in) low = val - err;
+    else if (l < q.G) high = val + err;
+  } else {
+    float val[SLOTS], err[SLOTS];
+    uint32_t key[SLOTS];
 #pragma unroll
-  for (int u = 0; u < SLOTS; ++u) {
-    const int g = u * LPT + l;
-    if (g >= q.G) continue;
-    if ((chosen >> g) & 1) low = fminf(low, val[u] - err[u]);
-    else high = fmaxf(high, val[u] + err[u]);
+    for (int u = 0; u < SLOTS; ++u) {
+      const int g = u * LPT + l;
+      val[u] = err[u] = 0.0f;
+      key[u] = 0u;
+      if (g < q.G) {
+        float a, b;
+        top(g, a, b);
+        val[u] = join_top(q.by, a, b);
+        err[u] = error_of(a, b);
+        key[u] = order_key(val[u]);
+      }
+    }
+    chosen = best_groups<LPT>(key, l, q.G, q.M);
+#pragma unroll
+    for (int u = 0; u < SLOTS; ++u) {
+      const int g = u * LPT + l;
+      if (g >= q.G) continue;
+      if ((chosen >> g) & 1) low = fminf(low, val[u] - err[u]);
+      else high = fmaxf(high, val[u] + err[u]);
+    }
   }
+  if (q.exact) return chosen;
   low = -group_fmax<LPT>(-low);
   high = group_fmax<LPT>(high);
   if (low > high) return chosen;
-  uint64_t wide[SLOTS];
+  uint64_t exact[SLOTS];
 #pragma unroll
   for (int u = 0; u < SLOTS; ++u) {
     const int g = u * LPT + l;
-    wide[u] = 0;
+    exact[u] = 0;
     if (g < q.G) {
       double a = kNone, b = kNone;
       for (int i = 0; i < q.S; ++i) {
@@ -382,10 +483,10 @@ __device__ __forceinline__ uint64_t choose_groups(const GroupScore& q, const flo
         b = fmax(b, fmin(a, v));
         a = fmax(a, v);
       }
-      wide[u] = order_key(join_top(q.by, a, b));
+      exact[u] = order_key(join_top(q.by, a, b));
     }
   }
-  return best_groups<LPT>(wide, l, q.G, q.M);
+  return best_groups<LPT>(exact, l, q.G, q.M);
 }
 
 // k rounds of "largest first, the lowest expert among equals".  The rounds and
@@ -454,7 +555,7 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
         else score[i] = a.score == MEP_SCORE_SOFTMAX ? fast_exp(x[i] - shift) : fast_sigmoid(x[i]);
       }
       const uint64_t chosen = choose_groups<TL, LPT, EPL>(
-          q, score, row, shift, E, l, group_scores + (size_t)(threadIdx.x / LPT) * E);
+          q, score, row, shift, E, l, a.wide, group_scores + (size_t)(threadIdx.x / LPT) * E);
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
         const int e = expert_of<TL, LPT>(i, l);

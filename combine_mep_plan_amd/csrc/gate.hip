@@ -113,8 +113,6 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-constexpr float kLog2E = 1.44269504088896341f;
-
 // exp(x) in two instructions: the hardware's power of two of the rounded x log2 e,
 // so within 2 + 1.5 |x| half-steps of fp32 (relative).  For the selection's keys,
 // whose absolute error counts, and for probabilities of all experts, of which those
@@ -122,20 +120,6 @@ constexpr float kLog2E = 1.44269504088896341f;
 // balance loss of 4096 x 256 16.0 -> 17.0 us, the gradient 6.6 -> 6.9).
 __device__ __forceinline__ float fast_exp(float x) {
   return __builtin_amdgcn_exp2f(x * kLog2E);
-}
-
-// For the weights, which may all be small: exp(x) of x <= 0 within 4 half-steps.
-// exp(x) = 2^t exp(x - t ln 2), where t is the rounded x log2 e; the rest, below
-// 2^-17, is worked out with ln 2 in two parts and enters to first order.  Where t is
-// -inf the rest is NaN (its parts are infinities of both signs), which the maximum
-// turns into a number that the power, 0, makes nothing of; NaN stays NaN by the
-// power.
-__device__ __forceinline__ float exp_f32(float x) {
-  constexpr float kLn2 = 0.693147180559945309f;
-  constexpr float kLn2Low = (float)(0.693147180559945309 - (double)kLn2);
-  const float t = x * kLog2E, y = __builtin_amdgcn_exp2f(t);
-  const float rest = fmaxf(fmaf(-t, kLn2Low, fmaf(-t, kLn2, x)), -1.0f);
-  return fmaf(y, rest, y);
 }
 
 template <bool EXACT>

@@ -59,7 +59,7 @@ struct Piece {
   __device__ __forceinline__ void scale(float f) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      q[i] = BF16 ? pack_bf16_rne(bf16_lo(q[i]) * f, bf16_hi(q[i]) * f)
+      q[i] = BF16 ? pack_bf16_pair(bf16_lo(q[i]) * f, bf16_hi(q[i]) * f)
                   : __float_as_uint(__uint_as_float(q[i]) * f);
   }
 };
@@ -152,7 +152,7 @@ __device__ __forceinline__ void clip_chunk(const Chunk& k, float f) {
       },
       [&](int i) {
         if (BF16)
-          reinterpret_cast<uint16_t*>(k.out)[k.at + i] = (uint16_t)pack_bf16_rne(
+          reinterpret_cast<uint16_t*>(k.out)[k.at + i] = (uint16_t)pack_bf16_pair(
               bf16_lo(reinterpret_cast<const uint16_t*>(k.data)[k.at + i]) * f, 0.0f);
         else
           reinterpret_cast<float*>(k.out)[k.at + i] =

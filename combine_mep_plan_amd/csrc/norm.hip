@@ -122,6 +122,10 @@ struct Raw<uint16_t> {
     q = __builtin_amdgcn_raw_buffer_load_b128(b.r, unit * 16, 0, kPast);
   }
   __device__ __forceinline__ float at(int i) const { return i & 1 ? bf16_hi(q[i / 2]) : bf16_lo(q[i / 2]); }
+  __device__ __forceinline__ void widen(float (&v)[kUnit]) const {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) v[i] = at(i);
+  }
   // The compiler forgets what it has made of the values so far, and widens them again
   // where they are needed next instead of keeping them in twice the registers.
   __device__ __forceinline__ void hold() { asm volatile("" : "+v"(q)); }
@@ -134,6 +138,10 @@ struct Raw<float> {
     q[1] = __builtin_amdgcn_raw_buffer_load_b128(b.r, unit * 32 + 16, 0, kPast);
   }
   __device__ __forceinline__ float at(int i) const { return __uint_as_float(q[i / 4][i % 4]); }
+  __device__ __forceinline__ void widen(float (&v)[kUnit]) const {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) v[i] = at(i);
+  }
   __device__ __forceinline__ void hold() { asm volatile("" : "+v"(q[0]), "+v"(q[1])); }
 };
 
@@ -141,7 +149,7 @@ __device__ __forceinline__ void store_unit(uint16_t*, const RowBuffer& b, int un
                                            const float (&v)[kUnit]) {
   u32x4 q;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = pack_bf16_rne(v[2 * i], v[2 * i + 1]);
+  for (int i = 0; i < 4; ++i) q[i] = pack_bf16_pair(v[2 * i], v[2 * i + 1]);
   __builtin_amdgcn_raw_buffer_store_b128(q, b.r, unit * 16, 0, kPast);
 }
 __device__ __forceinline__ void store_unit(float*, const RowBuffer& b, int unit,
@@ -175,15 +183,24 @@ __device__ __forceinline__ float load_token(const void* p, int64_t t, int64_t T)
   return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b.r, 0, 0, 0));
 }
 
-// The gate's factor and its slope.
-__device__ __forceinline__ float open_gate(float g, int sigmoid, float& slope) {
-  if (!sigmoid) {
-    slope = 1.0f;
-    return g;
+// A gate's factors and their slopes, N of them; sigmoids within 8 half-steps.
+template <int N>
+__device__ __forceinline__ void open_gate(const float (&g)[N], int sigmoid, float (&f)[N],
+                                          float (&slope)[N]) {
+  if (sigmoid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float e = exp_f32(-fabsf(g[i])), r = __builtin_amdgcn_rcpf(1.0f + e);
+      slope[i] = e * r * r;
+      f[i] = g[i] < 0.0f ? e * r : r;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      slope[i] = 1.0f;
+      f[i] = g[i];
+    }
   }
-  const float e = expf(-fabsf(g)), r = 1.0f / (1.0f + e);
-  slope = e * r * r;
-  return g < 0.0f ? e * r : r;
 }
 
 // Within 2 half-steps of fp32, as the root's error and the quotient's together would be.
@@ -240,11 +257,20 @@ __device__ __forceinline__ u32x2 encode_unit(const float (&v)[kUnit], float& sca
   return u32x2{pack_e4m3x4(q[0], q[1], q[2], q[3]), pack_e4m3x4(q[4], q[5], q[6], q[7])};
 }
 
+// Waves a SIMD that a forward kernel of bf16 rows is kept to.  8 without FULL, so that two
+// blocks of 14 waves (7168 columns) share a CU, whose first SIMD then holds 8 waves: 4096
+// rows with E4M3 codes too take 49.4 us (5.4 TB/s), an earlier state of the kernel 58 where
+// one block had the CU 64 to 70.  6 for half blocks with FULL: 4096 x 2056 20.6 us, 25.6
+// with 5; not for whole blocks, of which one has the CU either way (4096 x 7168 55.0, 56.6).
+constexpr int forward_waves(int rows, int upt, bool full, bool bf16) {
+  if (rows == kWaveRows || upt > 1 || !bf16) return 1;
+  return rows == kHalfBlock ? full ? 6 : 1 : full ? 1 : 8;
+}
+
 // FULL: with biases, layer norms or a gate for every element, which take registers and
-// instructions of their own; 8 waves a SIMD without, so that two blocks of 7168 columns
-// fit a CU (4096 rows in bf16: 58 us, with one block 64 to 70).
+// instructions of their own.
 template <class TL, int UPT, int ROWS, bool FULL>
-__global__ __launch_bounds__(most_threads(ROWS), ROWS == kBlock && !FULL && sizeof(TL) * UPT == 2 ? 8 : 1)
+__global__ __launch_bounds__(most_threads(ROWS), forward_waves(ROWS, UPT, FULL, sizeof(TL) == 2))
 void norm_kernel(NormArgs a) {
   constexpr bool WAVE = ROWS == kWaveRows;
   __shared__ float4 lds[2][kMaxWaves];
@@ -310,7 +336,7 @@ void norm_kernel(NormArgs a) {
     if (t + p.step < a.T) load(t + p.step, next);
     float v[UPT][kUnit];
     if (a.y) {
-      float mean = 0.0f, r = 1.0f, slope;
+      float mean = 0.0f, r = 1.0f;
       if (post_layer) {
         float q[1] = {0.0f};
 #pragma unroll
@@ -334,19 +360,28 @@ void norm_kernel(NormArgs a) {
         r = inv_root(q[0] * inv_h, a.eps);
       }
       float c = a.block_scale;
-      if (by_token) c *= open_gate(now.g, a.sigmoid, slope);
+      if (by_token) {
+        float f[1], slope[1];
+        open_gate({now.g}, a.sigmoid, f, slope);
+        c *= f[0];
+      }
 #pragma unroll
       for (int u = 0; u < UPT; ++u)
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) {
-          if constexpr (FULL) {
-            float f = fmaf((now.y[u].at(i) - mean) * r, wp[u][i], bp[u][i]);
-            if (by_element) f *= open_gate(now.gate[u].at(i), a.sigmoid, slope);
-            v[u][i] = f * c;
-          } else {
-            v[u][i] = now.y[u].at(i) * (r * c) * wp[u][i];
-          }
+          if constexpr (FULL) v[u][i] = fmaf((now.y[u].at(i) - mean) * r, wp[u][i], bp[u][i]) * c;
+          else v[u][i] = now.y[u].at(i) * (r * c) * wp[u][i];
         }
+      if (by_element) {
+#pragma unroll
+        for (int u = 0; u < UPT; ++u) {
+          float g[kUnit], f[kUnit], slope[kUnit];
+          now.gate[FULL ? u : 0].widen(g);
+          open_gate(g, a.sigmoid, f, slope);
+#pragma unroll
+          for (int i = 0; i < kUnit; ++i) v[u][i] *= f[i];
+        }
+      }
     } else {
 #pragma unroll
       for (int u = 0; u < UPT; ++u)
@@ -635,12 +670,19 @@ void norm_backward_kernel(NormBackwardArgs a) {
       store_unit((TL*)nullptr, grad_x, p.at[u], f);
     }
     // the block's part (without a block y is 0, and nothing of this is stored)
-    float slope_row = 1.0f, c = a.block_scale;
-    if (by_token) c *= open_gate(now.g, a.sigmoid, slope_row);
-    // the gate's factor without c
-    auto factor = [&](int u, int i, float& slope) __attribute__((always_inline)) {
-      slope = 1.0f;
-      return by_element ? open_gate(now.gate[FULL ? u : 0].at(i), a.sigmoid, slope) : 1.0f;
+    float f_row[1] = {1.0f}, slope_row[1] = {1.0f};
+    if (by_token) open_gate({now.g}, a.sigmoid, f_row, slope_row);
+    const float c = a.block_scale * f_row[0];
+    // a unit's gate factors without c, and their slopes
+    auto factors = [&](int u, float(&f)[kUnit], float(&slope)[kUnit]) __attribute__((always_inline)) {
+      if (by_element) {
+        float g[kUnit];
+        now.gate[FULL ? u : 0].widen(g);
+        open_gate(g, a.sigmoid, f, slope);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) f[i] = slope[i] = 1.0f;
+      }
     };
     const bool token_grad = by_token && a.grad_gate;
     float mean_v = 0.0f, along_y = 0.0f, of_row = 0.0f;
@@ -648,16 +690,18 @@ void norm_backward_kernel(NormBackwardArgs a) {
       float q[FULL ? 3 : 1] = {0.0f};
 #pragma unroll
       for (int u = 0; u < UPT; ++u) {
-        float wp[kUnit], bp[kUnit];
+        float wp[kUnit], bp[kUnit], f[kUnit], slope[kUnit];
         vector(1, u, wp);
-        if constexpr (FULL) vector(2, u, bp);
+        if constexpr (FULL) {
+          vector(2, u, bp);
+          factors(u, f, slope);
+        }
         if (!FULL || p.on(u))
 #pragma unroll
           for (int i = 0; i < kUnit; ++i) {
             if constexpr (FULL) {
-              float slope;
               const float h = (now.y[u].at(i) - mean_y) * r_y;
-              const float g = factor(u, i, slope) * grad[u][i] * wp[i];
+              const float g = f[i] * grad[u][i] * wp[i];
               q[0] = fmaf(g, h, q[0]);
               q[1] += g;
               q[2] = fmaf(grad[u][i], bp[i], q[2]);
@@ -673,7 +717,7 @@ void norm_backward_kernel(NormBackwardArgs a) {
         if (post == MEP_NORM_LAYER) mean_v = c * q[1] * inv_h;
         q[0] += q[2];
       }
-      of_row = a.block_scale * q[0] * slope_row;  // a gate a row: sum of grad v
+      of_row = a.block_scale * q[0] * slope_row[0];  // a gate a row: sum of grad v
 #pragma unroll
       for (int u = 0; u < UPT; ++u) now.y[u].hold();
     }
@@ -681,19 +725,21 @@ void norm_backward_kernel(NormBackwardArgs a) {
     const RowBuffer grad_gate(by_element ? a.grad_gate : nullptr, t, a.T, bytes);
 #pragma unroll
     for (int u = 0; u < UPT; ++u) {
-      float back[kUnit], of_gate[kUnit], wp[kUnit], bp[kUnit];
+      float back[kUnit], of_gate[kUnit], wp[kUnit], bp[kUnit], f[kUnit], slope[kUnit];
       vector(1, u, wp);
-      if constexpr (FULL) vector(2, u, bp);
+      if constexpr (FULL) {
+        vector(2, u, bp);
+        factors(u, f, slope);
+      }
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) {
         if constexpr (FULL) {
-          float slope;
           const float h = (now.y[u].at(i) - mean_y) * r_y;
-          const float gv = c * factor(u, i, slope) * grad[u][i];
+          const float gv = c * f[i] * grad[u][i];
           acc[0][u][i] = fmaf(gv, h, acc[0][u][i]);
           acc[2][u][i] += gv;
           back[i] = r_y * fmaf(gv, wp[i], -fmaf(h, along_y, mean_v));
-          of_gate[i] = a.block_scale * slope * grad[u][i] * fmaf(h, wp[i], bp[i]);
+          of_gate[i] = a.block_scale * slope[i] * grad[u][i] * fmaf(h, wp[i], bp[i]);
         } else {
           const float h = now.y[u].at(i) * r_y, gv = c * grad[u][i];
           acc[0][u][i] = fmaf(gv, h, acc[0][u][i]);

@@ -317,19 +317,22 @@ __device__ __forceinline__ void join_lanes(float& a, float& b) {
   join_parts(oa, ob, a, b);
 }
 
-// Adds to `before` the lanes TURN, TURN + 1, .. 15 places down the row of 16 whose key is
-// above lane l's, or equal in a lower lane, those of another token left out.
-template <int LPT, int TURN = 1>
+// Adds to `before` the lanes TURN, TURN + 1, .. LAST places down the row of 16, wrapping
+// around, whose key is above this lane's, or equal in a lower lane: of a lane that has not
+// wrapped around (l >= TURN) that is a key above key - 1.  With 8 lanes a token the other
+// token's lanes are left out.
+template <int LPT, int LAST, int TURN = 1>
 __device__ __forceinline__ void rank_in_row(uint32_t key, int l, int& before) {
   const uint32_t o = dpp<0x120 + TURN>(key);  // row_ror: lane i gets lane i - TURN's
   const int from = (lane_id() - TURN) & 15;
   const bool mine = LPT >= 16 || ((from ^ lane_id()) & LPT) == 0;
-  before += mine && (o > key || (o == key && (from & (LPT - 1)) < l));
-  if constexpr (TURN < 15) rank_in_row<LPT, TURN + 1>(key, l, before);
+  before += mine && o > key - (LPT >= 16 ? l >= TURN : (from & (LPT - 1)) < l);
+  if constexpr (TURN < LAST) rank_in_row<LPT, LAST, TURN + 1>(key, l, before);
 }
 
 // How many groups come before lane l's among the token's lanes, which hold a group each
-// (key 0: none).  All lanes must call it.
+// (keys above 0; 0: none), the first G lanes of 16, or with G <= 8 the same ones twice over,
+// so that 7 turns go round.  All lanes must call it; of lanes past G it says nothing.
 template <int LPT>
 __device__ __forceinline__ int group_rank(uint32_t key, int l, int G) {
   int before = 0;
@@ -338,8 +341,10 @@ __device__ __forceinline__ int group_rank(uint32_t key, int l, int G) {
       const uint32_t o = (uint32_t)lane_value((int)key, g);
       before += o > key || (o == key && g < l);
     }
+  } else if (LPT == 16 && G <= 8) {
+    rank_in_row<LPT, 7>(key, l & 7, before);
   } else {
-    rank_in_row<LPT>(key, l, before);
+    rank_in_row<LPT, 15>(key, l, before);
   }
   return before;
 }
@@ -409,9 +414,10 @@ __device__ __forceinline__ uint64_t choose_groups(const GroupScore& q, const flo
   if (q.G <= LPT) {  // a lane a group
     float val = 0.0f, err = 0.0f;
     uint32_t key = 0u;
-    if (l < q.G) {
+    const int g = LPT == 16 && q.G <= 8 ? l & 7 : l;
+    if (g < q.G) {
       float a, b;
-      top(l, a, b);
+      top(g, a, b);
       val = join_top(q.by, a, b);
       err = error_of(a, b);
       key = order_key(val);
@@ -512,8 +518,9 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
     const int e = expert_of<TL, LPT>(i, l);
     float s = x[i];
     if constexpr (BIAS) s = fast_sigmoid(s) + bias[i];
-    key[i] = e < E ? order_key(s) : 0u;
-    if (PACKED && e < E) key[i] = (key[i] & 0xffff0000u) | (uint32_t)(0xffff - e);
+    key[i] = order_key(s);
+    if (PACKED) key[i] = (key[i] & 0xffff0000u) | (uint32_t)(0xffff - e);
+    key[i] &= e < E ? ~0u : 0u;  // as a mask: a choice would put each key behind a branch
   }
   int have = E;  // experts to choose from
   if constexpr (GROUPED) {
@@ -540,10 +547,21 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
       }
       const uint64_t chosen = choose_groups<TL, LPT, EPL>(
           q, score, row, shift, E, l, a.wide, group_scores + (size_t)(threadIdx.x / LPT) * E);
+      constexpr int V = Vec<TL>::V;
+      auto mask_of = [&](int i) __attribute__((always_inline)) {
+        const int g = min(group_of(q, expert_of<TL, LPT>(i, l)), 63);
+        return 0u - (uint32_t)((chosen >> g) & 1);
+      };
+      if (a.wide && q.S % V == 0) {  // one group for all values of a load
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const int e = expert_of<TL, LPT>(i, l);
-        if (e < E && !((chosen >> group_of(q, e)) & 1)) key[i] = 0u;
+        for (int c = 0; c < EPL; c += V) {
+          const uint32_t mask = mask_of(c);
+#pragma unroll
+          for (int i = 0; i < V; ++i) key[c + i] &= mask;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) key[i] &= mask_of(i);
       }
     }
   }

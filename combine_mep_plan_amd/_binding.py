@@ -751,7 +751,8 @@ class MepGrads:
     """The gradients of one model as mep_grad_norm and mep_grad_clip take them: a
     mep_grad for each tensor (fp32 or bf16, dense, on one GPU).  ``outs`` are the
     tensors that clipping writes, of the same types and sizes; None: the gradients
-    themselves.  The tensors are kept alive and their memory is used as it was when
+    themselves.  An out overlaps no other tensor of the list (a gradient named twice
+    would be clipped twice over).  The tensors are kept alive and their memory is used as it was when
     this was made, so it serves as long as the gradients stay where they are."""
 
     def __init__(self, grads, outs=None):
@@ -776,6 +777,28 @@ class MepGrads:
             if g.get_device() != self.device or o.get_device() != self.device:
                 raise ValueError(f"MepGrads: tensor {i} is not on GPU {self.device}")
             self.array[i] = MepGrad(data, out, g.numel(), kinds[g.dtype], 0)
+        self._refuse_overlaps()
+
+    def _refuse_overlaps(self):
+        # every memory range once for each tensor that it is, an in-place one as one range
+        ranges = []
+        for i, (g, o) in enumerate(zip(self.grads, self.outs)):
+            if g.numel():
+                a, b, n = g.data_ptr(), o.data_ptr(), g.nbytes
+                ranges.append((b, b + n, i, True))
+                if a != b:
+                    ranges.append((a, a + n, i, False))
+        ranges.sort()
+        # in order of their starts, a range overlaps an earlier one if that reaches into it;
+        # the furthest ends so far of all ranges and of the written ones tell
+        far = far_out = (0, -1)
+        for start, end, i, written in ranges:
+            if start < (far if written else far_out)[0]:
+                j = (far if written else far_out)[1]
+                raise ValueError(f"MepGrads: tensors {min(i, j)} and {max(i, j)} overlap")
+            far = max(far, (end, i))
+            if written:
+                far_out = max(far_out, (end, i))
 
     def __len__(self):
         return len(self.grads)

@@ -39,6 +39,7 @@ int check_grads(const mep_grad* g, int32_t n) {
   if (n > 0 && !g) return MEP_ERR_NULL;
   for (int32_t i = 0; i < n; ++i) {
     if (g[i].dtype != MEP_FP32 && g[i].dtype != MEP_BF16) return MEP_ERR_CONFIG;
+    if (g[i].reserved != 0) return MEP_ERR_CONFIG;
     if (g[i].numel < 0 || g[i].numel > ((int64_t)1 << 44)) return MEP_ERR_SHAPE;
   }
   return MEP_OK;

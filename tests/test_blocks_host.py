@@ -149,6 +149,9 @@ def test_grad_refusals():
     assert lib.mep_grad_clip(a, n, F, 1.0, None) == NULL
     a, n = grads((F, F + 8, 8, 0))
     assert lib.mep_grad_clip(a, n, F, 1.0, None) == ALIGN
+    a, n = grads(ok)
+    a[0].reserved = 1
+    assert lib.mep_grad_norm(a, n, F, F, 1 << 40, None) == lib.mep_grad_clip(a, n, F, 1.0, None) == CONFIG
     for limit in (0.0, -1.0, float("nan")):
         assert lib.mep_grad_clip(*grads(ok), F, limit, None) == CONFIG
     assert lib.mep_grad_clip(*grads((None, None, 0, 0)), F, 1.0, None) == M.MEP_OK  # nothing to do

@@ -124,6 +124,19 @@ def test_forward(T, H, dtype, post, pre):
                        c=1.5, offset=1.0 if pre == "rms" else 0.0, seed=T + H))
 
 
+# more rows than blocks, so that every block takes several, in each way of holding a row
+MANY = [(3200, 72), (3200, 520), (1100, 1048), (1100, 2056), (520, 4104), (270, 8200)]
+
+
+@pytest.mark.parametrize("T,H", MANY)
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("kind,gate", [("rms", "token"), ("layer", "element")])
+def test_many_rows(T, H, dtype, kind, gate):
+    k = Case(T, H, dtype, kind, kind, gate, 1, biases=kind == "layer", seed=H)
+    check_forward(k, codes=H % 128 == 0)
+    check_backward(k)
+
+
 @pytest.mark.parametrize("gate", ["none", "token", "element"])
 @pytest.mark.parametrize("sigmoid", [0, 1])
 @pytest.mark.parametrize("H", [1024, 1536])

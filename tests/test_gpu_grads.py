@@ -214,6 +214,17 @@ def test_lists_that_are_refused():
         M.MepGrads([torch.zeros((4, 4), device="cuda").t()[:2]])
     with pytest.raises(ValueError, match="on the GPU"):
         M.MepGrads([torch.zeros(4)])
+    flat = torch.zeros(64, device="cuda")
+    for grads in ([a, a], [flat[:32], flat[16:48]]):
+        with pytest.raises(ValueError, match="overlap"):
+            M.MepGrads(grads)
+    with pytest.raises(ValueError, match="overlap"):
+        M.MepGrads([flat[:16], flat[32:48]], [flat[48:], flat[:16]])   # an out over another's gradient
+    with pytest.raises(ValueError, match="overlap"):
+        M.MepGrads([flat[:16]], [flat[8:24]])                          # over its own, moved
+    M.MepGrads([flat[:16], flat[:16], flat[8:40]], [torch.zeros_like(t) for t in
+                                                    (flat[:16], flat[:16], flat[8:40])])
+    M.MepGrads([flat[:16], flat[16:32], flat[:0]])                     # neighbours are no overlap
     lst = M.MepGrads([a])
     norm, ws = norm_of(lst)
     with pytest.raises(M.MepError) as e:

@@ -357,8 +357,8 @@ __device__ __forceinline__ int group_rank(uint32_t key, int l, int G) {
 //   Groups that are whole 16-byte units over a power of two of lanes are joined in
 // registers; the others' scores go through LDS (`shared`, E values of the token's own),
 // where a lane takes a whole group.  256 experts in 8 groups, the best 4 by their two
-// best: 16384 tokens 21.1 us, one token 7.3 (15.4 and 5.2 to 5.9 without groups); all
-// groups through LDS and chosen round by round 28.2 and 10.1.
+// best: 16384 tokens 18.8 to 19.9 us, one token 6.2 (15.4 and 5.2 to 5.9 without groups);
+// all groups through LDS and chosen round by round 28.2 and 10.1.
 template <class TL, int LPT, int EPL>
 __device__ __forceinline__ uint64_t choose_groups(const GroupScore& q, const float (&score)[EPL],
                                                   const TL* row, float shift, int E, int l, bool wide,

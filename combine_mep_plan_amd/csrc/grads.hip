@@ -3,6 +3,11 @@
 // The tensors are cut into chunks of 32 KiB; a table of the tensors and of each one's
 // first chunk goes along in the launch's arguments (128 tensors a launch), so that a
 // list of any sizes is one grid of equal pieces of work and needs no memory of its own.
+//
+// Bound by memory: 2.8 GB of gradients (1.4 billion values, nearly all bf16) have their norm
+// in 458 us (6.2 TB/s, loads alone) and are clipped into buffers of their own in 1050 (5.4
+// TB/s).  59 tensors of 1.1 MB together take 8.6 us in three launches, of which calls one by
+// one need 15 on the host.
 #include <algorithm>
 
 #include "dev.h"
@@ -13,9 +18,9 @@ namespace mep {
 namespace {
 
 constexpr int kGradThreads = 256;
-constexpr int kChunkBytes = 32768;
+constexpr int kChunkBytes = 32768;  // 16 KiB: 2.8 GB clipped 0.6% slower
 constexpr uint32_t kGradBlocks = 2048;  // blocks of the norm's launches at most: one sum each
-constexpr uint32_t kClipBlocks = 8192;  // of the clipping's
+constexpr uint32_t kClipBlocks = 8192;  // of the clipping's: 1% faster than 4096, 2% than 2048
 constexpr int kPieces = kChunkBytes / 16 / kGradThreads;  // 16-byte pieces a thread
 
 // The tensor that holds a chunk: the last one that starts at or before it.
@@ -141,6 +146,7 @@ __global__ __launch_bounds__(kGradThreads) void grad_join_kernel(const double* p
   if (threadIdx.x == 0) norm[0] = (float)sqrt(s);
 }
 
+// Stores go past the caches: nothing here reads them again (0.4% at 2.8 GB).
 template <bool BF16>
 __device__ __forceinline__ void clip_chunk(const Chunk& k, float f) {
   over_chunk<BF16>(

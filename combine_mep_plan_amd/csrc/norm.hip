@@ -10,6 +10,14 @@
 // values a thread (a unit; UPT units for long rows), so every byte moves once.  Rows of
 // up to 1024 values belong to one wave, longer ones to a block of just as many waves as
 // they fill; a block works on several rows and keeps the weights in registers.
+//
+// Bound by memory for many rows: 4096 x 7168 in bf16, both norms, a gate a row, rows and E4M3
+// codes out, 49.3 us (265 MB, 5.4 TB/s; a copy reaches 5.1), its gradients 70.1 (352 MB, 5.0
+// TB/s).  What stood in the way was instructions as much as loads: a wave's takes 4 cycles,
+// and 30 a value would be half of that time.  So a norm that subtracts no mean, has no bias
+// and no gate for every value has kernels of its own, its factors are joined before they
+// meet the values, and the vector units are 54% (61%) busy now.  By the launch for few rows:
+// one row of 7168 values 2.9 us, 128 rows 4.1.
 #include <algorithm>
 #include <type_traits>
 

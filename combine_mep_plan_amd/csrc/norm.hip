@@ -469,8 +469,8 @@ void norm_kernel(NormArgs a) {
 // where it is needed: sums of both norms that do not wait for each other share a round.
 // The weights have registers, or lie in LDS where those would not do: 1024 threads leave
 // 128 a thread, and what spills costs as much as the rows (4096 x 7168 with layer norms,
-// biases and a gate for every element 122 us, with all in registers 248; 4096 x 16384
-// without any of these 190 and 345).
+// biases and a gate for every element 131 us, with all in registers 248; 4096 x 16384
+// without any of these 184 and 345).
 //   Each block adds up its rows' share of the column sums in registers and leaves them in
 // a row of `part`; norm_columns_kernel adds those up, in order, so that a result does
 // not depend on timing.
@@ -540,6 +540,7 @@ void norm_backward_kernel(NormBackwardArgs a) {
   load_stream(t, rows[0]);
   load_block(t, rows[0]);
   extern __shared__ float4 weights[];  // IN_LDS: pre weight, post weight, post bias
+  const int slots = UPT * blockDim.x;  // units of each
   float kept[IN_LDS ? 1 : FULL ? 3 : 2][UPT][kUnit];
   if constexpr (IN_LDS) {
     for (int v = 0; v < vectors_in_lds(FULL, a.H); ++v) {
@@ -550,12 +551,11 @@ void norm_backward_kernel(NormBackwardArgs a) {
         raw.load(from, a.H, p.at[u]);
         float w[kUnit];
         raw.widen(v == 2 ? 0.0f : from ? a.offset : 1.0f, w);
-        if (!p.on(u)) continue;
-        float4* to = weights + (int64_t)(v * p.units + p.at[u]) * 2;
+        float4* to = weights + (v * slots + p.at[u]) * 2;
         to[0] = make_float4(w[0], w[1], w[2], w[3]);
         to[1] = make_float4(w[4], w[5], w[6], w[7]);
       }
-    }  // read by the thread that wrote them
+    }  // read by the thread that wrote them, threads past the row's end with numbers too
   } else {
     RawVector raw[FULL ? 3 : 2][UPT];
 #pragma unroll
@@ -581,7 +581,7 @@ void norm_backward_kernel(NormBackwardArgs a) {
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) w[i] = kept[v][u][i];
     } else if (v < vectors_in_lds(FULL, a.H)) {
-      const float4* from = weights + (int64_t)(v * p.units + min(p.at[u], p.units - 1)) * 2;
+      const float4* from = weights + (v * slots + p.at[u]) * 2;
       const float4 lo = from[0], hi = from[1];
       w[0] = lo.x; w[1] = lo.y; w[2] = lo.z; w[3] = lo.w;
       w[4] = hi.x; w[5] = hi.y; w[6] = hi.z; w[7] = hi.w;
@@ -926,7 +926,7 @@ hipError_t launch_block_norm_backward(const NormBackwardArgs& a, hipStream_t s) 
   const int blocks = backward_blocks(r, a.T, full, a.dtype == MEP_BF16);
   if (blocks > 0) {
     const size_t lds = weights_in_lds(r.kind, r.upt, full, a.dtype == MEP_BF16)
-                           ? (size_t)vectors_in_lds(full, a.H) * a.H * sizeof(float)
+                           ? (size_t)vectors_in_lds(full, a.H) * r.upt * r.threads * kUnit * sizeof(float)
                            : 0;
     by_shape(r, [&](auto upt, auto kind) {
       by_type(a.dtype, full, [&](auto type, auto f) {

@@ -407,10 +407,11 @@ int mep_gate(const mep_gate_config *cfg, const void *logits, const float *bias, 
  *   MEP_GROUP_TOP2   the sum of the two largest (the largest where that is +inf).
  * Groups are chosen in the order of these scores' 64-bit values (MEP_GROUP_MAX
  * without a bias: in the logits' order), equal ones the lower first; a NaN among the
- * scores counts as -inf there, and a logit of +inf puts its group first.  Within the chosen groups everything is as in
- * mep_gate, and so is the gradient (mep_gate_backward).  num_groups: 1..64, divides
- * E; top_groups: 1..num_groups; k at most the chosen groups' experts; for
- * MEP_GROUP_TOP2 two experts a group at least (MEP_ERR_CONFIG otherwise).
+ * scores counts as -inf there, and a logit of +inf puts its group first.  Within the
+ * chosen groups everything is as in mep_gate, and so is the gradient
+ * (mep_gate_backward).  num_groups: 1..64, divides E; top_groups: 1..num_groups; k at
+ * most the chosen groups' experts; for MEP_GROUP_TOP2 two experts a group at least
+ * (MEP_ERR_CONFIG otherwise).
  */
 int mep_gate_grouped(const mep_gate_config *cfg, int32_t num_groups, int32_t top_groups,
                      int32_t group_score, const void *logits, const float *bias, int32_t T,
@@ -580,7 +581,8 @@ int mep_block_norm(const mep_norm_config *cfg, const void *x, const void *y, con
  * Results do not depend on timing.  workspace: mep_block_norm_workspace_bytes(cfg, T)
  * bytes (0 if cfg or T is invalid), of any content; it serves one call at a time.
  * grad_x may be grad_s itself and grad_y may be y itself; other outputs overlap
- * nothing.  0 <= T <= 2^26; the sums over no rows are 0.
+ * nothing.  0 <= T <= 2^26; the sums over no rows are 0.  Every row counts in the column
+ * sums: padding among the T rows has to be finite and its gradients 0.
  */
 size_t mep_block_norm_workspace_bytes(const mep_norm_config *cfg, int32_t T);
 int mep_block_norm_backward(const mep_norm_config *cfg, const void *grad_s, const void *grad_n,

@@ -330,6 +330,18 @@ def test_gradients_are_the_definitions(post, pre, gate):
     assert abs(float(up - down) / (2 * h) - slope) <= 1e-5 * size + 1e-8 * float(gn.abs().sum())
 
 
+@pytest.mark.parametrize("H", [2056, 4104, 8200])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_threads_past_the_row_hold_no_weights(kind, H):
+    # NaN weights of a longer row before it: what they leave in LDS reaches no sum
+    left = Case(300, 16384 if H > 8192 else 8192, "bf16", kind, kind, biases=True, seed=1)
+    for w in (left.wp, left.wn, left.bp):
+        w.fill_(float("nan"))
+    for _ in range(3):
+        left.backward(left.x)
+        check_backward(Case(300, H, "bf16", kind, kind, "token", 1, seed=H))
+
+
 def test_results_repeat():
     k = Case(2000, 1536, "bf16", "rms", "rms", "token", 1, seed=5)
     a, b = k.backward(k.x), k.backward(k.x)

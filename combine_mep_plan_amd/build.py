@@ -9,10 +9,12 @@ disabled in the device pass.
 
 from __future__ import annotations
 
+import concurrent.futures
 import glob
 import os
 import subprocess
 import sys
+import tempfile
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -27,7 +29,6 @@ FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     "-ffp-contract=off",
     "-fno-fast-math",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -41,9 +42,8 @@ def sources() -> list[str]:
         sorted(glob.glob(os.path.join(CSRC, "*.cpp")))
 
 
-def build(verbose: bool = False) -> str:
-    tmp = LIB + ".tmp"
-    cmd = [HIPCC, *FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC, *sources(), "-o", tmp]
+def _hipcc(args: list[str], verbose: bool) -> None:
+    cmd = [HIPCC, *FLAGS, *args]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -54,6 +54,18 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"hipcc failed ({r.returncode}):\n{err}")
     if err.strip() and verbose:
         print(err, file=sys.stderr)
+
+
+def build(verbose: bool = False) -> str:
+    """Compiles every source, several at a time, and links them."""
+    tmp = LIB + ".tmp"
+    with tempfile.TemporaryDirectory() as objects:
+        jobs = [(src, os.path.join(objects, os.path.basename(src) + ".o")) for src in sources()]
+        workers = min(8, len(os.sched_getaffinity(0)), len(jobs))
+        with concurrent.futures.ThreadPoolExecutor(workers) as pool:
+            list(pool.map(lambda j: _hipcc(["-I", os.path.join(ROOT, "include"), "-I", CSRC, "-c",
+                                            j[0], "-o", j[1]], verbose), jobs))
+        _hipcc(["-shared", *(o for _, o in jobs), "-o", tmp], verbose)
     os.replace(tmp, LIB)
     return LIB
 

@@ -236,6 +236,13 @@ struct Place {
   __device__ __forceinline__ bool on(int u) const { return at[u] < units; }
 };
 
+// What a kernel has registers and instructions for: norms without a mean and one factor a
+// row; layer norms too; biases, their gradients and a gate for every element too.  Layer
+// norms in kernels of their own and in those for everything, with one factor a row (us):
+// 4096 x 7168 bf16 forward 44.9 and 51.5, gradients 88.8 and 108.9, in fp32 165 and 249,
+// gradients of 4096 x 16384 bf16 239 and 690.  RMS norms take 43.1, 70.5, 153 and 184.
+constexpr int kPlain = 0, kMeans = 1, kAll = 2;
+
 // Threads that kernels are built for: four rows of a wave each, or one row of up to 512
 // or 1024 threads (which leave a thread 256 or 128 registers).
 constexpr int kWaveRows = 0, kHalfBlock = 512, kBlock = 1024;
@@ -265,32 +272,34 @@ __device__ __forceinline__ u32x2 encode_unit(const float (&v)[kUnit], float& sca
   return u32x2{pack_e4m3x4(q[0], q[1], q[2], q[3]), pack_e4m3x4(q[4], q[5], q[6], q[7])};
 }
 
-// Waves a SIMD that a forward kernel of bf16 rows is kept to.  8 without FULL, so that two
-// blocks of 14 waves (7168 columns) share a CU, whose first SIMD then holds 8 waves: 4096
-// rows with E4M3 codes too take 49.4 us (5.4 TB/s), an earlier state of the kernel 58 where
-// one block had the CU 64 to 70.  6 for half blocks with FULL: 4096 x 2056 20.6 us, 25.6
-// with 5; not for whole blocks, of which one has the CU either way (4096 x 7168 55.0, 56.6).
-constexpr int forward_waves(int rows, int upt, bool full, bool bf16) {
+// Waves a SIMD that a forward kernel of bf16 rows is kept to.  8 for whole blocks without
+// biases or a gate for every element, so that two blocks of 14 waves (7168 columns) share a
+// CU, whose first SIMD then holds 8 waves: 4096 rows with E4M3 codes too take 49.4 us (5.4
+// TB/s), an earlier state of the kernel 58 where one block had the CU 64 to 70; with layer
+// norms 44.9 us without codes, 51.8 where one has it (few enough vector registers alone do
+// not do it).  6 for half blocks with everything: 4096 x 2056 20.6 us, 25.6 with 5; not for
+// whole blocks, of which one has the CU either way (4096 x 7168 55.0, 56.6).
+constexpr int forward_waves(int rows, int upt, int what, bool bf16) {
   if (rows == kWaveRows || upt > 1 || !bf16) return 1;
-  return rows == kHalfBlock ? full ? 6 : 1 : full ? 1 : 8;
+  if (what == kAll) return rows == kHalfBlock ? 6 : 1;
+  return rows == kBlock ? 8 : 1;
 }
 
-// FULL: with biases, layer norms or a gate for every element, which take registers and
-// instructions of their own.
-template <class TL, int UPT, int ROWS, bool FULL>
-__global__ __launch_bounds__(most_threads(ROWS), forward_waves(ROWS, UPT, FULL, sizeof(TL) == 2))
+template <class TL, int UPT, int ROWS, int WHAT>
+__global__ __launch_bounds__(most_threads(ROWS), forward_waves(ROWS, UPT, WHAT, sizeof(TL) == 2))
 void norm_kernel(NormArgs a) {
-  constexpr bool WAVE = ROWS == kWaveRows;
+  constexpr bool WAVE = ROWS == kWaveRows, MEANS = WHAT != kPlain, ALL = WHAT == kAll;
   __shared__ float4 lds[2][kMaxWaves];
   const Place<UPT, WAVE> p(a.H);
   const float inv_h = 1.0f / (float)a.H;
   RowSum<WAVE> sum{lds, 0, (int)blockDim.x / kWave};
-  const bool by_element = FULL && a.gate_kind == MEP_BLOCK_GATE_ELEMENT;
+  const bool by_element = ALL && a.gate_kind == MEP_BLOCK_GATE_ELEMENT;
   const bool by_token = a.gate_kind == MEP_BLOCK_GATE_TOKEN;
-  const bool post_layer = FULL && a.post == MEP_NORM_LAYER, pre_layer = FULL && a.pre == MEP_NORM_LAYER;
+  const bool post_layer = MEANS && a.post == MEP_NORM_LAYER;
+  const bool pre_layer = MEANS && a.pre == MEP_NORM_LAYER;
   // A row as it lies in memory; the next one's loads run while this one is worked on.
   struct Row {
-    Raw<TL> x[UPT], y[UPT], gate[FULL ? UPT : 1];
+    Raw<TL> x[UPT], y[UPT], gate[ALL ? UPT : 1];
     float g;
   };
   const int bytes = a.H * (int)sizeof(TL);
@@ -304,7 +313,7 @@ void norm_kernel(NormArgs a) {
 #pragma unroll
       for (int u = 0; u < UPT; ++u) r.x[u].load(x, p.at[u]);
     }
-    if constexpr (FULL)
+    if constexpr (ALL)
       if (by_element) {
 #pragma unroll
         for (int u = 0; u < UPT; ++u) r.gate[u].load(gate, p.at[u]);
@@ -317,14 +326,14 @@ void norm_kernel(NormArgs a) {
   if (t >= a.T) return;
   load(t, now);
   float wp[UPT][kUnit], wn[UPT][kUnit];
-  float bp[FULL ? UPT : 1][kUnit], bn[FULL ? UPT : 1][kUnit];
+  float bp[ALL ? UPT : 1][kUnit], bn[ALL ? UPT : 1][kUnit];
   {
-    RawVector post_w[UPT], pre_w[UPT], post_b[FULL ? UPT : 1], pre_b[FULL ? UPT : 1];
+    RawVector post_w[UPT], pre_w[UPT], post_b[ALL ? UPT : 1], pre_b[ALL ? UPT : 1];
 #pragma unroll
     for (int u = 0; u < UPT; ++u) {
       post_w[u].load(a.post_weight, a.H, p.at[u]);
       pre_w[u].load(a.pre_weight, a.H, p.at[u]);
-      if constexpr (FULL) {
+      if constexpr (ALL) {
         post_b[u].load(a.post_bias, a.H, p.at[u]);
         pre_b[u].load(a.pre_bias, a.H, p.at[u]);
       }
@@ -333,7 +342,7 @@ void norm_kernel(NormArgs a) {
     for (int u = 0; u < UPT; ++u) {
       post_w[u].widen(a.post_weight ? a.offset : 1.0f, wp[u]);
       pre_w[u].widen(a.pre_weight ? a.offset : 1.0f, wn[u]);
-      if constexpr (FULL) {
+      if constexpr (ALL) {
         post_b[u].widen(0.0f, bp[u]);
         pre_b[u].widen(0.0f, bn[u]);
       }
@@ -358,10 +367,10 @@ void norm_kernel(NormArgs a) {
         float q[1] = {0.0f};
 #pragma unroll
         for (int u = 0; u < UPT; ++u)
-          if (!FULL || p.on(u))
+          if (!MEANS || p.on(u))
 #pragma unroll
             for (int i = 0; i < kUnit; ++i) {
-              const float d = FULL ? now.y[u].at(i) - mean : now.y[u].at(i);
+              const float d = MEANS ? now.y[u].at(i) - mean : now.y[u].at(i);
               q[0] = fmaf(d, d, q[0]);
             }
         sum(q);
@@ -377,14 +386,15 @@ void norm_kernel(NormArgs a) {
       for (int u = 0; u < UPT; ++u)
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) {
-          if constexpr (FULL) v[u][i] = fmaf((now.y[u].at(i) - mean) * r, wp[u][i], bp[u][i]) * c;
+          if constexpr (ALL) v[u][i] = fmaf((now.y[u].at(i) - mean) * r, wp[u][i], bp[u][i]) * c;
+          else if constexpr (MEANS) v[u][i] = (now.y[u].at(i) - mean) * (r * c) * wp[u][i];
           else v[u][i] = now.y[u].at(i) * (r * c) * wp[u][i];
         }
       if (by_element) {
 #pragma unroll
         for (int u = 0; u < UPT; ++u) {
           float g[kUnit], f[kUnit], slope[kUnit];
-          now.gate[FULL ? u : 0].widen(g);
+          now.gate[ALL ? u : 0].widen(g);
           open_gate(g, a.sigmoid, f, slope);
 #pragma unroll
           for (int i = 0; i < kUnit; ++i) v[u][i] *= f[i];
@@ -423,10 +433,10 @@ void norm_kernel(NormArgs a) {
         float q[1] = {0.0f};
 #pragma unroll
         for (int u = 0; u < UPT; ++u)
-          if (!FULL || p.on(u))
+          if (!MEANS || p.on(u))
 #pragma unroll
             for (int i = 0; i < kUnit; ++i) {
-              const float d = FULL ? v[u][i] - mean : v[u][i];
+              const float d = MEANS ? v[u][i] - mean : v[u][i];
               q[0] = fmaf(d, d, q[0]);
             }
         sum(q);
@@ -436,7 +446,8 @@ void norm_kernel(NormArgs a) {
       for (int u = 0; u < UPT; ++u)
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) {
-          if constexpr (FULL) v[u][i] = fmaf((v[u][i] - mean) * r, wn[u][i], bn[u][i]);
+          if constexpr (ALL) v[u][i] = fmaf((v[u][i] - mean) * r, wn[u][i], bn[u][i]);
+          else if constexpr (MEANS) v[u][i] = (v[u][i] - mean) * r * wn[u][i];
           else v[u][i] = v[u][i] * r * wn[u][i];
         }
       if (a.n) {
@@ -474,29 +485,29 @@ void norm_kernel(NormArgs a) {
 //   Each block adds up its rows' share of the column sums in registers and leaves them in
 // a row of `part`; norm_columns_kernel adds those up, in order, so that a result does
 // not depend on timing.
-constexpr bool weights_in_lds(int rows, int upt, bool full, bool bf16) {
-  return rows == kBlock ? full || upt > 1 : rows == kHalfBlock && full && bf16;
+constexpr bool weights_in_lds(int rows, int upt, bool all, bool bf16) {
+  return rows == kBlock ? all || upt > 1 : rows == kHalfBlock && all && bf16;
 }
 // Half blocks kept to 128 registers, so that 4 waves a SIMD fit whatever the block's
-// waves: all but those of fp32 rows with all of it, which would spill (4096 x 2056 90 us,
+// waves: all but those of fp32 rows with everything, which would spill (4096 x 2056 90 us,
 // in 128 registers 101).
-constexpr bool packed_halves(int rows, bool full, bool bf16) {
-  return rows == kHalfBlock && (!full || bf16);
+constexpr bool packed_halves(int rows, bool all, bool bf16) {
+  return rows == kHalfBlock && (!all || bf16);
 }
 constexpr int kLdsRow = 8192;  // values of a row of which three vectors fit LDS, else two
-__host__ __device__ constexpr int vectors_in_lds(bool full, int H) {
-  return full && H <= kLdsRow ? 3 : 2;
+__host__ __device__ constexpr int vectors_in_lds(bool all, int H) {
+  return all && H <= kLdsRow ? 3 : 2;
 }
 
-template <class TL, int UPT, int ROWS, bool FULL>
-__global__ __launch_bounds__(most_threads(ROWS), packed_halves(ROWS, FULL, sizeof(TL) == 2) ? 4 : 1)
+template <class TL, int UPT, int ROWS, int WHAT>
+__global__ __launch_bounds__(most_threads(ROWS), packed_halves(ROWS, WHAT == kAll, sizeof(TL) == 2) ? 4 : 1)
 void norm_backward_kernel(NormBackwardArgs a) {
-  constexpr bool WAVE = ROWS == kWaveRows;
+  constexpr bool WAVE = ROWS == kWaveRows, MEANS = WHAT != kPlain, ALL = WHAT == kAll;
   __shared__ float4 lds[2][kMaxWaves];
-  constexpr int COLS = FULL ? 4 : 2;  // post weight, pre weight, their biases
+  constexpr int COLS = ALL ? 4 : 2;  // post weight, pre weight, their biases
   // Rows whose loads have registers, and whether the weights have (else they lie in LDS,
   // as far as that holds them).
-  constexpr bool IN_LDS = weights_in_lds(ROWS, UPT, FULL, sizeof(TL) == 2);
+  constexpr bool IN_LDS = weights_in_lds(ROWS, UPT, ALL, sizeof(TL) == 2);
   constexpr int AHEAD = sizeof(TL) == 2 && !IN_LDS ? 2 : 1;
   const Place<UPT, WAVE> p(a.H);
   const float inv_h = 1.0f / (float)a.H;
@@ -508,11 +519,11 @@ void norm_backward_kernel(NormBackwardArgs a) {
     for (int u = 0; u < UPT; ++u)
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) acc[c][u][i] = 0.0f;
-  const bool by_element = FULL && a.gate_kind == MEP_BLOCK_GATE_ELEMENT;
+  const bool by_element = ALL && a.gate_kind == MEP_BLOCK_GATE_ELEMENT;
   const bool by_token = a.gate_kind == MEP_BLOCK_GATE_TOKEN;
   const int pre = a.grad_n ? a.pre : MEP_NORM_NONE, post = a.y ? a.post : MEP_NORM_NONE;
   struct Row {
-    Raw<TL> gs[UPT], gn[UPT], s[UPT], y[UPT], gate[FULL ? UPT : 1];
+    Raw<TL> gs[UPT], gn[UPT], s[UPT], y[UPT], gate[ALL ? UPT : 1];
     float g;
   };
   const int bytes = a.H * (int)sizeof(TL);
@@ -531,7 +542,7 @@ void norm_backward_kernel(NormBackwardArgs a) {
 #pragma unroll
     for (int u = 0; u < UPT; ++u) {
       r.y[u].load(y, p.at[u]);
-      if constexpr (FULL) r.gate[u].load(gate, p.at[u]);
+      if constexpr (ALL) r.gate[u].load(gate, p.at[u]);
     }
     r.g = load_token(by_token ? a.gate : nullptr, t, a.T);
   };
@@ -541,9 +552,9 @@ void norm_backward_kernel(NormBackwardArgs a) {
   load_block(t, rows[0]);
   extern __shared__ float4 weights[];  // IN_LDS: pre weight, post weight, post bias
   const int slots = UPT * blockDim.x;  // units of each
-  float kept[IN_LDS ? 1 : FULL ? 3 : 2][UPT][kUnit];
+  float kept[IN_LDS ? 1 : ALL ? 3 : 2][UPT][kUnit];
   if constexpr (IN_LDS) {
-    for (int v = 0; v < vectors_in_lds(FULL, a.H); ++v) {
+    for (int v = 0; v < vectors_in_lds(ALL, a.H); ++v) {
       const float* from = v == 0 ? a.pre_weight : v == 1 ? a.post_weight : a.post_bias;
 #pragma unroll
       for (int u = 0; u < UPT; ++u) {
@@ -557,12 +568,12 @@ void norm_backward_kernel(NormBackwardArgs a) {
       }
     }  // read by the thread that wrote them, threads past the row's end with numbers too
   } else {
-    RawVector raw[FULL ? 3 : 2][UPT];
+    RawVector raw[ALL ? 3 : 2][UPT];
 #pragma unroll
     for (int u = 0; u < UPT; ++u) {
       raw[0][u].load(a.pre_weight, a.H, p.at[u]);
       raw[1][u].load(a.post_weight, a.H, p.at[u]);
-      if constexpr (FULL) raw[2][u].load(a.post_bias, a.H, p.at[u]);
+      if constexpr (ALL) raw[2][u].load(a.post_bias, a.H, p.at[u]);
     }
     if constexpr (AHEAD == 2) {
       load_stream(t + p.step, rows[1]);
@@ -572,7 +583,7 @@ void norm_backward_kernel(NormBackwardArgs a) {
     for (int u = 0; u < UPT; ++u) {
       raw[0][u].widen(a.pre_weight ? a.offset : 1.0f, kept[0][u]);
       raw[1][u].widen(a.post_weight ? a.offset : 1.0f, kept[1][u]);
-      if constexpr (FULL) raw[2][u].widen(0.0f, kept[2][u]);
+      if constexpr (ALL) raw[2][u].widen(0.0f, kept[2][u]);
     }
   }
   // a vector's values at a unit, in the order above
@@ -580,7 +591,7 @@ void norm_backward_kernel(NormBackwardArgs a) {
     if constexpr (!IN_LDS) {
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) w[i] = kept[v][u][i];
-    } else if (v < vectors_in_lds(FULL, a.H)) {
+    } else if (v < vectors_in_lds(ALL, a.H)) {
       const float4* from = weights + (v * slots + p.at[u]) * 2;
       const float4 lo = from[0], hi = from[1];
       w[0] = lo.x; w[1] = lo.y; w[2] = lo.z; w[3] = lo.w;
@@ -604,7 +615,7 @@ void norm_backward_kernel(NormBackwardArgs a) {
     const int64_t then = t + AHEAD * p.step;
     // the means of both norms' rows, and of the next norm's gradient
     float mean_s = 0.0f, r_s = 1.0f, mean_n = 0.0f, along_n = 0.0f, mean_y = 0.0f, r_y = 1.0f;
-    if (FULL && (pre == MEP_NORM_LAYER || post == MEP_NORM_LAYER)) {
+    if (MEANS && (pre == MEP_NORM_LAYER || post == MEP_NORM_LAYER)) {
       float q[3] = {0.0f, 0.0f, 0.0f};  // what lies past the row's end is 0
 #pragma unroll
       for (int u = 0; u < UPT; ++u) {
@@ -632,11 +643,11 @@ void norm_backward_kernel(NormBackwardArgs a) {
       for (int u = 0; u < UPT; ++u) {
         float wn[kUnit];
         vector(0, u, wn);
-        if (!FULL || p.on(u))
+        if (!MEANS || p.on(u))
 #pragma unroll
           for (int i = 0; i < kUnit; ++i) {
-            const float s = FULL ? now.s[u].at(i) - mean_s : now.s[u].at(i);
-            const float y = FULL ? now.y[u].at(i) - mean_y : now.y[u].at(i);
+            const float s = MEANS ? now.s[u].at(i) - mean_s : now.s[u].at(i);
+            const float y = MEANS ? now.y[u].at(i) - mean_y : now.y[u].at(i);
             q[0] = fmaf(s, s, q[0]);
             q[1] = fmaf(s, now.gn[u].at(i) * wn[i], q[1]);
             q[2] = fmaf(y, y, q[2]);
@@ -660,11 +671,11 @@ void norm_backward_kernel(NormBackwardArgs a) {
       for (int i = 0; i < kUnit; ++i) {
         float g = now.gs[u].at(i);  // 0 without grad_s; without grad_n, s and gn are 0
         const float gn = now.gn[u].at(i);
-        const float h = FULL ? (now.s[u].at(i) - mean_s) * r_s : now.s[u].at(i) * r_s;
-        const float off = FULL ? fmaf(h, along_n, mean_n) : h * along_n;
+        const float h = MEANS ? (now.s[u].at(i) - mean_s) * r_s : now.s[u].at(i) * r_s;
+        const float off = MEANS ? fmaf(h, along_n, mean_n) : h * along_n;
         g = fmaf(r_s, fmaf(gn, wn[i], -off), g);
         acc[1][u][i] = fmaf(gn, h, acc[1][u][i]);
-        if constexpr (FULL) acc[3][u][i] += gn;
+        if constexpr (ALL) acc[3][u][i] += gn;
         grad[u][i] = g;
       }
     }
@@ -685,7 +696,7 @@ void norm_backward_kernel(NormBackwardArgs a) {
     auto factors = [&](int u, float(&f)[kUnit], float(&slope)[kUnit]) __attribute__((always_inline)) {
       if (by_element) {
         float g[kUnit];
-        now.gate[FULL ? u : 0].widen(g);
+        now.gate[ALL ? u : 0].widen(g);
         open_gate(g, a.sigmoid, f, slope);
       } else {
 #pragma unroll
@@ -695,36 +706,39 @@ void norm_backward_kernel(NormBackwardArgs a) {
     const bool token_grad = by_token && a.grad_gate;
     float mean_v = 0.0f, along_y = 0.0f, of_row = 0.0f;
     if (post != MEP_NORM_NONE || token_grad) {
-      float q[FULL ? 3 : 1] = {0.0f};
+      float q[ALL ? 3 : MEANS ? 2 : 1] = {0.0f};
 #pragma unroll
       for (int u = 0; u < UPT; ++u) {
         float wp[kUnit], bp[kUnit], f[kUnit], slope[kUnit];
         vector(1, u, wp);
-        if constexpr (FULL) {
+        if constexpr (ALL) {
           vector(2, u, bp);
           factors(u, f, slope);
         }
-        if (!FULL || p.on(u))
+        if (!MEANS || p.on(u))
 #pragma unroll
           for (int i = 0; i < kUnit; ++i) {
-            if constexpr (FULL) {
+            if constexpr (ALL) {
               const float h = (now.y[u].at(i) - mean_y) * r_y;
               const float g = f[i] * grad[u][i] * wp[i];
               q[0] = fmaf(g, h, q[0]);
               q[1] += g;
               q[2] = fmaf(grad[u][i], bp[i], q[2]);
+            } else if constexpr (MEANS) {
+              const float g = grad[u][i] * wp[i];
+              q[0] = fmaf(g, (now.y[u].at(i) - mean_y) * r_y, q[0]);
+              q[1] += g;
             } else {
               q[0] = fmaf(grad[u][i] * wp[i], now.y[u].at(i), q[0]);
             }
           }
       }
       sum(q);
-      if constexpr (!FULL) q[0] *= r_y;
+      if constexpr (!MEANS) q[0] *= r_y;
       if (post != MEP_NORM_NONE) along_y = c * q[0] * inv_h;
-      if constexpr (FULL) {
+      if constexpr (MEANS)
         if (post == MEP_NORM_LAYER) mean_v = c * q[1] * inv_h;
-        q[0] += q[2];
-      }
+      if constexpr (ALL) q[0] += q[2];
       of_row = a.block_scale * q[0] * slope_row[0];  // a gate a row: sum of grad v
 #pragma unroll
       for (int u = 0; u < UPT; ++u) now.y[u].hold();
@@ -735,13 +749,13 @@ void norm_backward_kernel(NormBackwardArgs a) {
     for (int u = 0; u < UPT; ++u) {
       float back[kUnit], of_gate[kUnit], wp[kUnit], bp[kUnit], f[kUnit], slope[kUnit];
       vector(1, u, wp);
-      if constexpr (FULL) {
+      if constexpr (ALL) {
         vector(2, u, bp);
         factors(u, f, slope);
       }
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) {
-        if constexpr (FULL) {
+        if constexpr (ALL) {
           const float h = (now.y[u].at(i) - mean_y) * r_y;
           const float gv = c * f[i] * grad[u][i];
           acc[0][u][i] = fmaf(gv, h, acc[0][u][i]);
@@ -749,13 +763,14 @@ void norm_backward_kernel(NormBackwardArgs a) {
           back[i] = r_y * fmaf(gv, wp[i], -fmaf(h, along_y, mean_v));
           of_gate[i] = a.block_scale * slope[i] * grad[u][i] * fmaf(h, wp[i], bp[i]);
         } else {
-          const float h = now.y[u].at(i) * r_y, gv = c * grad[u][i];
+          const float h = MEANS ? (now.y[u].at(i) - mean_y) * r_y : now.y[u].at(i) * r_y;
+          const float gv = c * grad[u][i];
           acc[0][u][i] = fmaf(gv, h, acc[0][u][i]);
-          back[i] = r_y * fmaf(gv, wp[i], -(h * along_y));
+          back[i] = r_y * fmaf(gv, wp[i], -(MEANS ? fmaf(h, along_y, mean_v) : h * along_y));
         }
       }
       store_unit((TL*)nullptr, grad_y, p.at[u], back);
-      if constexpr (FULL) store_unit((TL*)nullptr, grad_gate, p.at[u], of_gate);
+      if constexpr (ALL) store_unit((TL*)nullptr, grad_gate, p.at[u], of_gate);
     }
     const RowBuffer row_gate(token_grad ? a.grad_gate : nullptr, t, a.T, 4);
     __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(of_row), row_gate.r, p.lane * 4, 0, 0);
@@ -869,14 +884,21 @@ void by_shape(const RowShape& r, F f) {
   }
 }
 
-// Calls f(a value of the rows' type, full).
+// Calls f(a value of the rows' type, what).
 template <class F>
-void by_type(int dtype, bool full, F f) {
-  if (dtype == MEP_BF16) {
-    if (full) f(uint16_t{}, std::true_type{}); else f(uint16_t{}, std::false_type{});
-  } else {
-    if (full) f(float{}, std::true_type{}); else f(float{}, std::false_type{});
-  }
+void by_type(int dtype, int what, F f) {
+  using std::integral_constant;
+  auto of = [&](auto type) {
+    if (what == kPlain) f(type, integral_constant<int, kPlain>{});
+    else if (what == kMeans) f(type, integral_constant<int, kMeans>{});
+    else f(type, integral_constant<int, kAll>{});
+  };
+  if (dtype == MEP_BF16) of(uint16_t{});
+  else of(float{});
+}
+
+int what_of(bool all, int post, int pre) {
+  return all ? kAll : post == MEP_NORM_LAYER || pre == MEP_NORM_LAYER ? kMeans : kPlain;
 }
 
 int blocks_for(const RowShape& r, int32_t T, int most) {
@@ -888,20 +910,19 @@ int blocks_for(const RowShape& r, int32_t T, int most) {
 hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) {
   if (a.T == 0) return hipSuccess;
   const RowShape r = row_shape(a.H);
-  const bool full = a.post_bias || a.pre_bias || a.gate_kind == MEP_BLOCK_GATE_ELEMENT ||
-                    a.post == MEP_NORM_LAYER || a.pre == MEP_NORM_LAYER;
+  const bool all = a.post_bias || a.pre_bias || a.gate_kind == MEP_BLOCK_GATE_ELEMENT;
   const bool bf16 = a.dtype == MEP_BF16;
   // Blocks that the CUs hold at once and no more, as each loads the weights.  4096 rows
   // with 256, 512, 1024 blocks (us): 7168 bf16 columns 44.4, 43.3, 48.7, with layer norms,
   // biases and a gate for every element 60.5, 62.1, 67.1; 2056 columns 22.0, 17.5, 15.3, in
   // fp32 with all of it 40.0, 38.0, 45.0; 512 by wave 5.3, 4.5, 4.5 (768: 4.2).
   const int most = r.kind == kWaveRows ? 768
-                   : r.kind == kBlock && (full || !bf16 || r.upt > 1) ? 256
+                   : r.kind == kBlock && (all || !bf16 || r.upt > 1) ? 256
                    : bf16 && r.threads <= 384 ? 1024 : 512;
   const int blocks = blocks_for(r, a.T, most);
   by_shape(r, [&](auto upt, auto kind) {
-    by_type(a.dtype, full, [&](auto type, auto f) {
-      norm_kernel<decltype(type), upt(), kind(), f()><<<blocks, r.threads, 0, s>>>(a);
+    by_type(a.dtype, what_of(all, a.post, a.pre), [&](auto type, auto what) {
+      norm_kernel<decltype(type), upt(), kind(), what()><<<blocks, r.threads, 0, s>>>(a);
     });
   });
   return hipGetLastError();
@@ -910,8 +931,8 @@ hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) {
 // Blocks of the gradients' launch, each of which leaves a row of partial sums: one a CU,
 // two where they fit.  4096 rows with 256 and 512 blocks (us): 2056 bf16 columns 42 and
 // 34, all of it in fp32 90 and 95, 7168 bf16 columns 72 and 80, 512 columns by wave 19 and 24.
-static int backward_blocks(const RowShape& r, int32_t T, bool full, bool bf16) {
-  return blocks_for(r, T, packed_halves(r.kind, full, bf16) ? 512 : 256);
+static int backward_blocks(const RowShape& r, int32_t T, bool all, bool bf16) {
+  return blocks_for(r, T, packed_halves(r.kind, all, bf16) ? 512 : 256);
 }
 
 int norm_backward_blocks(int32_t H, int32_t T) {  // the most of all
@@ -920,17 +941,16 @@ int norm_backward_blocks(int32_t H, int32_t T) {  // the most of all
 
 hipError_t launch_block_norm_backward(const NormBackwardArgs& a, hipStream_t s) {
   const RowShape r = row_shape(a.H);
-  const bool full = a.columns[1] || a.columns[3] || a.post_bias ||
-                    a.gate_kind == MEP_BLOCK_GATE_ELEMENT || a.post == MEP_NORM_LAYER ||
-                    a.pre == MEP_NORM_LAYER;
-  const int blocks = backward_blocks(r, a.T, full, a.dtype == MEP_BF16);
+  const bool all = a.columns[1] || a.columns[3] || a.post_bias ||
+                   a.gate_kind == MEP_BLOCK_GATE_ELEMENT;
+  const int blocks = backward_blocks(r, a.T, all, a.dtype == MEP_BF16);
   if (blocks > 0) {
-    const size_t lds = weights_in_lds(r.kind, r.upt, full, a.dtype == MEP_BF16)
-                           ? (size_t)vectors_in_lds(full, a.H) * r.upt * r.threads * kUnit * sizeof(float)
+    const size_t lds = weights_in_lds(r.kind, r.upt, all, a.dtype == MEP_BF16)
+                           ? (size_t)vectors_in_lds(all, a.H) * r.upt * r.threads * kUnit * sizeof(float)
                            : 0;
     by_shape(r, [&](auto upt, auto kind) {
-      by_type(a.dtype, full, [&](auto type, auto f) {
-        norm_backward_kernel<decltype(type), upt(), kind(), f()><<<blocks, r.threads, lds, s>>>(a);
+      by_type(a.dtype, what_of(all, a.post, a.pre), [&](auto type, auto what) {
+        norm_backward_kernel<decltype(type), upt(), kind(), what()><<<blocks, r.threads, lds, s>>>(a);
       });
     });
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;

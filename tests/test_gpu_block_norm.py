@@ -137,6 +137,19 @@ def test_many_rows(T, H, dtype, kind, gate):
     check_backward(k)
 
 
+# layer norms without biases or a gate for every element, and no gradients of biases, have
+# kernels of their own
+@pytest.mark.parametrize("T,H", SIZES + MANY)
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("post,pre", [("layer", "layer"), ("rms", "layer"), ("layer", "rms"),
+                                      ("none", "layer"), ("layer", "none")])
+def test_layer_norms_without_biases(T, H, dtype, post, pre):
+    k = Case(T, H, dtype, post, pre, ("token", "none")[(T + H // 8) % 2], sigmoid=T % 2,
+             weights=H % 3 != 0, a=0.5, c=1.5, offset=1.0 if pre == "rms" else 0.0, seed=T + H, mean=2.0)
+    check_forward(k, codes=H % 128 == 0 and pre != "none")
+    check_backward(k, ("x", "y", "gate", "post_weight", "pre_weight"))
+
+
 @pytest.mark.parametrize("gate", ["none", "token", "element"])
 @pytest.mark.parametrize("sigmoid", [0, 1])
 @pytest.mark.parametrize("H", [1024, 1536])

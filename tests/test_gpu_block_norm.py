@@ -150,6 +150,20 @@ def test_layer_norms_without_biases(T, H, dtype, post, pre):
     check_backward(k, ("x", "y", "gate", "post_weight", "pre_weight"))
 
 
+@pytest.mark.parametrize("H", [264, 2056, 4104, 8200])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("without", ["gs", "gn", "y", "weights"])
+def test_layer_norms_of_parts(H, dtype, without):
+    k = Case(40, H, dtype, "layer", "layer", "none" if without == "y" else "token", 1,
+             y=without != "y", weights=without != "weights", seed=H, mean=-1.0)
+    check_forward(k)
+    if without in ("gs", "gn"):
+        setattr(k, without, None)
+    whole, _, _ = check_backward(k, ("x", "y", "gate", "post_weight", "pre_weight"))
+    some, _, _ = check_backward(k, ("y", "pre_weight"))
+    assert all(torch.equal(t, whole[n]) for n, t in some.items())
+
+
 @pytest.mark.parametrize("gate", ["none", "token", "element"])
 @pytest.mark.parametrize("sigmoid", [0, 1])
 @pytest.mark.parametrize("H", [1024, 1536])

@@ -108,7 +108,9 @@ int mep_block_norm(const mep_norm_config* cfg, const void* x, const void* y, con
   a.dtype = cfg->dtype;
   a.post = cfg->post;
   a.pre = cfg->pre;
-  a.gate_kind = cfg->gate;
+  // without a block there is no gate, whatever the config names: the kernels load a
+  // row's factor wherever the kind says that there is one
+  a.gate_kind = y ? cfg->gate : MEP_BLOCK_GATE_NONE;
   a.sigmoid = cfg->gate_sigmoid != 0;
   a.eps = cfg->eps;
   a.offset = cfg->weight_offset;

@@ -555,8 +555,8 @@ typedef struct mep_norm_config {
  * of n before its rounding, the reciprocal and the product rounded to fp32 (zeros where
  * amax_b is 0; a NaN counts for no maximum and stays one; a block with an infinity in it is
  * NaN throughout).  s, n and n_codes are NULL where not wanted, not all
- * three.  x NULL: no residual; y NULL: no block part (gate then NULL too), so that the
- * call norms or only encodes rows; not both NULL.  Weights and biases are fp32 [H]; a
+ * three.  x NULL: no residual; y NULL: no block part (gate then NULL too, whatever
+ * cfg->gate is), so that the call norms or only encodes rows; not both NULL.  Weights and biases are fp32 [H]; a
  * NULL weight stands for the factor 1, a NULL bias for 0.  A row's mean square must fit
  * fp32.  s may be x or y itself and n may be y itself; other outputs overlap nothing.
  * 0 <= T <= 2^26.

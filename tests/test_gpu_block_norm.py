@@ -388,3 +388,27 @@ def test_long_batch():
     M.mep_block_norm(cfg, x[-3:].contiguous(), None, None, None, None, None, None, 3, None, small, None,
                      None)
     assert torch.equal(n[-3:], small) and bool(small.any()) and not bool(n[:-3].any())
+
+
+# a layer's config serves its first rows too, which no block stands before: the gate that
+# it names is not there then.  More rows than blocks in the last size of each width.
+@pytest.mark.parametrize("T,H", [(1, 128), (3, 640), (3200, 640), (1100, 2048), (600, 7168), (5, 8320),
+                                 (300, 16384)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("gate", ["token", "element"])
+@pytest.mark.parametrize("sigmoid", [0, 1])
+def test_config_with_a_gate_and_no_block(T, H, dtype, gate, sigmoid):
+    k = Case(T, H, dtype, "rms", "rms", "none", sigmoid, y=False, seed=H)
+    want = []
+    for outs in ((True, True, True), (False, True, False), (False, False, True)):
+        k.cfg.gate = GATE["none"]
+        k.forward(*outs)
+        want.append((k.s, k.n, k.codes, k.scales))
+    k.cfg.gate = GATE[gate]
+    for outs, w in zip(((True, True, True), (False, True, False), (False, False, True)), want):
+        k.forward(*outs)
+        for a, b in zip((k.s, k.n, k.codes, k.scales), w):
+            assert (a is None) == (b is None)
+            assert a is None or torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    check_forward(k, codes=True)
+    check_backward(k, ("x", "pre_weight", "pre_bias"))

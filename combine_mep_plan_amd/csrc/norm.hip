@@ -265,9 +265,15 @@ __device__ __forceinline__ u32x2 encode_unit(const float (&v)[kUnit], float& sca
     const float inv = scale == 0.0f ? 0.0f : 1.0f / scale;
 #pragma unroll
     for (int i = 0; i < kUnit; ++i) q[i] = v[i] * inv;
-  } else {  // 1 / scale may leave fp32
+  } else {
+    // 1 / scale may leave fp32, and a scale of few bits may lie so far below amax / 448 that
+    // quotients pass the largest code (amax = 600 * 2^-149: scale 2^-149, quotient 600).
+    // The comparison leaves a NaN as it is.
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) q[i] = v[i] / scale;
+    for (int i = 0; i < kUnit; ++i) {
+      q[i] = v[i] / scale;
+      if (fabsf(q[i]) > 448.0f) q[i] = copysignf(448.0f, q[i]);
+    }
   }
   return u32x2{pack_e4m3x4(q[0], q[1], q[2], q[3]), pack_e4m3x4(q[4], q[5], q[6], q[7])};
 }

@@ -412,3 +412,28 @@ def test_config_with_a_gate_and_no_block(T, H, dtype, gate, sigmoid):
             assert a is None or torch.equal(a.view(torch.uint8), b.view(torch.uint8))
     check_forward(k, codes=True)
     check_backward(k, ("x", "pre_weight", "pre_bias"))
+
+
+def test_codes_of_blocks_whose_scales_have_few_bits():
+    # a block's largest value by steps of fp32's smallest number, the others random below
+    # it: every finite block has finite codes, whatever amax / 448 rounds to
+    amax = np.r_[np.arange(1, 8192), 2 ** np.arange(13, 24), 3 * 2 ** np.arange(12, 22) + 1]
+    H = 128 * 64
+    amax = np.resize(amax, (len(amax) + 63) // 64 * 64)
+    rng = np.random.default_rng(6)
+    steps = np.round(rng.uniform(-1, 1, (len(amax), 128)) * amax[:, None])
+    steps[np.arange(len(amax)), rng.integers(0, 128, len(amax))] = amax * rng.choice([-1, 1], len(amax))
+    k = Case(len(amax) // 64, H, "fp32", "none", "none", y=False, weights=False)
+    k.x = torch.from_numpy((steps * 2.0 ** -149).astype(np.float32).reshape(k.T, H)).cuda()
+    k.forward(False, False, True)
+    scale = h64(k.scales)[:k.T].reshape(-1, 1) * 2.0 ** 149
+    got = h64(k.codes)[:k.T].reshape(-1, 128)
+    assert np.isfinite(got).all()
+    assert np.array_equal(scale[:, 0], np.round(amax / 448.0))  # to the nearest, even, step
+    # half a step of the code, or what the largest code does not reach: 448 times the half
+    # step that the scale may lie below amax / 448
+    off = np.abs(got * scale - steps)
+    lim = np.maximum(np.abs(steps) / 16, scale / 1024) * (1 + 2.0 ** -18)
+    past = np.abs(steps) > 448 * scale
+    assert bool((off <= np.where(past, 224.0, lim)).all())
+    assert bool((np.abs(got[past & (scale > 0)]) == 448).all()) and past.any()

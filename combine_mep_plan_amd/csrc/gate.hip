@@ -536,6 +536,16 @@ __global__ __launch_bounds__(kGateThreads) void gate_kernel(GateArgs a) {
 #pragma unroll
         for (int i = 0; i < EPL; ++i) shift = fmaxf(shift, x[i]);
         shift = group_fmax<LPT>(shift);
+        // Beside an infinite logit the finite ones are taken relative to the largest of
+        // them: as they are those above 709 would be infinite in 64 bits too.
+        if (ballot(shift == __builtin_inff())) {
+          float finite = -__builtin_inff();
+#pragma unroll
+          for (int i = 0; i < EPL; ++i)
+            finite = fmaxf(finite, x[i] < __builtin_inff() ? x[i] : -__builtin_inff());
+          finite = group_fmax<LPT>(finite);
+          if (shift == __builtin_inff()) shift = finite;
+        }
         shift = fabsf(shift) < __builtin_inff() ? shift : 0.0f;
       }
       float score[EPL];

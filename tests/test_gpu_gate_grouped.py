@@ -165,3 +165,45 @@ def test_batches():
     check(x, b, 6, "sigmoid", 8, 3, "top2", "bf16")
     cfg = M.MepGateConfig(64, 6, M.MEP_SCORE_SIGMOID, M.MEP_BF16, 1, 1.0, 0.0)
     M.mep_gate_grouped(cfg, 8, 3, M.MEP_GROUP_TOP2, None, None, 0, None, None)  # no tokens
+
+
+@pytest.mark.parametrize("by", ["max", "top2"])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("E,G", [(24, 4), (256, 8), (1024, 16), (126, 42)])
+def test_infinite_logits_beside_ones_past_exp(E, G, dtype, by):
+    # a logit of +inf puts its group first, also among finite ones whose exponentials 64
+    # bits do not hold; the groups behind it go by those
+    S, k = E // G, 3
+    rng = np.random.default_rng(E)
+    x = rng.standard_normal((40, G, S)).astype(np.float32)
+    for t in range(40):
+        at = rng.permutation(G)
+        x[t, at[0], rng.integers(S)] = np.inf
+        x[t, at[1], :2] = (760.0, 750.0) if t % 4 else (3e38, 2e38)
+        x[t, at[2], :2] = (768.0, 90.0) if t % 4 else (2.5e38, 2.25e38)
+        if t % 5 == 1:
+            x[t, at[1], 1] = np.inf
+        if t % 5 == 2:
+            x[t, at[1], 0] = np.nan
+        if t % 5 == 3:
+            x[t, at[0]][x[t, at[0]] < np.inf] = -np.inf
+        if t == 39:
+            x[t][x[t] < np.inf] = -np.inf    # nothing finite is left
+    x = x.reshape(40, E)
+    for top in (1, 2, 3):
+        if top * S < k:
+            continue
+        idx, _, x64 = run(x, None, k, "softmax", 1, 1.0, G, top, by, dtype)
+        of = np.where(np.isnan(x64), -np.inf, x64)
+        if by == "top2":  # a softmax is the same of logits that are all less by one number
+            largest = np.where(np.isfinite(x64), x64, -np.inf).max(axis=1, keepdims=True)
+            of = np.exp(of - np.where(np.isfinite(largest), largest, 0.0))
+        inside = -np.sort(-of.reshape(40, G, S), axis=2)
+        best = inside[:, :, 0]
+        if by == "top2":
+            best = np.where(best == np.inf, best, best + inside[:, :, 1])
+        chosen = R.top(best, top)
+        for t in range(40):
+            at = np.concatenate([np.arange(g * S, g * S + S) for g in sorted(chosen[t])])
+            assert np.array_equal(idx[t], at[R.top(x64[t, at][None], k)[0]]), (top, t, idx[t])
+            assert x64[t, idx[t, 0]] == np.inf

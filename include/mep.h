@@ -558,8 +558,9 @@ typedef struct mep_norm_config {
  * being infinite.)  s, n and n_codes are NULL where not wanted, not all
  * three.  x NULL: no residual; y NULL: no block part (gate then NULL too, whatever
  * cfg->gate is), so that the call norms or only encodes rows; not both NULL.  Weights and biases are fp32 [H]; a
- * NULL weight stands for the factor 1, a NULL bias for 0.  A row's mean square must fit
- * fp32.  s may be x or y itself and n may be y itself; other outputs overlap nothing.
+ * NULL weight stands for the factor 1, a NULL bias for 0.  Of a row that is normed the sum
+ * of the squares must fit fp32 (of 4096 equal values: up to 2.8e17 each); past that the
+ * norm gives 0 or NaN.  s may be x or y itself and n may be y itself; other outputs overlap nothing.
  * 0 <= T <= 2^26.
  */
 int mep_block_norm(const mep_norm_config *cfg, const void *x, const void *y, const void *gate,

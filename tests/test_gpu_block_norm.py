@@ -437,3 +437,21 @@ def test_codes_of_blocks_whose_scales_have_few_bits():
     past = np.abs(steps) > 448 * scale
     assert bool((off <= np.where(past, 224.0, lim)).all())
     assert bool((np.abs(got[past & (scale > 0)]) == 448).all()) and past.any()
+
+
+@pytest.mark.parametrize("H", [256, 4096, 16384])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_rows_whose_squares_just_fit(kind, H):
+    # equal magnitudes, the row's sum of squares 0.95 of fp32's largest number (the gradients
+    # 1e-3 of it, whose products with the rows are sums as well)
+    size = np.sqrt(0.95 * float(np.finfo(np.float32).max) / H)
+    sign = np.random.default_rng(H).choice([-1.0, 1.0], (5, H))
+    sign[:, ::2] = -sign[:, 1::2]     # their mean is 0, so that a layer norm takes off nothing
+    k = Case(5, H, "fp32", "none", kind, y=False, seed=H)
+    k.x = k.put(size * sign)
+    check_forward(k, codes=True)
+    k.x = k.put(1e-3 * size * sign)
+    check_backward(k)
+    k = Case(5, H, "fp32", kind, "none", x=False, seed=H)
+    k.y = k.put(size * sign)
+    check_forward(k)

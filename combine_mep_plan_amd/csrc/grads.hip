@@ -169,7 +169,8 @@ __device__ __forceinline__ void clip_chunk(const Chunk& k, float f) {
 __global__ __launch_bounds__(kGradThreads) void grad_clip_kernel(GradTable t, const float* norm,
                                                                  float max_norm, bool in_place) {
   const float f = max_norm / (norm[0] + 1e-6f);
-  const bool keep = f >= 1.0f;  // not for NaN
+  // Not for NaN; without a limit nothing is over it, an infinite norm neither.
+  const bool keep = f >= 1.0f || (max_norm == __builtin_inff() && norm[0] == __builtin_inff());
   if (keep && in_place) return;
   const float factor = keep ? 1.0f : f;
   const uint32_t chunks = t.first[t.n];

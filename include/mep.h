@@ -620,7 +620,8 @@ int mep_grad_norm(const mep_grad *grads, int32_t n, float *norm, void *workspace
  * Clipping: out = data * min(1, max_norm / (norm[0] + 1e-6)) for each of n gradients,
  * rounded to its type; norm is mep_grad_norm's, or several ranks' put together.  Where
  * the factor is 1, tensors that are their own `out` are not touched.  A NaN norm gives
- * NaN, an infinite one 0 (NaN where the gradient is not finite).  max_norm > 0.
+ * NaN, an infinite one 0 (NaN where the gradient is not finite).  max_norm > 0; infinite: no
+ * limit, the factor is 1 for every norm but NaN.
  * Outputs overlap neither each other nor other inputs.
  */
 int mep_grad_clip(const mep_grad *grads, int32_t n, const float *norm, float max_norm,

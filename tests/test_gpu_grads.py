@@ -235,3 +235,21 @@ def test_lists_that_are_refused():
     assert e.value.code == M.MEP_ERR_ALIGN
     with pytest.raises(ValueError, match="norm"):
         M.mep_grad_norm(lst, norm.double(), ws)
+
+
+@pytest.mark.parametrize("worst", [1.0, math.inf, -math.inf, math.nan])
+def test_no_limit(worst):
+    # an infinite limit: gradients stay as they are, infinite ones too, unless the norm is NaN
+    grads = make([100, 40000, 7], dtypes=(torch.float32, torch.bfloat16))
+    grads[1][123] = worst
+    norm, _ = norm_of(M.MepGrads(grads))
+    outs = [torch.zeros_like(t) for t in grads]
+    M.mep_grad_clip(M.MepGrads(grads, outs), norm, math.inf)
+    own = [t.clone() for t in grads]
+    M.mep_grad_clip(M.MepGrads(own), norm, math.inf)
+    torch.cuda.synchronize()
+    for g, o, i in zip(grads, outs, own):
+        if math.isnan(worst):
+            assert bool(torch.isnan(o).all()) and bool(torch.isnan(i).all())
+        else:
+            assert torch.equal(o, g) and torch.equal(i, g)

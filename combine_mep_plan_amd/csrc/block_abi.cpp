@@ -157,7 +157,7 @@ int mep_block_norm_backward(const mep_norm_config* cfg, const void* grad_s, cons
   a.gate = gate;
   a.post_weight = post_weight;
   a.post_bias = post_bias;
-  a.pre_weight = pre_weight;
+  a.pre_weight = grad_n ? pre_weight : nullptr;  // else it would meet gradients of 0
   a.grad_x = grad_x;
   a.grad_y = grad_y;
   a.grad_gate = grad_gate;

@@ -455,3 +455,19 @@ def test_rows_whose_squares_just_fit(kind, H):
     k = Case(5, H, "fp32", kind, "none", x=False, seed=H)
     k.y = k.put(size * sign)
     check_forward(k)
+
+
+@pytest.mark.parametrize("H", [72, 520, 2056, 4104, 8200])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("kind,biases", [("rms", False), ("layer", False), ("layer", True)])
+def test_gradients_of_the_stream_alone_pass_by_the_next_norm(H, dtype, kind, biases):
+    # without grad_n the next norm hands nothing back, whatever its weights are
+    k = Case(9, H, dtype, kind, kind, "token", 1, biases=biases, seed=H)
+    k.gn = None
+    want = ("x", "y", "gate", "post_weight")
+    whole, _, _ = check_backward(k, want)
+    k.wn[3], k.wn[4] = float("inf"), float("nan")
+    got = k.backward(k.x, want)
+    assert all(torch.equal(got[n], whole[n]) for n in want)
+    got = k.backward(k.x, ("x",))
+    assert torch.equal(got["x"], whole["x"])

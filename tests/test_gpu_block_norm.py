@@ -471,3 +471,28 @@ def test_gradients_of_the_stream_alone_pass_by_the_next_norm(H, dtype, kind, bia
     assert all(torch.equal(got[n], whole[n]) for n in want)
     got = k.backward(k.x, ("x",))
     assert torch.equal(got["x"], whole["x"])
+
+
+# codes and scales of rows that a block takes after its first, in each way of holding a row
+# and each kind of kernel
+@pytest.mark.parametrize("T,H", [(3200, 128), (3200, 640), (1100, 1152), (1100, 2048), (600, 7168),
+                                 (300, 8320)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("kind,gate,biases", [("rms", "token", False), ("layer", "token", False),
+                                              ("layer", "element", True)])
+def test_codes_of_many_rows(T, H, dtype, kind, gate, biases):
+    k = Case(T, H, dtype, kind, kind, gate, 1, biases=biases, seed=H)
+    check_forward(k, codes=True)
+    # a row's codes do not depend on which block took it, nor on the rows around it
+    codes, scales = k.codes[:T].view(torch.uint8).clone(), k.scales[:T].clone()
+    at = torch.randperm(T, generator=torch.Generator().manual_seed(T)).cuda()
+    k.x, k.y, k.gate = k.x[at].contiguous(), k.y[at].contiguous(), k.gate[at].contiguous()
+    k.forward(False, False, True)
+    assert torch.equal(k.codes[:T].view(torch.uint8), codes[at]) and torch.equal(k.scales[:T], scales[at])
+
+
+@pytest.mark.parametrize("T,H", [(1, 128), (9, 256), (5, 1536), (3, 7168), (2, 16384)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("gate,biases", [("element", False), ("none", True), ("element", True)])
+def test_codes_with_biases_or_a_gate_for_every_element(T, H, dtype, gate, biases):
+    check_forward(Case(T, H, dtype, "rms", "rms", gate, 1, biases=biases, offset=1.0, seed=H), codes=True)

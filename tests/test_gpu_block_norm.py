@@ -496,3 +496,25 @@ def test_codes_of_many_rows(T, H, dtype, kind, gate, biases):
 @pytest.mark.parametrize("gate,biases", [("element", False), ("none", True), ("element", True)])
 def test_codes_with_biases_or_a_gate_for_every_element(T, H, dtype, gate, biases):
     check_forward(Case(T, H, dtype, "rms", "rms", gate, 1, biases=biases, offset=1.0, seed=H), codes=True)
+
+
+@pytest.mark.parametrize("T,H", [(3200, 72), (4096, 512), (3200, 1024), (1100, 1048), (1100, 2056),
+                                 (520, 4104), (600, 7168), (270, 8200)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("kind,gate,biases", [("rms", "token", False), ("layer", "token", False),
+                                              ("layer", "element", True)])
+def test_column_sums_within_their_depth(T, H, dtype, kind, gate, biases):
+    # A thread adds up one row in `blocks` (of 4 rows each up to 1024 columns), the waves of
+    # such a block are joined by 3 additions, and the rest is added in fp64 and rounded once:
+    # so many roundings of the magnitudes added are allowed, not one for every row.
+    k = Case(T, H, dtype, kind, kind, gate, 1, biases=biases, seed=H)
+    blocks = min(256, M.mep_block_norm_workspace_bytes(k.cfg, T) // (16 * H))
+    depth = -(-T // (blocks * (4 if H <= 1024 else 1)))
+    assert depth <= 16
+    want = ("post_weight", "pre_weight") + (("post_bias", "pre_bias") if biases else ())
+    got = k.backward(k.x, want)
+    ref = B.block_norm_backward(k.ref, h64(k.gs), h64(k.gn), h64(k.x), h64(k.y), h64(k.gate), h64(k.wp),
+                                h64(k.bp), h64(k.wn), depth + 3)
+    assert set(got) == set(want)
+    for name, t in got.items():
+        close(t, ref[name][0], B.rounded(*ref[name], "fp32"), name)

@@ -407,8 +407,8 @@ int mep_gate(const mep_gate_config *cfg, const void *logits, const float *bias, 
  *   MEP_GROUP_TOP2   the sum of the two largest (the largest where that is +inf).
  * Groups are chosen in the order of these scores' 64-bit values (MEP_GROUP_MAX
  * without a bias: in the logits' order), equal ones the lower first; a NaN among the
- * scores counts as -inf there, and a logit of +inf puts its group first (the others then
- * go by their scores without it).  Within the chosen groups everything is as in mep_gate,
+ * scores counts as -inf there, and under softmax a logit of +inf puts its group first (the
+ * others then go by their scores without it).  Within the chosen groups everything is as in mep_gate,
  * and so is the gradient (mep_gate_backward).  num_groups: 1..64, divides E; top_groups: 1..num_groups; k at
  * most the chosen groups' experts; for MEP_GROUP_TOP2 two experts a group at least
  * (MEP_ERR_CONFIG otherwise).

@@ -518,3 +518,46 @@ def test_column_sums_within_their_depth(T, H, dtype, kind, gate, biases):
     assert set(got) == set(want)
     for name, t in got.items():
         close(t, ref[name][0], B.rounded(*ref[name], "fp32"), name)
+
+
+@pytest.mark.parametrize("T,H", [(3200, 640), (1100, 1152), (1100, 2056), (600, 7168), (300, 8200)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("kind,gate", [("rms", "token"), ("layer", "element")])
+def test_in_place_of_many_rows(T, H, dtype, kind, gate):
+    # the loads of a block's next rows run ahead of the stores over its present one
+    k = Case(T, H, dtype, kind, kind, gate, 1, biases=gate == "element", seed=H)
+    k.forward()
+    s, n = k.s[:T].clone(), k.n[:T].clone()
+    call = lambda x, y, s, n: M.mep_block_norm(k.cfg, x, y, k.gate, k.wp, k.bp, k.wn, k.bn, T, s, n,  # noqa: E731
+                                               None, None)
+    for s_of, n_of in (("x", "y"), ("y", None), (None, "y"), ("x", None)):
+        rows = {"x": k.x.clone(), "y": k.y.clone(), None: torch.zeros_like(k.x)}
+        out_s, out_n = rows[s_of], rows[n_of]
+        if s_of is None or n_of is None:
+            other = torch.zeros_like(k.x)
+            out_s, out_n = (other, out_n) if s_of is None else (out_s, other)
+        call(rows["x"], rows["y"], out_s, out_n)
+        assert torch.equal(out_s, s) and torch.equal(out_n, n), (s_of, n_of)
+    want = k.backward(k.x)
+    gs, y = k.gs.clone(), k.y.clone()
+    ws = torch.zeros(M.mep_block_norm_workspace_bytes(k.cfg, T), dtype=torch.uint8, device="cuda")
+    cols = [torch.zeros(H, device="cuda") for _ in range(4)]
+    cols = [c if gate == "element" or i % 2 == 0 else None for i, c in enumerate(cols)]
+    of_gate = torch.zeros_like(k.gate)
+    M.mep_block_norm_backward(k.cfg, gs, k.gn, k.x, y, k.gate, k.wp, k.bp, k.wn, T, gs, y, of_gate, *cols, ws)
+    torch.cuda.synchronize()
+    if gate == "element":
+        assert torch.equal(gs, want["x"]) and torch.equal(y, want["y"]) and torch.equal(of_gate, want["gate"])
+    apart = k.backward(k.x, ("x", "y", "gate", "post_weight", "pre_weight") +
+                       (("post_bias", "pre_bias") if gate == "element" else ()))
+    got = dict(zip(("post_weight", "post_bias", "pre_weight", "pre_bias"), cols), x=gs, y=y, gate=of_gate)
+    assert all(torch.equal(got[n], apart[n]) for n in apart)
+
+
+@pytest.mark.parametrize("eps", [1e-45, 1e-40, 1e-38])
+@pytest.mark.parametrize("H", [72, 7168])
+def test_zero_rows_and_the_smallest_eps(eps, H):
+    k = Case(4, H, "fp32", "rms", "rms", x=False, eps=eps, seed=H)
+    k.y[1], k.y[2] = 0.0, 1e-12
+    check_forward(k)
+    assert not bool(k.n[1].any()) and not bool(k.s[1].any())

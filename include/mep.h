@@ -552,8 +552,9 @@ typedef struct mep_norm_config {
  * s is the new stream; n the next block's input, for its router and, as E4M3 codes with
  * a scale per 128 columns, for a dispatch with MEP_QUANT_FP8_CARRY:
  *   n_scales[t, b] = amax_b / 448 (fp32 [T,H/128]),  n_codes = E4M3_rne(n * (1 / scale))
- * of n before its rounding, the reciprocal and the product rounded to fp32; for a scale
- * below 2^-125, n / scale held within +-448.  (Zeros where the scale is 0; a NaN counts for
+ * of n before its rounding, the reciprocal and the product rounded to fp32's bits, n held
+ * within +-448 scales (a scale of few bits may be less than amax_b / 448).  (Zeros where
+ * the scale is 0; a NaN counts for
  * no maximum and stays one; a block with an infinity in it is NaN throughout, its scale
  * being infinite.)  s, n and n_codes are NULL where not wanted, not all
  * three.  x NULL: no residual; y NULL: no block part (gate then NULL too, whatever

@@ -561,3 +561,25 @@ def test_zero_rows_and_the_smallest_eps(eps, H):
     k.y[1], k.y[2] = 0.0, 1e-12
     check_forward(k)
     assert not bool(k.n[1].any()) and not bool(k.s[1].any())
+
+
+def test_codes_on_both_sides_of_the_lifted_scales():
+    # scales from 2^-130 to 2^-122, and NaN among values that are held to 448 scales
+    H = 128 * 8
+    x = torch.randn((64, H), generator=torch.Generator().manual_seed(4), dtype=torch.float64)
+    amax = x.reshape(64, 8, 128).abs().amax(2)
+    e = 448 * 2.0 ** (-130 + 8 * torch.arange(512, dtype=torch.float64).reshape(64, 8) / 511)
+    x = (x.reshape(64, 8, 128) * (e / amax)[:, :, None]).float().reshape(64, H)
+    x[7, 130] = float("nan")
+    k = Case(64, H, "fp32", "none", "none", y=False, weights=False)
+    k.x = x.cuda()
+    k.forward(False, False, True)
+    scale, got = h64(k.scales)[:64, :, None], h64(k.codes)[:64].reshape(64, 8, 128)
+    v = x.double().numpy().reshape(64, 8, 128)
+    assert np.isnan(got[7, 1, 2]) and np.isnan(got).sum() == 1
+    got[7, 1, 2] = v[7, 1, 2] = 0.0
+    # the scale is within half a step of fp32, which is 2^-150 at least; so is the largest
+    # value beyond 448 scales at most 448 times that
+    assert bool((np.abs(scale[..., 0] - np.abs(v).max(2) / 448) <= scale[..., 0] * B.U32 + 2.0 ** -150).all())
+    lim = np.maximum(np.abs(v) / 16, scale / 1024) * (1 + 2.0 ** -18)
+    assert bool((np.abs(got * scale - v) <= lim).all())

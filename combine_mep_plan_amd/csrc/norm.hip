@@ -12,12 +12,12 @@
 // they fill; a block works on several rows and keeps the weights in registers.
 //
 // Bound by memory for many rows: 4096 x 7168 in bf16, both norms, a gate a row, rows and E4M3
-// codes out, 49.3 us (265 MB, 5.4 TB/s; a copy reaches 5.1), its gradients 70.1 (352 MB, 5.0
+// codes out, 49.2 us (265 MB, 5.4 TB/s; a copy reaches 5.1), its gradients 70.6 (352 MB, 5.0
 // TB/s).  What stood in the way was instructions as much as loads: a wave's takes 4 cycles,
 // and 30 a value would be half of that time.  So a norm that subtracts no mean, has no bias
 // and no gate for every value has kernels of its own, its factors are joined before they
-// meet the values, and the vector units are 54% (61%) busy now.  By the launch for few rows:
-// one row of 7168 values 2.9 us, 128 rows 4.1.
+// meet the values, and the vector units are 57% (61%) busy; with layer norms 73% (72%).  By
+// the launch for few rows: one row of 7168 values 2.9 us, 128 rows 4.1.
 #include <algorithm>
 #include <type_traits>
 
@@ -496,8 +496,9 @@ constexpr bool weights_in_lds(int rows, int upt, bool all, bool bf16) {
   return rows == kBlock ? all || upt > 1 : rows == kHalfBlock && all && bf16;
 }
 // Half blocks kept to 128 registers, so that 4 waves a SIMD fit whatever the block's
-// waves: all but those of fp32 rows with everything, which would spill (4096 x 2056 90 us,
-// in 128 registers 101).
+// waves: all but those of fp32 rows with everything, which would spill too much (4096 x 2056
+// 88 us, in 128 registers 115).  In bf16 that kernel spills 40 bytes a thread and
+// gains by it all the same: 60 us, without the bound 68.
 constexpr bool packed_halves(int rows, bool all, bool bf16) {
   return rows == kHalfBlock && (!all || bf16);
 }
@@ -920,9 +921,10 @@ hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) {
   const bool all = a.post_bias || a.pre_bias || a.gate_kind == MEP_BLOCK_GATE_ELEMENT;
   const bool bf16 = a.dtype == MEP_BF16;
   // Blocks that the CUs hold at once and no more, as each loads the weights.  4096 rows
-  // with 256, 512, 1024 blocks (us): 7168 bf16 columns 44.4, 43.3, 48.7, with layer norms,
-  // biases and a gate for every element 60.5, 62.1, 67.1; 2056 columns 22.0, 17.5, 15.3, in
-  // fp32 with all of it 40.0, 38.0, 45.0; 512 by wave 5.3, 4.5, 4.5 (768: 4.2).
+  // with 256, 512, 1024 blocks (us): 7168 bf16 columns 40.9, 42.8, 46.9, with codes 49.4, 49.2,
+  // 55.5, between layer norms 49.4, 44.4, 53.9, with biases and a gate for every element too
+  // 54.2, 58.2, 64.9, in fp32 113, 117, 120; 2056 columns 20.4, 16.3, 15.2, in fp32 30.4, 29.8,
+  // 30.8, with everything 41.7, 38.7, 46.2; 512 by wave 5.3, 4.7, 4.6 (768: 4.5).
   const int most = r.kind == kWaveRows ? 768
                    : r.kind == kBlock && (all || !bf16 || r.upt > 1) ? 256
                    : bf16 && r.threads <= 384 ? 1024 : 512;
@@ -936,8 +938,9 @@ hipError_t launch_block_norm(const NormArgs& a, hipStream_t s) {
 }
 
 // Blocks of the gradients' launch, each of which leaves a row of partial sums: one a CU,
-// two where they fit.  4096 rows with 256 and 512 blocks (us): 2056 bf16 columns 42 and
-// 34, all of it in fp32 90 and 95, 7168 bf16 columns 72 and 80, 512 columns by wave 19 and 24.
+// two where they fit.  4096 rows with 256 and 512 blocks (us): 2056 bf16 columns 38.2 and
+// 31.1, between layer norms 54.2 and 41.3, with everything 75.8 and 59.7, in fp32 88 and 93,
+// 7168 bf16 columns 71 and 80, 512 columns by wave 11.2 and 11.4.
 static int backward_blocks(const RowShape& r, int32_t T, bool all, bool bf16) {
   return blocks_for(r, T, packed_halves(r.kind, all, bf16) ? 512 : 256);
 }

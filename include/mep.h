@@ -408,10 +408,10 @@ int mep_gate(const mep_gate_config *cfg, const void *logits, const float *bias, 
  * Groups are chosen in the order of these scores' 64-bit values (MEP_GROUP_MAX
  * without a bias: in the logits' order), equal ones the lower first; a NaN among the
  * scores counts as -inf there, and under softmax a logit of +inf puts its group first (the
- * others then go by their scores without it).  Within the chosen groups everything is as in mep_gate,
- * and so is the gradient (mep_gate_backward).  num_groups: 1..64, divides E; top_groups: 1..num_groups; k at
- * most the chosen groups' experts; for MEP_GROUP_TOP2 two experts a group at least
- * (MEP_ERR_CONFIG otherwise).
+ * others then go by their scores without it).  Within the chosen groups everything is as
+ * in mep_gate, and so is the gradient (mep_gate_backward).  num_groups: 1..64, divides E;
+ * top_groups: 1..num_groups; k at most the chosen groups' experts; for MEP_GROUP_TOP2 two
+ * experts a group at least (MEP_ERR_CONFIG otherwise).
  */
 int mep_gate_grouped(const mep_gate_config *cfg, int32_t num_groups, int32_t top_groups,
                      int32_t group_score, const void *logits, const float *bias, int32_t T,
@@ -554,14 +554,14 @@ typedef struct mep_norm_config {
  *   n_scales[t, b] = amax_b / 448 (fp32 [T,H/128]),  n_codes = E4M3_rne(n * (1 / scale))
  * of n before its rounding, the reciprocal and the product rounded to fp32's bits, n held
  * within +-448 scales (a scale of few bits may be less than amax_b / 448).  (Zeros where
- * the scale is 0; a NaN counts for
- * no maximum and stays one; a block with an infinity in it is NaN throughout, its scale
- * being infinite.)  s, n and n_codes are NULL where not wanted, not all
- * three.  x NULL: no residual; y NULL: no block part (gate then NULL too, whatever
- * cfg->gate is), so that the call norms or only encodes rows; not both NULL.  Weights and biases are fp32 [H]; a
- * NULL weight stands for the factor 1, a NULL bias for 0.  Of a row that is normed the sum
- * of the squares must fit fp32 (of 4096 equal values: up to 2.8e17 each); past that the
- * norm gives 0 or NaN.  s may be x or y itself and n may be y itself; other outputs overlap nothing.
+ * the scale is 0; a NaN counts for no maximum and stays one; a block with an infinity in it
+ * is NaN throughout, its scale being infinite.)  s, n and n_codes are NULL where not wanted,
+ * not all three.  x NULL: no residual; y NULL: no block part (gate then NULL too, whatever
+ * cfg->gate is), so that the call norms or only encodes rows; not both NULL.  Weights and
+ * biases are fp32 [H]; a NULL weight stands for the factor 1, a NULL bias for 0.  Of a row
+ * that is normed the sum of the squares must fit fp32 (of 4096 equal values: up to 2.8e17
+ * each); past that the norm gives 0 or NaN.  s may be x or y itself and n may be y itself
+ * (not both y); other outputs overlap nothing.
  * 0 <= T <= 2^26.
  */
 int mep_block_norm(const mep_norm_config *cfg, const void *x, const void *y, const void *gate,
